@@ -61,12 +61,14 @@ enum zero_status {
     ZERO_OK = 0,
     ZERO_EINVAL = -1,  /* bad argument: null pointer, negative size, unknown dtype ... */
     ZERO_ERANGE = -2,  /* a size or offset overflows int64                              */
-    ZERO_EDEVICE = -3  /* a HIP launch failed                                           */
+    ZERO_EDEVICE = -3, /* a HIP launch failed                                           */
+    ZERO_ENOMEM = -4   /* host memory ran out (zero_tensor_plan_init only)              */
 };
 
 enum zero_dtype {
     ZERO_FP16 = 1,     /* IEEE 754 binary16 */
-    ZERO_BF16 = 2      /* bfloat16          */
+    ZERO_BF16 = 2,     /* bfloat16          */
+    ZERO_FP32 = 3      /* IEEE 754 binary32; in the zero_tensor_* calls' tables only */
 };
 
 #define ZERO_MAX_RANKS 16
@@ -442,6 +444,130 @@ int zero_adamw_step_ranges(float* master, float* exp_avg, float* exp_avg_sq, voi
                            int32_t dtype, const zero_adamw_hparams* hp,
                            const zero_step_control* ctl, const zero_step_result* res,
                            hipStream_t stream);
+
+/* ------------------------------------------------------- tensor tables ---- */
+/* Operators over a table of gradient tensors as backward leaves them, before
+ * (or instead of) a copy into a flat buffer: their norm and clipping by it
+ * (wmrh.cn ZeRO article, section 3.3 gradient_clipping; the pages give no
+ * formula, this is the one zero_adamw_step applies), and the accumulation of a
+ * micro-batch's gradients, each tensor of any size, type and alignment.
+ *
+ * An entry is a tensor x of `numel` elements and where the calls that write put
+ * its output y: elsewhere, in another type perhaps, or x itself (the same
+ * pointer and type).  An entry with numel 0 is allowed; its pointers are not
+ * read. */
+typedef struct zero_tensor_entry {
+    const void* src;     /* device, x: aligned to its element size  */
+    void* dst;           /* device, y: likewise; src for in place   */
+    int64_t numel;       /* elements, >= 0                          */
+    int32_t src_dtype;   /* zero_dtype: FP16, BF16 or FP32          */
+    int32_t dst_dtype;
+} zero_tensor_entry;
+
+/* What zero_tensor_plan_init finds out about a list of entries (host); passed,
+ * unchanged, to every call with the device table that belongs to it. */
+typedef struct zero_tensor_plan {
+    int64_t n_tensors;   /* entries                                           */
+    int64_t numel;       /* elements of all                                   */
+    int64_t n_chunks;    /* pieces that the kernels work on                   */
+    int64_t chunk;       /* elements of a whole piece                         */
+    int64_t table_bytes; /* size of the device table                          */
+    int32_t writable;    /* 1: no output overlaps another output, nor an input
+                            that is not its own in place; 0: the calls that
+                            write refuse this plan (ZERO_EINVAL)              */
+    int32_t reserved;
+} zero_tensor_plan;
+
+enum zero_norm_kind {
+    ZERO_NORM_L2 = 1,    /* sqrt(sum of x^2) */
+    ZERO_NORM_MAX = 2    /* max of |x|       */
+};
+
+/* Sizes of the plan for entries[0, n_tensors) (host array; n_tensors 0 is
+ * allowed).  The same tensor may be listed twice: its norm then counts twice,
+ * and the plan is not writable.
+ * Errors: ZERO_EINVAL for a NULL argument, a negative count, an unknown type, a
+ * NULL or misaligned pointer with a nonzero numel; ZERO_ERANGE for addresses or
+ * sizes that overflow, or more pieces than one launch holds (16,777,215);
+ * ZERO_ENOMEM. */
+int zero_tensor_plan_init(const zero_tensor_entry* entries, int64_t n_tensors,
+                          zero_tensor_plan* plan);
+
+/* Writes the plan's table, plan->table_bytes bytes, 8-byte aligned, to host
+ * memory; the caller copies it to device memory (16-byte aligned) and passes
+ * that to the calls, for as long as the tensors stay where they are.
+ * Errors: as zero_tensor_plan_init, and ZERO_EINVAL if the plan is not that of
+ * these entries. */
+int zero_tensor_plan_table(const zero_tensor_entry* entries, const zero_tensor_plan* plan,
+                           void* table);
+
+/* Bytes of device workspace for the calls that take a norm: one 8-byte partial
+ * per piece, plus one per 2048 of them where there are over 16384. */
+size_t zero_tensor_workspace_bytes(const zero_tensor_plan* plan);
+
+/* Norm of the whole table, overflow flag and each tensor's own norm, unscaled
+ * by inv = inv_scale (or ctl->inv_scale where ctl is not NULL):
+ *   overflow = some element is +-inf or NaN;
+ *   kind L2:  sumsq = inv^2 * sum x^2,     norms[k] = inv * sqrt(sum of tensor k's x^2)
+ *   kind MAX: sumsq = (inv * max |x|)^2,   norms[k] = inv * max of tensor k's |x|
+ * in fp64 (each x^2 is exact), norms[k] rounded once to fp32 (a norm beyond
+ * fp32's range to inf).  No element gives 0.  Either way res is the square of
+ * the norm, so zero_adamw_step and zero_tensor_clip clip by that norm.  With
+ * accumulate != 0, *res is joined with what it held (L2: the sum; MAX: the
+ * larger; the flags ORed), so several tables checked in turn on one stream give
+ * one result.  The order of every sum is fixed by the plan.  With the flag set,
+ * sumsq and the norms of the tensors concerned are inf or NaN.
+ *   table      device, the plan's table
+ *   ctl        device zero_step_control, or NULL
+ *   res        device, out (in/out when accumulating)
+ *   norms      device, out, fp32[n_tensors], or NULL
+ *   workspace  device scratch of zero_tensor_workspace_bytes(plan), 8-byte
+ *              aligned; needs no initialisation, not shared by calls that may
+ *              overlap
+ * Errors: ZERO_EINVAL for NULL pointers, an unknown kind, an inv_scale (without
+ * ctl) not finite and > 0, a small or misaligned workspace. */
+int zero_tensor_norm(const zero_tensor_plan* plan, const void* table, int32_t kind,
+                     float inv_scale, const zero_step_control* ctl, zero_step_result* res,
+                     float* norms, void* workspace, size_t workspace_bytes, int32_t accumulate,
+                     hipStream_t stream);
+
+/* Unscale and clip: y = round(x * f) with f = fp32(res->inv_scale * coef),
+ *   coef = max_norm / (norm + 1e-6) if max_norm > 0 and that is below 1, else 1
+ * (fp64), where norm is sqrt(res->sumsq) or, with norms != NULL, tensor k's
+ * norms[k].  The product is fp32, then rounded once (nearest, ties to even)
+ * to y's type.  With res->overflow set nothing is written.
+ *   res    device, in: written by zero_tensor_norm or any check of this library
+ *   norms  device, in, fp32[n_tensors], or NULL
+ * Errors: ZERO_EINVAL for NULL pointers, a plan that is not writable, a NaN
+ * max_norm. */
+int zero_tensor_clip(const zero_tensor_plan* plan, const void* table, float max_norm,
+                     const zero_step_result* res, const float* norms, hipStream_t stream);
+
+/* zero_tensor_norm, then zero_tensor_clip by its result (per_tensor != 0: by
+ * each tensor's own norm; norms is then required).  Same results as the two
+ * calls, with less launched or read where that is possible.  Arguments and
+ * errors as theirs. */
+int zero_tensor_clip_norm(const zero_tensor_plan* plan, const void* table, int32_t kind,
+                          float max_norm, float inv_scale, const zero_step_control* ctl,
+                          zero_step_result* res, float* norms, int32_t per_tensor, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream);
+
+/* Accumulation of a micro-batch: y = round(y + weight * x), one fused
+ * multiply-add in fp32, or with overwrite != 0 (the first micro-batch; y is not
+ * read) y = round(weight * x); rounded to y's type once.
+ * Errors: ZERO_EINVAL for NULL pointers, a plan that is not writable, a weight
+ * that is not finite. */
+int zero_tensor_accumulate(const zero_tensor_plan* plan, const void* table, float weight,
+                           int32_t overwrite, hipStream_t stream);
+
+/* zero_tensor_accumulate and, in the same pass, zero_tensor_norm of the y that
+ * it stores (the last micro-batch of a step).  Arguments and errors as
+ * theirs. */
+int zero_tensor_accumulate_norm(const zero_tensor_plan* plan, const void* table, float weight,
+                                int32_t overwrite, int32_t kind, float inv_scale,
+                                const zero_step_control* ctl, zero_step_result* res, float* norms,
+                                void* workspace, size_t workspace_bytes, int32_t accumulate,
+                                hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,209 @@
+"""Tensor-table plans on the CPU: sizes, the device table's contents, which
+plans may be written to, and the refusals of every zero_tensor_* call (no device
+pointer is ever read: a refused call launches nothing)."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import zero_partitioned_mixed_shard_amd as Z
+from zero_partitioned_mixed_shard_amd import tensors as T
+
+FP16, BF16, FP32 = Z.ZERO_FP16, Z.ZERO_BF16, Z.ZERO_FP32
+SIZE = {FP16: 2, BF16: 2, FP32: 4}
+CHUNK_T = np.dtype([("src", np.uint64), ("dst", np.uint64), ("count", np.int32),
+                    ("tensor", np.int32), ("src_dtype", np.int32), ("dst_dtype", np.int32)])
+
+
+def entries(rows):
+    """rows: (src, dst, numel, src_dtype, dst_dtype)."""
+    e = np.zeros(max(1, len(rows)), dtype=T._ENTRY)
+    if rows:
+        e[:len(rows)] = rows
+    return e
+
+
+def init(rows, n=None):
+    plan = T.zero_tensor_plan_t()
+    rc = Z.lib().zero_tensor_plan_init(entries(rows).ctypes.data, len(rows) if n is None else n,
+                                       ctypes.byref(plan))
+    return rc, plan
+
+
+def table(rows, plan):
+    buf = np.full(plan.table_bytes // 8 + 2, -7, dtype=np.int64)
+    rc = Z.lib().zero_tensor_plan_table(entries(rows).ctypes.data, ctypes.byref(plan),
+                                        buf.ctypes.data)
+    assert (buf[plan.table_bytes // 8:] == -7).all()
+    return rc, buf
+
+
+def test_entry_and_plan_sizes():
+    assert T._ENTRY.itemsize == 32 and ctypes.sizeof(T.zero_tensor_plan_t) == 48
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_table_covers_every_element_once(seed):
+    rng = np.random.default_rng(seed)
+    rows, at = [], 1 << 20
+    for _ in range(int(rng.integers(0, 12))):
+        n = int(rng.choice([0, 1, 7, 100, 16383, 16384, 16385, 70000, 1000003]))
+        s, d = (int(x) for x in rng.choice([FP16, BF16, FP32], 2))
+        dst = at + n * SIZE[s] + (-(at + n * SIZE[s])) % 4
+        rows.append((at, dst, n, s, d))
+        at = dst + n * SIZE[d] + 64
+        at += -at % 4
+    rc, plan = init(rows)
+    assert rc == Z.ZERO_OK and plan.writable == 1
+    assert plan.n_tensors == len(rows) and plan.numel == sum(r[2] for r in rows)
+    rc, buf = table(rows, plan)
+    assert rc == Z.ZERO_OK
+    chunks = buf[:plan.n_chunks * 4].view(CHUNK_T)
+    first = buf[plan.n_chunks * 4:plan.table_bytes // 8]
+    assert len(first) == len(rows) + 1 and first[0] == 0 and first[-1] == plan.n_chunks
+    for k, (src, dst, n, s, d) in enumerate(rows):
+        mine = chunks[first[k]:first[k + 1]]
+        done = 0
+        for c in mine:
+            assert (c["tensor"], c["src_dtype"], c["dst_dtype"]) == (k, s, d)
+            assert c["src"] == src + done * SIZE[s] and c["dst"] == dst + done * SIZE[d]
+            assert 0 < c["count"] <= plan.chunk
+            done += int(c["count"])
+        assert done == n
+        # every chunk but a tensor's last is whole, so aligned tensors stay aligned
+        assert (mine["count"][:-1] == plan.chunk).all() and plan.chunk % 8 == 0
+
+
+def test_large_tensors_have_64_bit_addresses():
+    n = (1 << 36) + 5
+    rows = [(1 << 40, 1 << 42, n, BF16, FP32)]
+    rc, plan = init(rows)
+    assert rc == Z.ZERO_OK and plan.numel == n
+    rc, buf = table(rows, plan)
+    last = buf[:plan.n_chunks * 4].view(CHUNK_T)[-1]
+    start = (plan.n_chunks - 1) * plan.chunk
+    assert last["src"] == (1 << 40) + 2 * start and last["dst"] == (1 << 42) + 4 * start
+    assert last["count"] == n - start
+
+
+@pytest.mark.parametrize("rows,writable", [
+    ([(4096, 4096, 10, FP16, FP16)], 1),                                   # in place
+    ([(4096, 4096, 10, FP16, BF16)], 0),                                   # in place, other type
+    ([(4096, 4098, 10, FP16, FP16)], 0),                                   # shifted onto itself
+    ([(4096, 4116, 10, FP16, FP16)], 1),                                   # right after itself
+    ([(4096, 4096, 10, FP32, FP16)], 0),                                   # narrowed onto itself
+    ([(4096, 8192, 10, FP16, FP32), (8192 + 36, 4096 * 4, 5, FP16, FP16)], 0),  # out over next input
+    ([(4096, 8192, 10, FP16, FP32), (8192 + 40, 4096 * 4, 5, FP16, FP16)], 1),
+    ([(4096, 8192, 10, FP16, FP16), (6000, 8210, 5, FP16, FP16)], 0),      # outputs overlap
+    ([(4096, 4096, 10, FP16, FP16), (4096, 4096, 10, FP16, FP16)], 0),     # the same tensor twice
+    ([(4096, 8192, 10, FP16, FP16), (4096, 9000, 10, FP16, FP16)], 1),     # one input, two outputs
+    ([(4096, 4096, 0, FP16, FP16), (4096, 4096, 3, FP16, FP16)], 1),       # an empty one beside it
+    ([], 1),
+])
+def test_writable(rows, writable):
+    rc, plan = init(rows)
+    assert rc == Z.ZERO_OK and plan.writable == writable
+
+
+def test_init_refusals():
+    ok = (4096, 8192, 10, FP16, FP32)
+    bad = {"negative count": (4096, 8192, -1, FP16, FP32), "null src": (0, 8192, 10, FP16, FP32),
+           "null dst": (4096, 0, 10, FP16, FP32), "type 0": (4096, 8192, 10, 0, FP32),
+           "type 4": (4096, 8192, 10, FP16, 4), "odd fp16": (4097, 8192, 10, FP16, FP32),
+           "fp32 at 2": (4096, 8194, 10, FP16, FP32)}
+    for what, row in bad.items():
+        assert init([ok, row])[0] == Z.ZERO_EINVAL, what
+    for row in ((4096, 8192, 1 << 62, FP16, FP32), (2 ** 64 - 8, 8192, 10, FP16, FP32)):
+        assert init([row])[0] == Z.ZERO_ERANGE
+    # a whole int64 of elements in two tensors; and more pieces than a launch has blocks
+    assert init([(4096, 4096, (1 << 62) - 1, FP16, FP16)] * 3)[0] == Z.ZERO_ERANGE
+    assert init([(4096, 4096, 1 << 50, FP16, FP16)])[0] == Z.ZERO_ERANGE
+    # pointers and types of nothing: only the types are looked at
+    assert init([(0, 0, 0, FP16, FP32)])[0] == Z.ZERO_OK
+    L, plan = Z.lib(), T.zero_tensor_plan_t()
+    assert L.zero_tensor_plan_init(None, 1, ctypes.byref(plan)) == Z.ZERO_EINVAL
+    assert L.zero_tensor_plan_init(entries([ok]).ctypes.data, -1, ctypes.byref(plan)) == Z.ZERO_EINVAL
+    assert L.zero_tensor_plan_init(entries([ok]).ctypes.data, 1, None) == Z.ZERO_EINVAL
+    assert L.zero_tensor_plan_init(None, 0, ctypes.byref(plan)) == Z.ZERO_OK
+    rc, plan = init([ok])
+    buf = np.zeros(plan.table_bytes, np.uint8)
+    e = entries([ok])
+    assert L.zero_tensor_plan_table(e.ctypes.data, None, buf.ctypes.data) == Z.ZERO_EINVAL
+    assert L.zero_tensor_plan_table(e.ctypes.data, ctypes.byref(plan), None) == Z.ZERO_EINVAL
+    assert L.zero_tensor_plan_table(None, ctypes.byref(plan), buf.ctypes.data) == Z.ZERO_EINVAL
+    other = entries([(4096, 8192, 100_000, FP16, FP32)])   # another plan's entries
+    assert L.zero_tensor_plan_table(other.ctypes.data, ctypes.byref(plan),
+                                    buf.ctypes.data) == Z.ZERO_EINVAL
+
+
+def test_workspace_bytes():
+    assert Z.lib().zero_tensor_workspace_bytes(None) == 0
+    for rows in ([], [(4096, 4096, 1, FP16, FP16)], [(4096, 4096, 1 << 33, FP16, FP16)]):
+        rc, plan = init(rows)
+        ws = Z.lib().zero_tensor_workspace_bytes(ctypes.byref(plan))
+        assert max(16, 8 * plan.n_chunks) <= ws <= 8 * (plan.n_chunks + plan.n_chunks // 2048 + 2)
+
+
+def test_call_refusals():
+    """Bad arguments of the device calls; the pointers are never read."""
+    L = Z.lib()
+    fake = 1 << 12
+    nan, inf = float("nan"), float("inf")
+    _, good = init([(4096, 8192, 100, FP16, FP32)])
+    _, closed = init([(4096, 8192, 10, FP16, FP32)] * 2)
+    assert closed.writable == 0
+    g, c = ctypes.byref(good), ctypes.byref(closed)
+    ws = L.zero_tensor_workspace_bytes(g)
+    L2 = Z.ZERO_NORM_L2
+
+    def norm(plan=g, table=fake, kind=L2, inv=1.0, ctl=None, res=fake, w=fake, wb=ws):
+        return L.zero_tensor_norm(plan, table, kind, inv, ctl, res, None, w, wb, 0, None)
+
+    def fused(plan=g, table=fake, kind=L2, clip=1.0, inv=1.0, res=fake, norms=None, each=0, w=fake,
+              wb=ws):
+        return L.zero_tensor_clip_norm(plan, table, kind, clip, inv, None, res, norms, each, w, wb,
+                                       None)
+
+    def add(plan=g, table=fake, weight=1.0, kind=L2, inv=1.0, res=fake, w=fake, wb=ws):
+        return L.zero_tensor_accumulate_norm(plan, table, weight, 0, kind, inv, None, res, None, w,
+                                             wb, 0, None)
+
+    shared = [dict(plan=None), dict(table=None), dict(table=fake + 8), dict(kind=0), dict(kind=3),
+              dict(inv=0.0), dict(inv=-1.0), dict(inv=nan), dict(inv=inf), dict(res=None),
+              dict(w=None), dict(w=fake + 4), dict(wb=ws - 1)]
+    for call in (norm, fused, add):
+        for bad in shared:
+            assert call(**bad) == Z.ZERO_EINVAL, (call.__name__, bad)
+    for bad in (dict(plan=c), dict(clip=nan), dict(each=1)):
+        assert fused(**bad) == Z.ZERO_EINVAL, bad
+    for bad in (dict(plan=c), dict(weight=nan), dict(weight=inf)):
+        assert add(**bad) == Z.ZERO_EINVAL, bad
+    for args in ((None, fake, 1.0, fake, None), (g, None, 1.0, fake, None), (c, fake, 1.0, fake, None),
+                 (g, fake, nan, fake, None), (g, fake, 1.0, None, None)):
+        assert L.zero_tensor_clip(*args, None) == Z.ZERO_EINVAL, args
+    for args in ((None, fake, 1.0), (g, None, 1.0), (c, fake, 1.0), (g, fake, nan), (g, fake, -inf)):
+        assert L.zero_tensor_accumulate(*args, 0, None) == Z.ZERO_EINVAL, args
+
+
+def test_binding_refuses_host_tensors():
+    import torch
+    for t in (torch.zeros(4), torch.zeros(4, dtype=torch.float64)):
+        with pytest.raises(ValueError, match="device"):
+            Z.zero_tensor_plan([t])
+
+
+def test_dense_orders():
+    import torch
+    x = torch.zeros(4, 6, 5)
+    assert T._order(x) is None and T._order(x[:, :1].contiguous()) is None
+    assert T._order(x.permute(2, 0, 1)) == (1, 30, 5)
+    assert T._order(torch.zeros(0, 3)) is None and T._order(torch.zeros(())) is None
+    assert T._order(x.transpose(0, 1)[:, :, None]) == (5, 30, 1)
+    for bad in (x[:, ::2], x[:, :, 1:], x[:1].expand(4, 6, 5), x.transpose(0, 2)[1:]):
+        with pytest.raises(ValueError, match="dense"):
+            T._order(bad)
+
+
+def test_unknown_norm_kind():
+    with pytest.raises(ValueError, match="kind"):
+        T._kind("l1")

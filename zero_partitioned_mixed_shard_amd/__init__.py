@@ -1,8 +1,8 @@
 """Python binding of the ZeRO-1/2 owner-shard step library (libzero_shard.so).
 
 Argument marshalling only: every phase runs in the HIP kernels of
-``csrc/zero_shard.hip`` and ``csrc/zero_flat.hip`` behind the C ABI of
-``include/zero_shard.h``.  The functions keep the C names.  Device buffers are
+``csrc/zero_shard.hip``, ``csrc/zero_flat.hip`` and ``csrc/zero_tensors.hip``
+behind the C ABI of ``include/zero_shard.h``.  The functions keep the C names.  Device buffers are
 torch tensors (device memory and streams are all torch is used for); 16-bit
 data is passed as torch.float16 / torch.bfloat16 tensors, fp32 state as
 torch.float32.  There is no fallback: if the library is missing, importing
@@ -19,8 +19,9 @@ import numpy as np
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libzero_shard.so")
 
-ZERO_OK, ZERO_EINVAL, ZERO_ERANGE, ZERO_EDEVICE = 0, -1, -2, -3
-ZERO_FP16, ZERO_BF16 = 1, 2
+ZERO_OK, ZERO_EINVAL, ZERO_ERANGE, ZERO_EDEVICE, ZERO_ENOMEM = 0, -1, -2, -3, -4
+ZERO_FP16, ZERO_BF16, ZERO_FP32 = 1, 2, 3
+ZERO_NORM_L2, ZERO_NORM_MAX = 1, 2
 ZERO_MAX_RANKS = 16
 
 
@@ -66,6 +67,9 @@ EXPORTS = (
     "zero_adamw_step_ctl", "zero_step_control_update",
     "zero_range_workspace_bytes", "zero_reduce_check_ranges", "zero_adamw_step_ranges",
     "zero_reduce_check_buckets", "zero_reduce_check_owned_noalloc",
+    "zero_tensor_plan_init", "zero_tensor_plan_table", "zero_tensor_workspace_bytes",
+    "zero_tensor_norm", "zero_tensor_clip", "zero_tensor_clip_norm", "zero_tensor_accumulate",
+    "zero_tensor_accumulate_norm",
 )
 
 
@@ -123,6 +127,16 @@ def _load():
         "zero_reduce_check_buckets": ([P, P, i32, P, i32, i32, f32, P, P, P, ctypes.c_size_t, i32,
                                        P], ctypes.c_int),
         "zero_reduce_check_owned_noalloc": ([P, P, i32, i64, i32, f32, P, i32, P], ctypes.c_int),
+        "zero_tensor_plan_init": ([P, i64, P], ctypes.c_int),
+        "zero_tensor_plan_table": ([P, P, P], ctypes.c_int),
+        "zero_tensor_workspace_bytes": ([P], ctypes.c_size_t),
+        "zero_tensor_norm": ([P, P, i32, f32, P, P, P, P, ctypes.c_size_t, i32, P], ctypes.c_int),
+        "zero_tensor_clip": ([P, P, f32, P, P, P], ctypes.c_int),
+        "zero_tensor_clip_norm": ([P, P, i32, f32, f32, P, P, P, i32, P, ctypes.c_size_t, P],
+                                  ctypes.c_int),
+        "zero_tensor_accumulate": ([P, P, f32, i32, P], ctypes.c_int),
+        "zero_tensor_accumulate_norm": ([P, P, f32, i32, i32, f32, P, P, P, P, ctypes.c_size_t,
+                                         i32, P], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -525,3 +539,9 @@ def zero_reduce_check_owned_noalloc(dst, srcs: Sequence, inv_scale: float, res,
                                                 dt, float(inv_scale), res.data_ptr(),
                                                 int(bool(accumulate)), _stream(stream)),
            "zero_reduce_check_owned_noalloc")
+
+
+# ---------------------------------------------------------- tensor tables ---
+from .tensors import (zero_tensor_accumulate, zero_tensor_accumulate_norm,  # noqa: E402,F401
+                      zero_tensor_clip, zero_tensor_clip_norm, zero_tensor_norm, zero_tensor_plan,
+                      zero_tensor_workspace_bytes)

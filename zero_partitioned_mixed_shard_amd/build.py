@@ -6,9 +6,10 @@ import subprocess
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-# owner-step kernels + C ABI, and the flat copy kernels; zero_common.h is
-# included by both
-SRCS = [os.path.join(PKG, "csrc", f) for f in ("zero_shard.hip", "zero_flat.hip")]
+# owner-step kernels + C ABI, the flat copy kernels and the operators over
+# tensor tables; zero_common.h is included by all
+SRCS = [os.path.join(PKG, "csrc", f)
+        for f in ("zero_shard.hip", "zero_flat.hip", "zero_tensors.hip")]
 LIB = os.path.join(PKG, "libzero_shard.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

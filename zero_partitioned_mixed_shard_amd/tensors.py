@@ -1,0 +1,231 @@
+"""Operators over tables of gradient tensors (the zero_tensor_* calls of
+``include/zero_shard.h``): a plan built once over a list of tensors, then their
+norm, clipping and accumulation.
+
+    acc = zero_tensor_plan(grads, out=accumulators)     # 16-bit -> fp32
+    zero_tensor_accumulate(acc, overwrite=True)         # first micro-batch
+    ...
+    zero_tensor_accumulate(acc, res=res, workspace=ws)  # last one, with the norm
+    bucket = zero_tensor_plan(accumulators, out=pieces_of_a_flat_buffer)
+    zero_tensor_clip(bucket, 1.0, res)                  # clipped, unscaled, 16-bit
+
+Calls are asynchronous on the current stream of the plan's device (or
+``stream``), allocate nothing and can be captured in a graph (build the plan
+before the capture and keep it, and the tensors' memory, for as long as the
+graph is replayed).  A plan holds addresses: where gradients are allocated anew
+(``zero_grad(set_to_none=True)``), build a new one.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Sequence
+
+import numpy as np
+
+from . import (RESULT_BYTES, ZERO_BF16, ZERO_FP16, ZERO_FP32, ZERO_NORM_L2, ZERO_NORM_MAX, _check,
+               _ctl, _lib)
+
+_ENTRY = np.dtype([("src", np.uint64), ("dst", np.uint64), ("numel", np.int64),
+                   ("src_dtype", np.int32), ("dst_dtype", np.int32)])
+_KINDS = {"l2": ZERO_NORM_L2, "max": ZERO_NORM_MAX}
+
+
+class zero_tensor_plan_t(ctypes.Structure):
+    _fields_ = [("n_tensors", ctypes.c_int64), ("numel", ctypes.c_int64),
+                ("n_chunks", ctypes.c_int64), ("chunk", ctypes.c_int64),
+                ("table_bytes", ctypes.c_int64), ("writable", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+def _order(t):
+    """The strides of a tensor whose elements fill its memory, dimensions of
+    one element left out (None: contiguous); raises where there are gaps or
+    overlaps."""
+    if t.is_contiguous():
+        return None
+    dims = [(st, n) for st, n in zip(t.stride(), t.shape) if n != 1]
+    at = 1
+    for st, n in sorted(dims):
+        if st != at:
+            raise ValueError("tensors must be dense: their elements fill their memory in some "
+                             "order of the dimensions")
+        at *= n
+    return tuple(st for st, _ in dims)
+
+
+class zero_tensor_plan:
+    """The plan and device table of a list of tensors.
+
+    tensors   device tensors of one device, each torch.float32, float16 or
+              bfloat16 and dense (contiguous, or a permutation of the dimensions
+              of a contiguous tensor); empty ones are allowed
+    out       where the calls that write put their results: one tensor for each,
+              of as many elements and the same order in memory, of any of the
+              types; None: the tensors themselves
+    device    the table's device (by default the tensors'; needed for an empty
+              list)
+
+    The plan keeps the tensors.  A plan over tensors that overlap can be read
+    only: the calls that write raise ZeroError.
+    """
+
+    def __init__(self, tensors: Sequence, out: Optional[Sequence] = None, device=None):
+        import torch
+        codes = {torch.float32: ZERO_FP32, torch.float16: ZERO_FP16, torch.bfloat16: ZERO_BF16}
+        tensors = list(tensors)
+        outs = tensors if out is None else list(out)
+        if len(outs) != len(tensors):
+            raise ValueError("out: one tensor for each tensor")
+        if device is None:
+            device = tensors[0].device if tensors else "cuda"
+        device = torch.device(device)
+        if device.type != "cuda":
+            raise ValueError("device tensors expected")
+        if device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        entries = np.zeros(max(1, len(tensors)), dtype=_ENTRY)
+        rows = []
+        for t, o in zip(tensors, outs):
+            for x in ((t,) if o is t else (t, o)):
+                if x.layout != torch.strided:
+                    raise ValueError("tensors must be strided (not sparse)")
+                if x.device != device:
+                    raise ValueError(f"tensors on {device} expected, got one on {x.device}")
+                if x.dtype not in codes:
+                    raise TypeError(f"float32, float16 or bfloat16 tensors expected, got {x.dtype}")
+            order = _order(t)
+            if o is not t and (o.numel() != t.numel() or _order(o) != order or
+                               (order is not None and o.shape != t.shape)):
+                raise ValueError("out: as many elements as the tensor, in the same order")
+            rows.append((t.data_ptr(), o.data_ptr(), t.numel(), codes[t.dtype], codes[o.dtype]))
+        if rows:
+            entries[:] = rows
+        self.c = zero_tensor_plan_t()
+        n = len(tensors)
+        _check(_lib.zero_tensor_plan_init(entries.ctypes.data, n, ctypes.byref(self.c)),
+               "zero_tensor_plan_init")
+        host = np.empty(self.c.table_bytes // 8, dtype=np.int64)
+        _check(_lib.zero_tensor_plan_table(entries.ctypes.data, ctypes.byref(self.c),
+                                           host.ctypes.data), "zero_tensor_plan_table")
+        self.tensors, self.out, self.device = tensors, outs, device
+        self.n_tensors, self.numel = n, self.c.numel
+        self.workspace_bytes = int(_lib.zero_tensor_workspace_bytes(ctypes.byref(self.c)))
+        with torch.cuda.device(device):
+            self.table = torch.from_numpy(host).to(device)
+            self._streams = {torch.cuda.current_stream(device).cuda_stream}
+        self._args = (ctypes.byref(self.c), self.table.data_ptr())
+
+    def _call(self, fn, args, stream) -> None:
+        """fn(plan, table, *args, stream) with the plan's device current."""
+        import torch
+        if stream is None:
+            raw = torch.cuda.current_stream(self.device).cuda_stream
+        elif isinstance(stream, int):
+            raw = stream
+        else:
+            if stream.device != self.device:
+                raise ValueError(f"a stream of {self.device} expected")
+            raw = stream.cuda_stream
+        if raw not in self._streams:
+            # the table is the plan's own: its memory stays until that stream is done
+            self.table.record_stream(torch.cuda.ExternalStream(raw, device=self.device))
+            self._streams.add(raw)
+        if torch.cuda.current_device() == self.device.index:
+            rc = fn(*self._args, *args, raw)
+        else:
+            with torch.cuda.device(self.device):
+                rc = fn(*self._args, *args, raw)
+        _check(rc, fn.__name__)
+
+    def _buffer(self, t, nbytes: int, name: str) -> int:
+        if t.device != self.device:
+            raise ValueError(f"{name} must be a tensor on {self.device}")
+        if not t.is_contiguous() or t.numel() * t.element_size() < nbytes or t.data_ptr() % 8:
+            raise ValueError(f"{name}: {nbytes} contiguous bytes, 8-byte aligned")
+        return t.data_ptr()
+
+    def _norms(self, norms) -> Optional[int]:
+        import torch
+        if norms is None:
+            return None
+        if norms.device != self.device or norms.dtype != torch.float32 or \
+                not norms.is_contiguous() or norms.numel() < self.n_tensors:
+            raise ValueError(f"norms: float32[{self.n_tensors}] on {self.device}, contiguous")
+        return norms.data_ptr() or None
+
+    def _norm_args(self, inv_scale, ctl_dev, res, norms):
+        """The norm calls' arguments from inv_scale to norms."""
+        if ctl_dev is not None and ctl_dev.device != self.device:
+            raise ValueError(f"ctl must be a tensor on {self.device}")
+        return (float(inv_scale), None if ctl_dev is None else _ctl(ctl_dev),
+                self._buffer(res, RESULT_BYTES, "res"), self._norms(norms))
+
+    def _workspace(self, workspace):
+        return (self._buffer(workspace, self.workspace_bytes, "workspace"),
+                workspace.numel() * workspace.element_size())
+
+
+def _kind(kind) -> int:
+    if kind not in _KINDS:
+        raise ValueError(f"kind: one of {sorted(_KINDS)}")
+    return _KINDS[kind]
+
+
+def zero_tensor_workspace_bytes(plan: zero_tensor_plan) -> int:
+    return plan.workspace_bytes
+
+
+def zero_tensor_norm(plan: zero_tensor_plan, inv_scale: float, res, workspace, kind: str = "l2",
+                     norms=None, accumulate: bool = False, ctl_dev=None, stream=None) -> None:
+    """res: one zero_step_result (16 bytes); norms: float32[n_tensors] for each
+    tensor's own norm, or None; kind: 'l2' or 'max'."""
+    plan._call(_lib.zero_tensor_norm,
+               (_kind(kind), *plan._norm_args(inv_scale, ctl_dev, res, norms),
+                *plan._workspace(workspace), int(bool(accumulate))), stream)
+
+
+def zero_tensor_clip(plan: zero_tensor_plan, max_norm: float, res, norms=None,
+                     stream=None) -> None:
+    """By the norm in res, or with norms each tensor by its own."""
+    plan._call(_lib.zero_tensor_clip,
+               (float(max_norm), plan._buffer(res, RESULT_BYTES, "res"), plan._norms(norms)),
+               stream)
+
+
+def zero_tensor_clip_norm(plan: zero_tensor_plan, max_norm: float, inv_scale: float, res,
+                          workspace, kind: str = "l2", norms=None, per_tensor: bool = False,
+                          ctl_dev=None, stream=None) -> None:
+    """zero_tensor_norm, then zero_tensor_clip (per_tensor: each tensor by its
+    own norm, which norms receives)."""
+    if per_tensor and norms is None:
+        raise ValueError("per_tensor needs norms")
+    inv, ctl, res_p, norms_p = plan._norm_args(inv_scale, ctl_dev, res, norms)
+    plan._call(_lib.zero_tensor_clip_norm,
+               (_kind(kind), float(max_norm), inv, ctl, res_p, norms_p, int(bool(per_tensor)),
+                *plan._workspace(workspace)), stream)
+
+
+def zero_tensor_accumulate(plan: zero_tensor_plan, weight: float = 1.0, overwrite: bool = False,
+                           res=None, workspace=None, inv_scale: float = 1.0, kind: str = "l2",
+                           norms=None, accumulate: bool = False, ctl_dev=None,
+                           stream=None) -> None:
+    """out = out + weight * tensor (overwrite: out = weight * tensor); with res
+    and workspace also the norm of out, in the same pass."""
+    if res is None:
+        if norms is not None or workspace is not None or ctl_dev is not None:
+            raise ValueError("the norm needs res and workspace")
+        plan._call(_lib.zero_tensor_accumulate, (float(weight), int(bool(overwrite))), stream)
+        return
+    if workspace is None:
+        raise ValueError("the norm needs res and workspace")
+    plan._call(_lib.zero_tensor_accumulate_norm,
+               (float(weight), int(bool(overwrite)), _kind(kind),
+                *plan._norm_args(inv_scale, ctl_dev, res, norms),
+                *plan._workspace(workspace), int(bool(accumulate))), stream)
+
+
+def zero_tensor_accumulate_norm(plan: zero_tensor_plan, inv_scale: float, res, workspace,
+                                weight: float = 1.0, overwrite: bool = False, **norm_args) -> None:
+    """zero_tensor_accumulate with its norm (the C call's name)."""
+    zero_tensor_accumulate(plan, weight, overwrite, res=res, workspace=workspace,
+                           inv_scale=inv_scale, **norm_args)
