@@ -469,8 +469,10 @@ typedef struct zero_tensor_entry {
 typedef struct zero_tensor_plan {
     int64_t n_tensors;   /* entries                                           */
     int64_t numel;       /* elements of all                                   */
-    int64_t n_chunks;    /* pieces that the kernels work on                   */
-    int64_t chunk;       /* elements of a whole piece                         */
+    int64_t bytes;       /* of their inputs and outputs                       */
+    int64_t n_pieces;    /* pieces that the passes that write work on         */
+    int64_t n_runs;      /* pieces that the norm works on: whole ones         */
+    int64_t n_rests;     /* and smaller ones at the tensors' ends             */
     int64_t table_bytes; /* size of the device table                          */
     int32_t writable;    /* 1: no output overlaps another output, nor an input
                             that is not its own in place; 0: the calls that
@@ -488,8 +490,7 @@ enum zero_norm_kind {
  * and the plan is not writable.
  * Errors: ZERO_EINVAL for a NULL argument, a negative count, an unknown type, a
  * NULL or misaligned pointer with a nonzero numel; ZERO_ERANGE for addresses or
- * sizes that overflow, or more pieces than one launch holds (16,777,215);
- * ZERO_ENOMEM. */
+ * sizes that overflow, or over 16,777,214 tensors; ZERO_ENOMEM. */
 int zero_tensor_plan_init(const zero_tensor_entry* entries, int64_t n_tensors,
                           zero_tensor_plan* plan);
 
@@ -502,7 +503,8 @@ int zero_tensor_plan_table(const zero_tensor_entry* entries, const zero_tensor_p
                            void* table);
 
 /* Bytes of device workspace for the calls that take a norm: one 8-byte partial
- * per piece, plus one per 2048 of them where there are over 16384. */
+ * for at most 4096 elements, plus one for 4096 of these where there are over
+ * 32768. */
 size_t zero_tensor_workspace_bytes(const zero_tensor_plan* plan);
 
 /* Norm of the whole table, overflow flag and each tensor's own norm, unscaled

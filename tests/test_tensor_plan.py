@@ -11,8 +11,7 @@ from zero_partitioned_mixed_shard_amd import tensors as T
 
 FP16, BF16, FP32 = Z.ZERO_FP16, Z.ZERO_BF16, Z.ZERO_FP32
 SIZE = {FP16: 2, BF16: 2, FP32: 4}
-CHUNK_T = np.dtype([("src", np.uint64), ("dst", np.uint64), ("count", np.int32),
-                    ("tensor", np.int32), ("src_dtype", np.int32), ("dst_dtype", np.int32)])
+PIECE_T = np.dtype([("src", np.uint64), ("tensor", np.int32), ("info", np.uint32)])
 
 
 def entries(rows):
@@ -39,7 +38,7 @@ def table(rows, plan):
 
 
 def test_entry_and_plan_sizes():
-    assert T._ENTRY.itemsize == 32 and ctypes.sizeof(T.zero_tensor_plan_t) == 48
+    assert T._ENTRY.itemsize == 32 and ctypes.sizeof(T.zero_tensor_plan_t) == 64
 
 
 @pytest.mark.parametrize("seed", range(20))
@@ -56,34 +55,66 @@ def test_table_covers_every_element_once(seed):
     rc, plan = init(rows)
     assert rc == Z.ZERO_OK and plan.writable == 1
     assert plan.n_tensors == len(rows) and plan.numel == sum(r[2] for r in rows)
+    assert plan.bytes == sum(r[2] * (SIZE[r[3]] + SIZE[r[4]]) for r in rows)
     rc, buf = table(rows, plan)
     assert rc == Z.ZERO_OK
-    chunks = buf[:plan.n_chunks * 4].view(CHUNK_T)
-    first = buf[plan.n_chunks * 4:plan.table_bytes // 8]
-    assert len(first) == len(rows) + 1 and first[0] == 0 and first[-1] == plan.n_chunks
+    runs, pieces, dsts, first_run, first_rest, first = parts(buf, plan)
+    for f, a, n in ((first, 0, plan.n_pieces), (first_run, 0, plan.n_runs),
+                    (first_rest, plan.n_runs, plan.n_rests)):
+        assert len(f) == len(rows) + 1 and f[0] == a and f[-1] == a + n
     for k, (src, dst, n, s, d) in enumerate(rows):
-        mine = chunks[first[k]:first[k + 1]]
         done = 0
-        for c in mine:
-            assert (c["tensor"], c["src_dtype"], c["dst_dtype"]) == (k, s, d)
-            assert c["src"] == src + done * SIZE[s] and c["dst"] == dst + done * SIZE[d]
-            assert 0 < c["count"] <= plan.chunk
-            done += int(c["count"])
+        for j in range(first[k], first[k + 1]):
+            p, count = pieces[j], int(pieces[j]["info"]) & 0xFFFFFF
+            assert p["tensor"] == k and p["info"] >> 24 == s | d << 4
+            assert p["src"] == src + done * SIZE[s] and dsts[j] == dst + done * SIZE[d]
+            assert 0 < count <= PIECE
+            # every piece but a tensor's first begins at a multiple of 128 bytes of
+            # the output, and no piece but the first and last is short
+            assert done == 0 or dsts[j] % 128 == 0
+            assert j in (first[k], first[k + 1] - 1) or count == PIECE
+            done += count
         assert done == n
-        # every chunk but a tensor's last is whole, so aligned tensors stay aligned
-        assert (mine["count"][:-1] == plan.chunk).all() and plan.chunk % 8 == 0
+        # the norm's go by the number of elements alone: whole runs, then the rest
+        mine = np.concatenate([runs[first_run[k]:first_run[k + 1]],
+                               runs[first_rest[k]:first_rest[k + 1]]])
+        counts = (mine["info"] & 0xFFFFFF).astype(np.int64)
+        whole = first_run[k + 1] - first_run[k]
+        assert whole == n // RUN and (counts[:whole] == RUN).all()
+        assert (counts[whole:-1] == PIECE).all() and counts.sum() == n and (counts > 0).all()
+        assert (mine["tensor"] == k).all() and (mine["info"] >> 24 & 15 == s).all()
+        starts = np.cumsum(counts) - counts
+        assert (mine["src"] == src + (starts * SIZE[s]).astype(np.uint64)).all()
+
+
+RUN, PIECE = 16384, 4096
+
+
+def parts(buf, plan):
+    """Runs and rests, pieces, outputs' addresses, and every tensor's first run, rest
+    and piece."""
+    n, r, t = plan.n_pieces, plan.n_runs + plan.n_rests, plan.n_tensors + 1
+    buf = buf[:plan.table_bytes // 8]
+    assert len(buf) == 2 * r + 3 * n + 3 * t
+    a, b = 2 * (r + n), 2 * r + 3 * n
+    return (buf[:2 * r].view(PIECE_T), buf[2 * r:a].view(PIECE_T), buf[a:b].view(np.uint64),
+            buf[b:b + t], buf[b + t:b + 2 * t], buf[b + 2 * t:])
 
 
 def test_large_tensors_have_64_bit_addresses():
     n = (1 << 36) + 5
-    rows = [(1 << 40, 1 << 42, n, BF16, FP32)]
+    rows = [(1 << 40, (1 << 42) + 4, n, BF16, FP32)]
     rc, plan = init(rows)
     assert rc == Z.ZERO_OK and plan.numel == n
     rc, buf = table(rows, plan)
-    last = buf[:plan.n_chunks * 4].view(CHUNK_T)[-1]
-    start = (plan.n_chunks - 1) * plan.chunk
-    assert last["src"] == (1 << 40) + 2 * start and last["dst"] == (1 << 42) + 4 * start
-    assert last["count"] == n - start
+    runs, pieces, dsts, _, _, _ = parts(buf, plan)
+    start = (plan.n_pieces - 1) * PIECE - 1            # the first piece is one element short
+    assert pieces[-1]["src"] == (1 << 40) + 2 * start and dsts[-1] == (1 << 42) + 4 + 4 * start
+    assert int(pieces[-1]["info"]) & 0xFFFFFF == n - start
+    start = plan.n_runs * RUN
+    assert plan.n_rests == 1 and runs[-1]["src"] == (1 << 40) + 2 * start
+    assert int(runs[-1]["info"]) & 0xFFFFFF == n - start
+    assert runs[-2]["src"] == (1 << 40) + 2 * (start - RUN)
 
 
 @pytest.mark.parametrize("rows,writable", [
@@ -115,9 +146,10 @@ def test_init_refusals():
         assert init([ok, row])[0] == Z.ZERO_EINVAL, what
     for row in ((4096, 8192, 1 << 62, FP16, FP32), (2 ** 64 - 8, 8192, 10, FP16, FP32)):
         assert init([row])[0] == Z.ZERO_ERANGE
-    # a whole int64 of elements in two tensors; and more pieces than a launch has blocks
+    # more than an int64 of elements, and more pieces than any memory holds
     assert init([(4096, 4096, (1 << 62) - 1, FP16, FP16)] * 3)[0] == Z.ZERO_ERANGE
-    assert init([(4096, 4096, 1 << 50, FP16, FP16)])[0] == Z.ZERO_ERANGE
+    assert init([(4096, 4096, 1 << 55, FP16, FP16)])[0] == Z.ZERO_ERANGE
+    assert init([(4096, 4096, 0, FP16, FP16)], n=1 << 24)[0] == Z.ZERO_ERANGE   # tensors
     # pointers and types of nothing: only the types are looked at
     assert init([(0, 0, 0, FP16, FP32)])[0] == Z.ZERO_OK
     L, plan = Z.lib(), T.zero_tensor_plan_t()
@@ -138,10 +170,11 @@ def test_init_refusals():
 
 def test_workspace_bytes():
     assert Z.lib().zero_tensor_workspace_bytes(None) == 0
-    for rows in ([], [(4096, 4096, 1, FP16, FP16)], [(4096, 4096, 1 << 33, FP16, FP16)]):
+    for rows in ([], [(4096, 4096, 1, FP16, FP16)], [(4096, 4096, 1 << 33, FP16, FP16)],
+                 [(4096, 4096, 1 << 40, FP16, FP16)]):
         rc, plan = init(rows)
         ws = Z.lib().zero_tensor_workspace_bytes(ctypes.byref(plan))
-        assert max(16, 8 * plan.n_chunks) <= ws <= 8 * (plan.n_chunks + plan.n_chunks // 2048 + 2)
+        assert max(16, 8 * plan.n_pieces) <= ws <= 8 * (plan.n_pieces + plan.n_pieces // 4096 + 2)
 
 
 def test_call_refusals():

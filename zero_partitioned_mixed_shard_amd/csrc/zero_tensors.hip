@@ -2,16 +2,17 @@
 // zero_tensor_* calls of include/zero_shard.h): the norm of all of them and of
 // each, clipping by it, and accumulation of one table into another.
 //
-// A host-built plan cuts every tensor into chunks of at most plan->chunk
-// elements and the device table holds one 32-byte record per chunk, so a block
-// learns all about its work from one scalar load (no search from a block
-// number to a tensor) and no block spans two tensors: a chunk's partial
-// belongs to one tensor, and a tensor's norm is the sum of its chunks'.
+// A host-built plan cuts every tensor into pieces of at most kPiece elements
+// and the device table holds a record per piece, so a wave or block learns all
+// about its work from one scalar load (no search from a block number to a
+// tensor) and nothing spans two tensors: a piece's partial belongs to one
+// tensor, and a tensor's norm is the sum of its pieces'.
 //
 // Every kernel is a streaming pass bound by HBM (at most 4 operations per
-// element).  Tensors start at any element, so lanes use 16-byte accesses that
-// are aligned to the element only, which gfx950 global memory takes as they
-// are; only a chunk's last tile, where it is short, goes element by element.
+// element).  Tensors start at any element, so lanes use 16-byte (or 8-byte)
+// accesses that are aligned to the element only, which gfx950 global memory
+// takes as they are; pieces are cut so that all but a tensor's first begin at a
+// multiple of 128 bytes of its output.
 //
 // Numerics: the squares and their sums are fp64 (the square of an fp32 value
 // is exact there, and the sum cannot overflow), the unscale factor is applied
@@ -29,26 +30,37 @@
 
 namespace {
 
-// One chunk of the device table.
-struct Chunk {
+// One piece in the device table.  The outputs' addresses are an array of their
+// own after the pieces.
+struct Piece {
     const void* src;
-    void* dst;
-    int32_t count;     // elements, 1 .. plan->chunk
     int32_t tensor;    // index in the table
-    int32_t src_dtype, dst_dtype;
+    uint32_t info;     // elements | src type << 24 | dst type << 28
+    __device__ int count() const { return (int)(info & 0xFFFFFFu); }
+    __device__ int src_dtype() const { return (int)(info >> 24 & 15u); }
+    __device__ int dst_dtype() const { return (int)(info >> 28); }
 };
-static_assert(sizeof(Chunk) == 32, "one scalar load");
+static_assert(sizeof(Piece) == 16, "one scalar load");
 
-// Elements per chunk.
-constexpr int64_t kChunk = 16384;
+// Elements of a whole piece of the passes that write, and of a rest.
+constexpr int kPiece = 4096;
+// Elements of a run.
+constexpr int kRun = 16384;
+// Loads of 16 bytes that a lane has in flight in the norm of a run, and of a
+// rest.
+constexpr int kRunLoads = 4, kRestLoads = 8;
+constexpr int kWaves = kThreads / 64;
 
 // Tensor pointers come out of the table; these types make the accesses global
-// ones (not flat), of 16 bytes at any element.
+// ones (not flat), at any element.
 typedef __attribute__((address_space(1))) const char g_cbyte;
 typedef __attribute__((address_space(1))) char g_byte;
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
 typedef __attribute__((address_space(1))) const u32x4_a2 g_cu32x4_a2;
 typedef __attribute__((address_space(1))) u32x4_a2 g_u32x4_a2;
+typedef __attribute__((address_space(1))) const u32x2_a2 g_cu32x2_a2;
+typedef __attribute__((address_space(1))) u32x2_a2 g_u32x2_a2;
 typedef __attribute__((address_space(1))) const uint16_t g_cu16;
 typedef __attribute__((address_space(1))) uint16_t g_u16;
 typedef __attribute__((address_space(1))) const float g_cf32;
@@ -57,16 +69,11 @@ typedef __attribute__((address_space(1))) float g_f32;
 template <int DT>
 constexpr int kBytes = DT == ZERO_FP32 ? 4 : 2;
 
-// ---------------------------------------------------------- 8 elements -----
-__device__ __forceinline__ float half_to_f32(uint16_t b) {
-    return (float)__builtin_bit_cast(_Float16, b);
-}
-__device__ __forceinline__ float bf_to_f32(uint16_t b) {
-    return __uint_as_float((uint32_t)b << 16);
-}
+// --------------------------------------------------------- elements --------
 template <int DT>
 __device__ __forceinline__ float widen(uint16_t b) {
-    return DT == ZERO_FP16 ? half_to_f32(b) : bf_to_f32(b);
+    return DT == ZERO_FP16 ? (float)__builtin_bit_cast(_Float16, b)
+                           : __uint_as_float((uint32_t)b << 16);
 }
 // Nearest, ties to even; overflow gives inf, NaN stays (quiet) NaN.
 template <int DT>
@@ -77,51 +84,82 @@ __device__ __forceinline__ uint16_t narrow(float f) {
     return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
 }
 
-// A tile of kVec elements as it lies in memory.
-template <int DT>
+// W (4 or 8) consecutive elements of a lane as they lie in memory.
+template <int DT, int W>
 struct Raw {
-    u32x4 w[DT == ZERO_FP32 ? 2 : 1];
+    static constexpr int kDwords = W * kBytes<DT> / 4;
+    uint32_t w[kDwords];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int k = 0; k < kDwords; ++k) w[k] = 0;
+    }
     __device__ __forceinline__ float get(int k) const {
-        if (DT == ZERO_FP32) return __uint_as_float(w[k >> 2][k & 3]);
-        return widen<DT>(half_of(w[0], k));
+        if constexpr (DT == ZERO_FP32) return __uint_as_float(w[k]);
+        else return widen<DT>((uint16_t)((k & 1) ? (w[k >> 1] >> 16) : (w[k >> 1] & 0xFFFFu)));
+    }
+    __device__ __forceinline__ void set(int k, float v) {
+        if constexpr (DT == ZERO_FP32) w[k] = __float_as_uint(v);
+        else if (k & 1) w[k >> 1] |= (uint32_t)narrow<DT>(v) << 16;   // after the even one
+        else w[k >> 1] = narrow<DT>(v);
     }
 };
-template <int DT>
-__device__ __forceinline__ Raw<DT> load_tile(const void* p, int e) {
-    Raw<DT> r;
-    g_cu32x4_a2* q = (g_cu32x4_a2*)((g_cbyte*)p + (int64_t)e * kBytes<DT>);
-    r.w[0] = q[0];
-    if (DT == ZERO_FP32) r.w[DT == ZERO_FP32 ? 1 : 0] = q[1];
+template <int DT, int W, bool NT>
+__device__ __forceinline__ Raw<DT, W> load_raw(const void* p, int e) {
+    Raw<DT, W> r;
+    g_cbyte* b = (g_cbyte*)p + (int64_t)e * kBytes<DT>;
+    if constexpr (Raw<DT, W>::kDwords == 2) {
+        const u32x2 v = NT ? __builtin_nontemporal_load((g_cu32x2_a2*)b) : *(g_cu32x2_a2*)b;
+        r.w[0] = v[0];
+        r.w[1] = v[1];
+    } else {
+#pragma unroll
+        for (int q = 0; q < Raw<DT, W>::kDwords / 4; ++q) {
+            g_cu32x4_a2* c = (g_cu32x4_a2*)b + q;
+            const u32x4 v = NT ? __builtin_nontemporal_load(c) : *c;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) r.w[4 * q + k] = v[k];
+        }
+    }
     return r;
 }
-template <int DT>
-__device__ __forceinline__ void store_tile(void* p, int e, const float (&v)[kVec]) {
-    g_u32x4_a2* q = (g_u32x4_a2*)((g_byte*)p + (int64_t)e * kBytes<DT>);
-    if (DT == ZERO_FP32) {
-        u32x4 a, b;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            a[k] = __float_as_uint(v[k]);
-            b[k] = __float_as_uint(v[k + 4]);
-        }
-        q[0] = a;
-        q[1] = b;
+template <int DT, int W, bool NT>
+__device__ __forceinline__ void store_raw(void* p, int e, const Raw<DT, W>& r) {
+    g_byte* b = (g_byte*)p + (int64_t)e * kBytes<DT>;
+    if constexpr (Raw<DT, W>::kDwords == 2) {
+        const u32x2 v = {r.w[0], r.w[1]};
+        if (NT) __builtin_nontemporal_store(v, (g_u32x2_a2*)b);
+        else *(g_u32x2_a2*)b = v;
     } else {
-        uint16_t h[kVec];
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) h[k] = narrow<DT>(v[k]);
-        q[0] = pack8(h);
+        for (int q = 0; q < Raw<DT, W>::kDwords / 4; ++q) {
+            g_u32x4_a2* c = (g_u32x4_a2*)b + q;
+            const u32x4 v = {r.w[4 * q], r.w[4 * q + 1], r.w[4 * q + 2], r.w[4 * q + 3]};
+            if (NT) __builtin_nontemporal_store(v, c);
+            else *c = v;
+        }
     }
 }
 template <int DT>
 __device__ __forceinline__ float load_one(const void* p, int e) {
-    if (DT == ZERO_FP32) return ((g_cf32*)p)[e];
-    return widen<DT>(((g_cu16*)p)[e]);
+    if constexpr (DT == ZERO_FP32) return ((g_cf32*)p)[e];
+    else return widen<DT>(((g_cu16*)p)[e]);
 }
 template <int DT>
 __device__ __forceinline__ void store_one(void* p, int e, float v) {
-    if (DT == ZERO_FP32) ((g_f32*)p)[e] = v;
+    if constexpr (DT == ZERO_FP32) ((g_f32*)p)[e] = v;
     else ((g_u16*)p)[e] = narrow<DT>(v);
+}
+
+template <int V>
+struct Int {
+    static constexpr int value = V;
+};
+// go(a type as an integral constant), for a piece's input, or output.
+template <typename F>
+__device__ __forceinline__ void by_type(int dtype, F&& go) {
+    if (dtype == ZERO_FP32) go(Int<ZERO_FP32>{});
+    else if (dtype == ZERO_FP16) go(Int<ZERO_FP16>{});
+    else go(Int<ZERO_BF16>{});
 }
 
 // ------------------------------------------------------------ norms --------
@@ -154,102 +192,182 @@ __device__ __forceinline__ double join(double a, double b) {
     const uint64_t y = __builtin_bit_cast(uint64_t, b) & ~(uint64_t(1) << 63);
     return __builtin_bit_cast(double, x > y ? x : y);
 }
-
-// The block's lanes joined, in a fixed order; valid in thread 0.
 template <int KIND>
-__device__ __forceinline__ double block_join(double v) {
-    __shared__ double part[kThreads / 64];
+__device__ __forceinline__ double wave_join(double v) {
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) v = join<KIND>(v, __shfl_xor(v, off, 64));
+    return v;
+}
+// The block's lanes joined, in a fixed order; valid in thread 0.
+template <int KIND, int T = kThreads>
+__device__ __forceinline__ double block_join(double v) {
+    __shared__ double part[T / 64];
+    v = wave_join<KIND>(v);
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
     __syncthreads();
     if (threadIdx.x == 0) {
         v = part[0];
 #pragma unroll
-        for (int k = 1; k < kThreads / 64; ++k) v = join<KIND>(v, part[k]);
+        for (int k = 1; k < T / 64; ++k) v = join<KIND>(v, part[k]);
     }
     return v;
 }
 
-template <int KIND, int DT>
-__device__ __forceinline__ double chunk_norm(const void* src, int count) {
+// Thread t's share, of T, of the norm of a run (WHOLE: exactly kRun elements) or
+// a rest, U loads of 16 bytes in flight.
+template <int KIND, int DT, int T, int U, bool WHOLE>
+__device__ __forceinline__ double span_norm(const void* src, int count, int t) {
+    constexpr int W = 16 / kBytes<DT>, R = T * W;
+    static_assert(kRun % (U * R) == 0, "whole batches");
     Norm<KIND> n;
-    int e = threadIdx.x * kVec;
-#pragma unroll 4
-    for (; e + kVec <= count; e += kTile) {
-        const Raw<DT> r = load_tile<DT>(src, e);
+    const int e = t * W;
+    auto add = [&](const Raw<DT, W>(&r)[U]) {
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) n.add(r.get(k));
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int k = 0; k < W; ++k) n.add(r[u].get(k));
+    };
+    if (WHOLE) {
+#pragma unroll
+        for (int b = 0; b < kRun; b += U * R) {
+            Raw<DT, W> r[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) r[u] = load_raw<DT, W, true>(src, b + e + u * R);
+            add(r);
+        }
+    } else {
+        for (int b = 0; b < count; b += U * R) {
+            Raw<DT, W> r[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                r[u].clear();
+                if (b + e + u * R + W <= count) r[u] = load_raw<DT, W, true>(src, b + e + u * R);
+            }
+            add(r);
+        }
+        const int last = count / W * W + t;
+        if (last < count) n.add(load_one<DT>(src, last));
     }
-    for (int end = e + kVec; e < end && e < count; ++e) n.add(load_one<DT>(src, e));
     return n.value();
 }
 
-// One partial per chunk.
+// One partial per run, a block each, then one per rest, a wave each.
 template <int KIND>
 __global__ void __launch_bounds__(kThreads)
-tensor_norm_kernel(const Chunk* __restrict__ chunks, double* __restrict__ part) {
-    const Chunk c = chunks[blockIdx.x];
-    double v;
-    if (c.src_dtype == ZERO_FP32) v = chunk_norm<KIND, ZERO_FP32>(c.src, c.count);
-    else if (c.src_dtype == ZERO_FP16) v = chunk_norm<KIND, ZERO_FP16>(c.src, c.count);
-    else v = chunk_norm<KIND, ZERO_BF16>(c.src, c.count);
-    v = block_join<KIND>(v);
-    if (threadIdx.x == 0) part[blockIdx.x] = v;
+tensor_norm_kernel(const Piece* __restrict__ runs, int64_t n_runs, int64_t n_rests, int64_t blk0,
+                   double* __restrict__ part) {
+    const int64_t b = blk0 + blockIdx.x;
+    double v = 0.0;
+    if (b < n_runs) {
+        const Piece p = runs[b];
+        by_type(p.src_dtype(), [&](auto s) {
+            v = span_norm<KIND, decltype(s)::value, kThreads, kRunLoads, true>(p.src, kRun, threadIdx.x);
+        });
+        v = block_join<KIND>(v);
+        if (threadIdx.x == 0) part[b] = v;
+        return;
+    }
+    const int64_t i = (b - n_runs) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (i >= n_rests) return;
+    const Piece p = runs[n_runs + i];
+    const int lane = threadIdx.x & 63;
+    by_type(p.src_dtype(), [&](auto s) {
+        v = span_norm<KIND, decltype(s)::value, 64, kRestLoads, false>(p.src, p.count(), lane);
+    });
+    v = wave_join<KIND>(v);
+    if (lane == 0) part[n_runs + i] = v;
 }
 
-// Block b joins partials [b*kFold, (b+1)*kFold).
+// Thread `t` of T's share of part[0, n): part[t], part[t + T], ..., kInFlight
+// loads at a time.
+constexpr int kInFlight = 16;
+template <int KIND, int T>
+__device__ __forceinline__ double strided_join(const double* __restrict__ part, int64_t n, int t) {
+    double v = 0.0;
+    for (int64_t b = 0; b < n; b += kInFlight * T) {
+        double x[kInFlight];
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) {
+            const int64_t j = b + u * T + t;
+            x[u] = j < n ? part[j] : 0.0;
+        }
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) v = join<KIND>(v, x[u]);
+    }
+    return v;
+}
+
+// Block b joins partials [b * kFoldEach, (b + 1) * kFoldEach).
+constexpr int kFoldEach = kInFlight * kThreads;
 template <int KIND>
 __global__ void __launch_bounds__(kThreads)
 tensor_fold_kernel(const double* __restrict__ part, int64_t n, double* __restrict__ out) {
-    double v = 0.0;
-    const int64_t base = (int64_t)blockIdx.x * kFold;
-#pragma unroll
-    for (int k = 0; k < kFold / kThreads; ++k) {
-        const int64_t j = base + k * kThreads + threadIdx.x;
-        if (j < n) v = join<KIND>(v, part[j]);
-    }
-    v = block_join<KIND>(v);
+    const int64_t a = (int64_t)blockIdx.x * kFoldEach;
+    const int64_t left = n - a < kFoldEach ? n - a : kFoldEach;
+    const double v = block_join<KIND>(strided_join<KIND, kThreads>(part + a, left, threadIdx.x));
     if (threadIdx.x == 0) out[blockIdx.x] = v;
 }
 
-// Block 0 joins the n (folded) partials into *res; block 1 + k joins tensor
-// k's chunk partials into norms[k].
+// The result for a joined norm v, and its way into *res.
 template <int KIND>
-__global__ void __launch_bounds__(kThreads)
-tensor_finish_kernel(const double* __restrict__ part, int64_t n, const double* __restrict__ chunk_part,
-                     const int64_t* __restrict__ first, float inv_scale,
+__device__ __forceinline__ zero_step_result result_of(double v, float inv) {
+    zero_step_result r;
+    const double x = KIND == ZERO_NORM_L2 ? v : v * v;
+    r.sumsq = x * ((double)inv * (double)inv);
+    r.overflow = x < INFINITY ? 0u : 1u;              // NaN and inf are not
+    r.inv_scale = inv;
+    return r;
+}
+template <int KIND>
+__device__ __forceinline__ void store_result(zero_step_result r, int accumulate,
+                                             zero_step_result* res) {
+    if (accumulate) {
+        r.overflow |= res->overflow;
+        r.sumsq = join<KIND>(res->sumsq, r.sumsq);
+    }
+    *res = r;
+}
+
+template <int KIND>
+__device__ __forceinline__ float tensor_norm(double v, float inv) {
+    return (float)((KIND == ZERO_NORM_L2 ? sqrt(v) : v) * (double)inv);
+}
+
+// Block 0 joins the n (folded) partials into *res; the others join each tensor's
+// partials, which are at first[t] to first[t + 1] and (where given) first2[t]
+// to first2[t + 1], into norms, T threads to a tensor.
+constexpr int kFinishThreads = 1024;
+template <int KIND, int T>
+__global__ void __launch_bounds__(kFinishThreads)
+tensor_finish_kernel(const double* __restrict__ part, int64_t n,
+                     const double* __restrict__ tensor_part, const int64_t* __restrict__ first,
+                     const int64_t* __restrict__ first2, int64_t n_tensors, float inv_scale,
                      const zero_step_control* __restrict__ ctl, int accumulate,
                      zero_step_result* res, float* __restrict__ norms) {
     const float inv = ctl ? ctl->inv_scale : inv_scale;
-    double v = 0.0;
     if (blockIdx.x == 0) {
-        for (int64_t j = threadIdx.x; j < n; j += kThreads) v = join<KIND>(v, part[j]);
-        v = block_join<KIND>(v);
-        if (threadIdx.x != 0) return;
-        const double x = KIND == ZERO_NORM_L2 ? v : v * v;
-        uint32_t bad = x < INFINITY ? 0u : 1u;        // NaN and inf are not
-        double sumsq = x * ((double)inv * (double)inv);
-        if (accumulate) {
-            bad |= res->overflow;
-            sumsq = join<KIND>(res->sumsq, sumsq);
-        }
-        res->sumsq = sumsq;
-        res->overflow = bad;
-        res->inv_scale = inv;
+        const double v = block_join<KIND, kFinishThreads>(
+            strided_join<KIND, kFinishThreads>(part, n, threadIdx.x));
+        if (threadIdx.x == 0) store_result<KIND>(result_of<KIND>(v, inv), accumulate, res);
         return;
     }
-    const int64_t t = (int64_t)blockIdx.x - 1;
-    for (int64_t j = first[t] + threadIdx.x; j < first[t + 1]; j += kThreads)
-        v = join<KIND>(v, chunk_part[j]);
-    v = block_join<KIND>(v);
-    if (threadIdx.x == 0)
-        norms[t] = (float)((KIND == ZERO_NORM_L2 ? sqrt(v) : v) * (double)inv);
+    const int64_t t = ((int64_t)blockIdx.x - 1) * (kFinishThreads / T) +
+                      __builtin_amdgcn_readfirstlane(threadIdx.x / T);
+    if (t >= n_tensors) return;                       // whole waves, or the whole block
+    const int64_t a = first[t];
+    double v = strided_join<KIND, T>(tensor_part + a, first[t + 1] - a, threadIdx.x % T);
+    if (first2) {
+        const int64_t a2 = first2[t];
+        v = join<KIND>(v, strided_join<KIND, T>(tensor_part + a2, first2[t + 1] - a2, threadIdx.x % T));
+    }
+    if (T == kFinishThreads) v = block_join<KIND, kFinishThreads>(v);
+    else v = wave_join<KIND>(v);
+    if (threadIdx.x % T == 0) norms[t] = tensor_norm<KIND>(v, inv);
 }
 
 // ------------------------------------------------------------- clip --------
-// max_norm / (norm + 1e-6) where that is below 1, else 1, times the unscale
-// factor; fp64, rounded once.
+// max_norm / (norm + 1e-6) where that is below 1, else 1 (a NaN norm: 1), times
+// the unscale factor; fp64, rounded once; never NaN.
 __device__ __forceinline__ float clip_factor(float max_norm, double norm, float inv) {
     double c = 1.0;
     if (max_norm > 0.0f) {
@@ -259,91 +377,212 @@ __device__ __forceinline__ float clip_factor(float max_norm, double norm, float 
     return (float)(c * (double)inv);
 }
 
+// Resident blocks per CU of the passes that write.
+constexpr int kClipBlocksPerCU = 5, kAddBlocksPerCU = 3;
+
+// Elements per lane access of a pass that reads SRC and writes DST: 16 bytes of
+// the wider of the two.
 template <int SRC, int DST>
-__device__ __forceinline__ void chunk_scale(const void* src, void* dst, int count, float f) {
-    int e = threadIdx.x * kVec;
-#pragma unroll 4
-    for (; e + kVec <= count; e += kTile) {
-        const Raw<SRC> r = load_tile<SRC>(src, e);
-        float v[kVec];
+constexpr int kWidth = kBytes<SRC> == 4 || kBytes<DST> == 4 ? 4 : 8;
+
+// factor() is called after the loads are issued: its fp64 root and division
+// overlap their latency.  It is NaN where the step is skipped.  NT: loads that do
+// not stay in the caches.
+template <int SRC, int DST, bool NT, int T, typename F>
+__device__ __forceinline__ void piece_scale(const void* src, void* dst, int count, F&& factor) {
+    constexpr int W = kWidth<SRC, DST>, R = W * T, U = (kPiece + R - 1) / R;
+    const int e = threadIdx.x * W;
+    auto scaled = [](const Raw<SRC, W>& x, float f) {
+        Raw<DST, W> y;
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) v[k] = r.get(k) * f;
-        store_tile<DST>(dst, e, v);
-    }
-    for (int end = e + kVec; e < end && e < count; ++e)
-        store_one<DST>(dst, e, load_one<SRC>(src, e) * f);
-}
-
-// Calls go(SRC, DST as integral constants) for a chunk's types.
-template <int V>
-struct Int {
-    static constexpr int value = V;
-};
-template <typename F>
-__device__ __forceinline__ void by_types(const Chunk& c, F&& go) {
-    auto by_dst = [&](auto src) {
-        if (c.dst_dtype == ZERO_FP32) go(src, Int<ZERO_FP32>{});
-        else if (c.dst_dtype == ZERO_FP16) go(src, Int<ZERO_FP16>{});
-        else go(src, Int<ZERO_BF16>{});
+        for (int k = 0; k < W; ++k) y.set(k, x.get(k) * f);
+        return y;
     };
-    if (c.src_dtype == ZERO_FP32) by_dst(Int<ZERO_FP32>{});
-    else if (c.src_dtype == ZERO_FP16) by_dst(Int<ZERO_FP16>{});
-    else by_dst(Int<ZERO_BF16>{});
+    Raw<SRC, W> r[U];
+    if (U * R == kPiece && count == kPiece) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) r[u] = load_raw<SRC, W, NT>(src, e + u * R);
+        const float f = factor();
+        if (f != f) return;                           // skipped step: write nothing
+#pragma unroll
+        for (int u = 0; u < U; ++u) store_raw<DST, W, true>(dst, e + u * R, scaled(r[u], f));
+        return;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (e + u * R + W <= count) r[u] = load_raw<SRC, W, NT>(src, e + u * R);
+    const int t = count / W * W + threadIdx.x;
+    const float last = t < count ? load_one<SRC>(src, t) : 0.0f;
+    const float f = factor();
+    if (f != f) return;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (e + u * R + W <= count) store_raw<DST, W, true>(dst, e + u * R, scaled(r[u], f));
+    if (t < count) store_one<DST>(dst, t, last * f);
+}
+template <bool NT, int T, typename F>
+__device__ __forceinline__ void scale_by_types(const Piece& p, void* dst, F&& factor) {
+    by_type(p.src_dtype(), [&](auto s) {
+        by_type(p.dst_dtype(), [&](auto d) {
+            piece_scale<decltype(s)::value, decltype(d)::value, NT, T>(p.src, dst, p.count(), factor);
+        });
+    });
 }
 
+template <bool NT>
 __global__ void __launch_bounds__(kThreads)
-tensor_clip_kernel(const Chunk* __restrict__ chunks, float max_norm,
+tensor_clip_kernel(const Piece* __restrict__ pieces, void* const* __restrict__ dsts, float max_norm,
                    const zero_step_result* __restrict__ res, const float* __restrict__ norms) {
     if (res->overflow) return;                       // skipped step: write nothing
-    const Chunk c = chunks[blockIdx.x];
-    const double norm = norms ? (double)norms[c.tensor] : sqrt(res->sumsq);
-    const float f = clip_factor(max_norm, norm, res->inv_scale);
-    by_types(c, [&](auto s, auto d) {
-        chunk_scale<decltype(s)::value, decltype(d)::value>(c.src, c.dst, c.count, f);
+    const Piece p = pieces[blockIdx.x];
+    scale_by_types<NT, kThreads>(p, dsts[blockIdx.x], [&] {
+        return clip_factor(max_norm, norms ? (double)norms[p.tensor] : sqrt(res->sumsq),
+                           res->inv_scale);
     });
+}
+
+// The clip right after the partials of a norm, at most kJoinPartials: every block
+// joins them itself (in the order of tensor_finish_kernel, so to the same
+// bits), which spares that launch; block 0 stores the result.
+constexpr int kJoinPartials = 1024;
+static_assert(kJoinPartials == kFinishThreads && kJoinPartials % kThreads == 0,
+              "the finishing block's one partial per thread");
+template <int KIND>
+__global__ void __launch_bounds__(kThreads)
+tensor_join_clip_kernel(const Piece* __restrict__ pieces, void* const* __restrict__ dsts,
+                        float max_norm, const double* __restrict__ part, int n, float inv_scale,
+                        const zero_step_control* __restrict__ ctl, zero_step_result* res) {
+    __shared__ double joined[kJoinPartials / 64];
+    const Piece p = pieces[blockIdx.x];
+    scale_by_types<false, kThreads>(p, dsts[blockIdx.x], [&] {
+        double x[kJoinPartials / kThreads];
+#pragma unroll
+        for (int q = 0; q < kJoinPartials / kThreads; ++q) {
+            const int j = q * kThreads + threadIdx.x;
+            x[q] = j < n ? part[j] : 0.0;
+        }
+        const float inv = ctl ? ctl->inv_scale : inv_scale;
+#pragma unroll
+        for (int q = 0; q < kJoinPartials / kThreads; ++q) {
+            x[q] = wave_join<KIND>(x[q]);
+            if ((threadIdx.x & 63) == 0) joined[q * kWaves + (threadIdx.x >> 6)] = x[q];
+        }
+        __syncthreads();
+        double v = joined[0];
+#pragma unroll
+        for (int k = 1; k < kJoinPartials / 64; ++k) v = join<KIND>(v, joined[k]);
+        const zero_step_result r = result_of<KIND>(v, inv);
+        if (blockIdx.x == 0 && threadIdx.x == 0) *res = r;
+        return r.overflow ? NAN : clip_factor(max_norm, sqrt(r.sumsq), inv);
+    });
+}
+
+// Norm, each tensor's norm and (CLIP) the clip of a table of at most kOneBlock
+// rests and no run, in one block: one launch instead of two or three.
+constexpr int kOneBlock = 16;
+template <int KIND, bool CLIP>
+__global__ void __launch_bounds__(kFinishThreads)
+tensor_one_block_kernel(const Piece* __restrict__ rests, int n_rests,
+                        const Piece* __restrict__ pieces, void* const* __restrict__ dsts, int n_pieces,
+                        const int64_t* __restrict__ first, int64_t n_tensors, float max_norm,
+                        int per_tensor, float inv_scale, const zero_step_control* __restrict__ ctl,
+                        int accumulate, zero_step_result* res, float* __restrict__ norms) {
+    __shared__ double part[kOneBlock];
+    static_assert(kOneBlock == kFinishThreads / 64, "a wave for each rest");
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    double v = 0.0;
+    if (w < n_rests) {
+        const Piece p = rests[w];
+        by_type(p.src_dtype(), [&](auto s) {
+            v = span_norm<KIND, decltype(s)::value, 64, kRestLoads, false>(p.src, p.count(), lane);
+        });
+    }
+    v = wave_join<KIND>(v);
+    if (lane == 0) part[w] = v;
+    const float inv = ctl ? ctl->inv_scale : inv_scale;
+    __syncthreads();
+    v = part[0];
+#pragma unroll
+    for (int k = 1; k < kOneBlock; ++k) v = join<KIND>(v, part[k]);
+    const zero_step_result r = result_of<KIND>(v, inv);
+    if (threadIdx.x == 0) store_result<KIND>(r, accumulate, res);
+    auto norm_of = [&](int64_t t) {
+        double x = 0.0;
+        for (int64_t j = first[t]; j < first[t + 1]; ++j) x = join<KIND>(x, part[j]);
+        return tensor_norm<KIND>(x, inv);
+    };
+    if (norms)
+        for (int64_t t = threadIdx.x; t < n_tensors; t += kFinishThreads) norms[t] = norm_of(t);
+    if (!CLIP || r.overflow) return;
+    for (int k = 0; k < n_pieces; ++k) {
+        const Piece p = pieces[k];
+        const double norm = per_tensor ? (double)norm_of(p.tensor) : sqrt(r.sumsq);
+        scale_by_types<false, kFinishThreads>(p, dsts[k],
+                                              [&] { return clip_factor(max_norm, norm, inv); });
+    }
 }
 
 // ------------------------------------------------------- accumulate --------
 // KIND 0: no norm of the result.
-template <int KIND, bool FIRST, int SRC, int DST>
-__device__ __forceinline__ void chunk_accumulate(const void* src, void* dst, int count, float w,
+template <int KIND, bool FIRST, int SRC, int DST, bool NT>
+__device__ __forceinline__ void piece_accumulate(const void* src, void* dst, int count, float w,
                                                  Norm<KIND>& n) {
-    // the value as stored: what a later pass over dst would read
-    auto stored = [](float v) { return DST == ZERO_FP32 ? v : widen<DST>(narrow<DST>(v)); };
-    int e = threadIdx.x * kVec;
-#pragma unroll 2
-    for (; e + kVec <= count; e += kTile) {
-        const Raw<SRC> x = load_tile<SRC>(src, e);
-        float v[kVec];
-        if (FIRST) {
+    constexpr int W = kWidth<SRC, DST>, R = W * kThreads, U = kPiece / R;
+    const int e = threadIdx.x * W;
+    Raw<SRC, W> x[U];
+    Raw<DST, W> y[U];
+    auto load = [&](int u) {
+        x[u] = load_raw<SRC, W, NT>(src, e + u * R);
+        if (FIRST) y[u].clear();
+        else y[u] = load_raw<DST, W, NT>(dst, e + u * R);
+    };
+    auto add = [&](int u) {
+        Raw<DST, W> z;
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) v[k] = w * x.get(k);
-        } else {
-            const Raw<DST> y = load_tile<DST>(dst, e);
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) v[k] = fmaf(w, x.get(k), y.get(k));
+        for (int k = 0; k < W; ++k) {
+            z.set(k, FIRST ? w * x[u].get(k) : fmaf(w, x[u].get(k), y[u].get(k)));
+            if (KIND) n.add(z.get(k));               // what a pass over dst would read
         }
-        if (KIND)
+        store_raw<DST, W, NT>(dst, e + u * R, z);
+    };
+    if (count == kPiece) {
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) n.add(stored(v[k]));
-        store_tile<DST>(dst, e, v);
+        for (int u = 0; u < U; ++u) load(u);
+#pragma unroll
+        for (int u = 0; u < U; ++u) add(u);
+        return;
     }
-    for (int end = e + kVec; e < end && e < count; ++e) {
-        const float x = load_one<SRC>(src, e);
-        const float v = FIRST ? w * x : fmaf(w, x, load_one<DST>(dst, e));
-        if (KIND) n.add(stored(v));
-        store_one<DST>(dst, e, v);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (e + u * R + W <= count) load(u);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (e + u * R + W <= count) add(u);
+    const int t = count / W * W + threadIdx.x;
+    if (t < count) {
+        const float a = load_one<SRC>(src, t);
+        const float v = FIRST ? w * a : fmaf(w, a, load_one<DST>(dst, t));
+        store_one<DST>(dst, t, v);
+        if (KIND) {
+            Raw<DST, 4> z;                           // v as stored
+            z.set(0, v);
+            n.add(z.get(0));
+        }
     }
 }
 
 template <int KIND, bool FIRST>
 __global__ void __launch_bounds__(kThreads)
-tensor_accumulate_kernel(const Chunk* __restrict__ chunks, float w, double* __restrict__ part) {
-    const Chunk c = chunks[blockIdx.x];
+tensor_accumulate_kernel(const Piece* __restrict__ pieces, void* const* __restrict__ dsts, float w,
+                         double* __restrict__ part) {
+    const Piece p = pieces[blockIdx.x];
+    void* dst = dsts[blockIdx.x];
     Norm<KIND> n;
-    by_types(c, [&](auto s, auto d) {
-        chunk_accumulate<KIND, FIRST, decltype(s)::value, decltype(d)::value>(c.src, c.dst, c.count,
-                                                                             w, n);
+    by_type(p.src_dtype(), [&](auto s) {
+        by_type(p.dst_dtype(), [&](auto d) {
+            piece_accumulate<KIND, FIRST, decltype(s)::value, decltype(d)::value, true>(
+                p.src, dst, p.count(), w, n);
+        });
     });
     if (KIND) {
         const double v = block_join<KIND>(n.value());
@@ -354,6 +593,9 @@ tensor_accumulate_kernel(const Chunk* __restrict__ chunks, float w, double* __re
 // ------------------------------------------------------------- host --------
 inline bool valid_table_dtype(int32_t dt) { return valid_dtype(dt) || dt == ZERO_FP32; }
 inline int64_t dtype_bytes(int32_t dt) { return dt == ZERO_FP32 ? 4 : 2; }
+
+// Tensors of a plan: one launch finishes a norm for each.
+constexpr int64_t kMaxTensors = kMaxLaunchBlocks;
 
 struct Span {
     uintptr_t begin, end;
@@ -394,8 +636,18 @@ bool writable(const zero_tensor_entry* entries, int64_t n) {
     return true;
 }
 
+// More pieces than any memory holds whole tensors of, and few enough for every
+// size computed from them.
+constexpr int64_t kMaxPieces = int64_t(1) << 40;
+
+// Elements of a tensor's first piece: the others then begin at a multiple of
+// 128 bytes of the output.
+int64_t first_piece(const zero_tensor_entry& e) {
+    return kPiece - (int64_t)((uintptr_t)e.dst % 128) / dtype_bytes(e.dst_dtype);
+}
+
 int plan_sizes(const zero_tensor_entry* entries, int64_t n, zero_tensor_plan* plan) {
-    int64_t numel = 0, chunks = 0;
+    int64_t numel = 0, bytes = 0, pieces = 0, runs = 0, rests = 0;
     for (int64_t k = 0; k < n; ++k) {
         const zero_tensor_entry& e = entries[k];
         if (e.numel < 0 || !valid_table_dtype(e.src_dtype) || !valid_table_dtype(e.dst_dtype))
@@ -408,15 +660,25 @@ int plan_sizes(const zero_tensor_entry* entries, int64_t n, zero_tensor_plan* pl
         Span s;
         if (!span_of(e.src, e.numel, e.src_dtype, &s) || !span_of(e.dst, e.numel, e.dst_dtype, &s))
             return ZERO_ERANGE;
-        if (__builtin_add_overflow(numel, e.numel, &numel)) return ZERO_ERANGE;
-        chunks += (e.numel - 1) / kChunk + 1;
-        if (chunks > kMaxLaunchBlocks) return ZERO_ERANGE;
+        int64_t more = e.numel - std::min(e.numel, first_piece(e));
+        more = 1 + more / kPiece + (more % kPiece != 0);
+        if (more > kMaxPieces - pieces) return ZERO_ERANGE;
+        pieces += more;
+        if (__builtin_add_overflow(numel, e.numel, &numel) ||
+            __builtin_add_overflow(bytes, e.numel * (dtype_bytes(e.src_dtype) + dtype_bytes(e.dst_dtype)),
+                                   &bytes))
+            return ZERO_ERANGE;
+        runs += e.numel / kRun;
+        rests += (e.numel % kRun + kPiece - 1) / kPiece;
     }
     plan->n_tensors = n;
     plan->numel = numel;
-    plan->n_chunks = chunks;
-    plan->chunk = kChunk;
-    plan->table_bytes = chunks * (int64_t)sizeof(Chunk) + (n + 1) * (int64_t)sizeof(int64_t);
+    plan->bytes = bytes;
+    plan->n_pieces = pieces;
+    plan->n_runs = runs;
+    plan->n_rests = rests;
+    plan->table_bytes = (pieces + runs + rests) * (int64_t)sizeof(Piece) +
+                        pieces * (int64_t)sizeof(void*) + 3 * (n + 1) * (int64_t)sizeof(int64_t);
     plan->writable = 0;
     plan->reserved = 0;
     return ZERO_OK;
@@ -424,15 +686,45 @@ int plan_sizes(const zero_tensor_entry* entries, int64_t n, zero_tensor_plan* pl
 
 // What a device call needs of a plan and its table.
 bool valid_plan(const zero_tensor_plan* p, const void* table) {
-    return p && p->n_tensors >= 0 && p->n_tensors < kMaxLaunchBlocks && p->n_chunks >= 0 &&
-           p->n_chunks <= kMaxLaunchBlocks && p->chunk > 0 && table && ((uintptr_t)table & 15) == 0;
+    return p && p->n_tensors >= 0 && p->n_tensors < kMaxTensors && p->n_pieces >= 0 &&
+           p->n_pieces <= kMaxPieces && p->n_runs >= 0 && p->n_rests >= 0 && p->n_runs <= p->n_pieces &&
+           p->n_rests <= p->n_pieces && table && ((uintptr_t)table & 15) == 0;
 }
 
-inline const int64_t* first_chunks(const zero_tensor_plan* p, const void* table) {
-    return (const int64_t*)((const char*)table + p->n_chunks * (int64_t)sizeof(Chunk));
+// The parts of a table, in its order: the norm's runs and rests, the pieces of
+// the passes that write and their outputs, and for every tensor (and the end)
+// its first run's partial, first rest's partial and first piece.
+const Piece* runs_of(const void* table) { return (const Piece*)table; }
+const Piece* pieces_of(const zero_tensor_plan* p, const void* table) {
+    return runs_of(table) + p->n_runs + p->n_rests;
+}
+void* const* dsts_of(const zero_tensor_plan* p, const void* table) {
+    return (void* const*)(pieces_of(p, table) + p->n_pieces);
+}
+const int64_t* first_runs_of(const zero_tensor_plan* p, const void* table) {
+    return (const int64_t*)(dsts_of(p, table) + p->n_pieces);
+}
+const int64_t* first_rests_of(const zero_tensor_plan* p, const void* table) {
+    return first_runs_of(p, table) + p->n_tensors + 1;
+}
+const int64_t* first_pieces_of(const zero_tensor_plan* p, const void* table) {
+    return first_rests_of(p, table) + p->n_tensors + 1;
 }
 
-inline int64_t folds(int64_t chunks) { return chunks <= kFinal ? 0 : (chunks + kFold - 1) / kFold; }
+// Partials that the finishing block takes as they are; more are folded first.
+constexpr int64_t kFinish = 2 * kInFlight * kFinishThreads;
+int64_t fold_blocks(int64_t n) { return n <= kFinish ? 0 : (n + kFoldEach - 1) / kFoldEach; }
+
+// Runs `blocks` blocks as launches of at most kMaxLaunchBlocks, in order:
+// go(first block, blocks).
+template <typename F>
+int in_launches(int64_t blocks, F&& go) {
+    for (int64_t b = 0; b < blocks; b += kMaxLaunchBlocks) {
+        const int rc = go(b, std::min(kMaxLaunchBlocks, blocks - b));
+        if (rc != ZERO_OK) return rc;
+    }
+    return ZERO_OK;
+}
 
 int norm_args(const zero_tensor_plan* plan, const void* table, int32_t kind, float inv_scale,
               const zero_step_control* ctl, const zero_step_result* res, const void* workspace,
@@ -444,43 +736,106 @@ int norm_args(const zero_tensor_plan* plan, const void* table, int32_t kind, flo
     return ZERO_OK;
 }
 
-// Joins the chunk partials at the workspace's start into *res and norms.
+// Joins the n partials at the workspace's start into *res and norms.
 template <int KIND>
-int finish(const zero_tensor_plan* plan, const void* table, float inv_scale,
+int finish(int64_t n, const int64_t* first, const int64_t* first2, int64_t n_tensors, float inv_scale,
            const zero_step_control* ctl, int32_t accumulate, zero_step_result* res, float* norms,
            double* part, hipStream_t stream) {
     const double* last = part;
-    int64_t n = plan->n_chunks;
-    if (const int64_t blocks = folds(n)) {
+    const int64_t nt = norms ? n_tensors : 0;
+    const bool wide = n / 1024 > nt;                  // a block for each tensor, or a wave
+    if (const int64_t blocks = fold_blocks(n)) {
         const int rc = launch(tensor_fold_kernel<KIND>, blocks, 0, stream, part, n, part + n);
         if (rc != ZERO_OK) return rc;
         last = part + n;
         n = blocks;
     }
-    return launch(tensor_finish_kernel<KIND>, 1 + (norms ? plan->n_tensors : 0), 0, stream, last, n,
-                  part, first_chunks(plan, table), inv_scale, ctl, (int)(accumulate != 0), res, norms);
+    const auto kernel = wide ? tensor_finish_kernel<KIND, kFinishThreads>
+                             : tensor_finish_kernel<KIND, 64>;
+    const int64_t each = wide ? 1 : kFinishThreads / 64;
+    return launch_shape(kernel, 1 + (nt + each - 1) / each, kFinishThreads, 0u, stream, last, n, part,
+                        first, first2, nt, inv_scale, ctl, (int)(accumulate != 0), res, norms);
+}
+
+// Whether the norm's calls of a plan take one block.
+bool one_block(const zero_tensor_plan* p) { return p->n_runs == 0 && p->n_rests <= kOneBlock; }
+
+template <int KIND, bool CLIP>
+int one_block_impl(const zero_tensor_plan* plan, const void* table, float max_norm,
+                   int32_t per_tensor, float inv_scale, const zero_step_control* ctl,
+                   int32_t accumulate, zero_step_result* res, float* norms, hipStream_t stream) {
+    return launch_shape(tensor_one_block_kernel<KIND, CLIP>, 1, kFinishThreads, 0u, stream,
+                        runs_of(table), (int)plan->n_rests, pieces_of(plan, table),
+                        dsts_of(plan, table), (int)plan->n_pieces, first_rests_of(plan, table),
+                        plan->n_tensors, max_norm, (int)(per_tensor != 0), inv_scale, ctl,
+                        (int)(accumulate != 0), res, norms);
+}
+
+// The partials of the norm, runs first.
+template <int KIND>
+int partials_impl(const zero_tensor_plan* plan, const void* table, double* part, hipStream_t stream) {
+    const int64_t n_runs = plan->n_runs, n_rests = plan->n_rests;
+    return in_launches(n_runs + (n_rests + kWaves - 1) / kWaves, [&](int64_t b, int64_t grid) {
+        return launch(tensor_norm_kernel<KIND>, grid, 0, stream, runs_of(table), n_runs, n_rests, b,
+                      part);
+    });
 }
 
 template <int KIND>
 int norm_impl(const zero_tensor_plan* plan, const void* table, float inv_scale,
               const zero_step_control* ctl, int32_t accumulate, zero_step_result* res, float* norms,
               double* part, hipStream_t stream) {
-    if (plan->n_chunks > 0) {
-        const int rc = launch(tensor_norm_kernel<KIND>, plan->n_chunks, 0, stream,
-                              (const Chunk*)table, part);
+    if (one_block(plan))
+        return one_block_impl<KIND, false>(plan, table, 0.0f, 0, inv_scale, ctl, accumulate, res, norms,
+                                           stream);
+    const int rc = partials_impl<KIND>(plan, table, part, stream);
+    if (rc != ZERO_OK) return rc;
+    return finish<KIND>(plan->n_runs + plan->n_rests, first_runs_of(plan, table),
+                        first_rests_of(plan, table), plan->n_tensors, inv_scale, ctl, accumulate, res,
+                        norms, part, stream);
+}
+
+// Whether a table is larger than the last-level cache (256 MB): the inputs of a
+// clip then do not stay in it.
+bool streams(const zero_tensor_plan* p) { return p->bytes > int64_t(256) << 20; }
+
+int clip_impl(const zero_tensor_plan* plan, const void* table, float max_norm,
+              const zero_step_result* res, const float* norms, hipStream_t stream) {
+    const auto kernel = streams(plan) ? tensor_clip_kernel<true> : tensor_clip_kernel<false>;
+    return in_launches(plan->n_pieces, [&](int64_t b, int64_t grid) {
+        return launch(kernel, grid, lds_for_blocks(kClipBlocksPerCU), stream, pieces_of(plan, table) + b,
+                      dsts_of(plan, table) + b, max_norm, res, norms);
+    });
+}
+
+template <int KIND>
+int clip_norm_impl(const zero_tensor_plan* plan, const void* table, float max_norm, float inv_scale,
+                   const zero_step_control* ctl, zero_step_result* res, float* norms,
+                   int32_t per_tensor, double* part, hipStream_t stream) {
+    if (one_block(plan))
+        return one_block_impl<KIND, true>(plan, table, max_norm, per_tensor, inv_scale, ctl, 0, res,
+                                          norms, stream);
+    const int64_t n = plan->n_runs + plan->n_rests;
+    if (!norms && n <= kJoinPartials) {
+        const int rc = partials_impl<KIND>(plan, table, part, stream);
         if (rc != ZERO_OK) return rc;
+        return launch(tensor_join_clip_kernel<KIND>, plan->n_pieces, 0, stream, pieces_of(plan, table),
+                      dsts_of(plan, table), max_norm, part, (int)n, inv_scale, ctl, res);
     }
-    return finish<KIND>(plan, table, inv_scale, ctl, accumulate, res, norms, part, stream);
+    const int rc = norm_impl<KIND>(plan, table, inv_scale, ctl, 0, res, norms, part, stream);
+    if (rc != ZERO_OK) return rc;
+    return clip_impl(plan, table, max_norm, res, per_tensor ? norms : nullptr, stream);
 }
 
 template <int KIND>
 int accumulate_impl(const zero_tensor_plan* plan, const void* table, float weight,
                     int32_t overwrite, double* part, hipStream_t stream) {
-    if (plan->n_chunks == 0) return ZERO_OK;
-    return overwrite ? launch(tensor_accumulate_kernel<KIND, true>, plan->n_chunks, 0, stream,
-                              (const Chunk*)table, weight, part)
-                     : launch(tensor_accumulate_kernel<KIND, false>, plan->n_chunks, 0, stream,
-                              (const Chunk*)table, weight, part);
+    const auto kernel = overwrite ? tensor_accumulate_kernel<KIND, true>
+                                  : tensor_accumulate_kernel<KIND, false>;
+    return in_launches(plan->n_pieces, [&](int64_t b, int64_t grid) {
+        return launch(kernel, grid, lds_for_blocks(kAddBlocksPerCU), stream, pieces_of(plan, table) + b, dsts_of(plan, table) + b, weight,
+                      part + b);
+    });
 }
 
 }  // namespace
@@ -490,7 +845,7 @@ extern "C" {
 int zero_tensor_plan_init(const zero_tensor_entry* entries, int64_t n_tensors,
                           zero_tensor_plan* plan) {
     if (!plan || n_tensors < 0 || (n_tensors > 0 && !entries)) return ZERO_EINVAL;
-    if (n_tensors >= kMaxLaunchBlocks) return ZERO_ERANGE;
+    if (n_tensors >= kMaxTensors) return ZERO_ERANGE;
     const int rc = plan_sizes(entries, n_tensors, plan);
     if (rc != ZERO_OK) return rc;
     try {
@@ -507,31 +862,51 @@ int zero_tensor_plan_table(const zero_tensor_entry* entries, const zero_tensor_p
     zero_tensor_plan again;
     const int rc = plan_sizes(entries, plan->n_tensors, &again);
     if (rc != ZERO_OK) return rc;
-    if (again.n_chunks != plan->n_chunks || again.chunk != plan->chunk) return ZERO_EINVAL;
-    Chunk* c = (Chunk*)table;
-    int64_t* first = (int64_t*)((char*)table + plan->n_chunks * (int64_t)sizeof(Chunk));
-    int64_t at = 0;
+    if (again.n_pieces != plan->n_pieces || again.n_runs != plan->n_runs ||
+        again.n_rests != plan->n_rests)
+        return ZERO_EINVAL;
+    Piece* run = (Piece*)runs_of(table);
+    Piece* rest = run + plan->n_runs;
+    Piece* piece = (Piece*)pieces_of(plan, table);
+    void** dst = (void**)dsts_of(plan, table);
+    int64_t* first_run = (int64_t*)first_runs_of(plan, table);
+    int64_t* first_rest = (int64_t*)first_rests_of(plan, table);
+    int64_t* first_of_pieces = (int64_t*)first_pieces_of(plan, table);
+    auto part = [](const zero_tensor_entry& e, int64_t k, int64_t begin, int64_t count) {
+        Piece p;
+        p.src = (const char*)e.src + begin * dtype_bytes(e.src_dtype);
+        p.tensor = (int32_t)k;
+        p.info = (uint32_t)count | (uint32_t)e.src_dtype << 24 | (uint32_t)e.dst_dtype << 28;
+        return p;
+    };
+    int64_t r = 0, t = 0, q = 0;
     for (int64_t k = 0; k < plan->n_tensors; ++k) {
         const zero_tensor_entry& e = entries[k];
-        first[k] = at;
-        for (int64_t b = 0; b < e.numel; b += plan->chunk) {
-            Chunk& r = c[at++];
-            r.src = (const char*)e.src + b * dtype_bytes(e.src_dtype);
-            r.dst = (char*)e.dst + b * dtype_bytes(e.dst_dtype);
-            r.count = (int32_t)std::min(plan->chunk, e.numel - b);
-            r.tensor = (int32_t)k;
-            r.src_dtype = e.src_dtype;
-            r.dst_dtype = e.dst_dtype;
+        first_run[k] = r;
+        first_rest[k] = plan->n_runs + t;
+        first_of_pieces[k] = q;
+        int64_t b = 0;
+        for (; e.numel - b >= kRun; b += kRun) run[r++] = part(e, k, b, kRun);
+        for (; b < e.numel; b += kPiece)
+            rest[t++] = part(e, k, b, std::min((int64_t)kPiece, e.numel - b));
+        b = 0;
+        for (int64_t c; b < e.numel; b += c, ++q) {
+            c = std::min(b == 0 ? first_piece(e) : (int64_t)kPiece, e.numel - b);
+            piece[q] = part(e, k, b, c);
+            dst[q] = (char*)e.dst + b * dtype_bytes(e.dst_dtype);
         }
     }
-    first[plan->n_tensors] = at;
+    first_run[plan->n_tensors] = r;
+    first_rest[plan->n_tensors] = plan->n_runs + t;
+    first_of_pieces[plan->n_tensors] = q;
     return ZERO_OK;
 }
 
 size_t zero_tensor_workspace_bytes(const zero_tensor_plan* plan) {
-    if (!plan || plan->n_chunks < 0) return 0;
-    const size_t partials = (size_t)(plan->n_chunks + folds(plan->n_chunks));
-    return std::max<size_t>(2, partials) * sizeof(double);
+    if (!plan || plan->n_pieces < 0 || plan->n_pieces > kMaxPieces) return 0;
+    // a tensor has at least as many pieces as runs and rests
+    const int64_t n = plan->n_pieces;
+    return (size_t)std::max<int64_t>(2, n + fold_blocks(n)) * sizeof(double);
 }
 
 int zero_tensor_norm(const zero_tensor_plan* plan, const void* table, int32_t kind,
@@ -550,9 +925,7 @@ int zero_tensor_clip(const zero_tensor_plan* plan, const void* table, float max_
                      const zero_step_result* res, const float* norms, hipStream_t stream) {
     if (!valid_plan(plan, table) || !plan->writable || !res || max_norm != max_norm)
         return ZERO_EINVAL;
-    if (plan->n_chunks == 0) return ZERO_OK;
-    return launch(tensor_clip_kernel, plan->n_chunks, 0, stream, (const Chunk*)table, max_norm, res,
-                  norms);
+    return clip_impl(plan, table, max_norm, res, norms, stream);
 }
 
 int zero_tensor_clip_norm(const zero_tensor_plan* plan, const void* table, int32_t kind,
@@ -562,10 +935,14 @@ int zero_tensor_clip_norm(const zero_tensor_plan* plan, const void* table, int32
     if (!valid_plan(plan, table) || !plan->writable || max_norm != max_norm ||
         (per_tensor && !norms && plan->n_tensors > 0))
         return ZERO_EINVAL;
-    const int rc = zero_tensor_norm(plan, table, kind, inv_scale, ctl, res, norms, workspace,
-                                    workspace_bytes, 0, stream);
+    const int rc = norm_args(plan, table, kind, inv_scale, ctl, res, workspace, workspace_bytes);
     if (rc != ZERO_OK) return rc;
-    return zero_tensor_clip(plan, table, max_norm, res, per_tensor ? norms : nullptr, stream);
+    double* part = (double*)workspace;
+    return kind == ZERO_NORM_L2
+               ? clip_norm_impl<ZERO_NORM_L2>(plan, table, max_norm, inv_scale, ctl, res, norms,
+                                              per_tensor, part, stream)
+               : clip_norm_impl<ZERO_NORM_MAX>(plan, table, max_norm, inv_scale, ctl, res, norms,
+                                               per_tensor, part, stream);
 }
 
 int zero_tensor_accumulate(const zero_tensor_plan* plan, const void* table, float weight,
@@ -586,11 +963,13 @@ int zero_tensor_accumulate_norm(const zero_tensor_plan* plan, const void* table,
     if (kind == ZERO_NORM_L2) {
         rc = accumulate_impl<ZERO_NORM_L2>(plan, table, weight, overwrite, part, stream);
         if (rc != ZERO_OK) return rc;
-        return finish<ZERO_NORM_L2>(plan, table, inv_scale, ctl, accumulate, res, norms, part, stream);
+        return finish<ZERO_NORM_L2>(plan->n_pieces, first_pieces_of(plan, table), nullptr,
+                                    plan->n_tensors, inv_scale, ctl, accumulate, res, norms, part, stream);
     }
     rc = accumulate_impl<ZERO_NORM_MAX>(plan, table, weight, overwrite, part, stream);
     if (rc != ZERO_OK) return rc;
-    return finish<ZERO_NORM_MAX>(plan, table, inv_scale, ctl, accumulate, res, norms, part, stream);
+    return finish<ZERO_NORM_MAX>(plan->n_pieces, first_pieces_of(plan, table), nullptr,
+                                    plan->n_tensors, inv_scale, ctl, accumulate, res, norms, part, stream);
 }
 
 }  // extern "C"
