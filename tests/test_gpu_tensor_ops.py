@@ -142,10 +142,12 @@ def test_norm_mixed_types_and_empty_tables(kind):
 
 
 @pytest.mark.parametrize("kind", ["l2", "max"])
-def test_norm_of_20000_tensors(kind):
-    """More pieces than one block joins; half of them empty or of one element."""
+@pytest.mark.parametrize("count", [40000, 60000])
+def test_norm_of_many_tensors(kind, count):
+    """At 60000 more partials than one block joins; half of the tensors empty or of
+    one element."""
     rng = np.random.default_rng(5)
-    sizes = [int(n) for n in rng.choice([0, 1, 3, 40], 40000)]
+    sizes = [int(n) for n in rng.choice([0, 1, 3, 40], count)]
     flat = torch.empty(sum(sizes), dtype=HALF, device="cuda").normal_(
         generator=torch.Generator(device="cuda").manual_seed(3))
     tensors = list(flat.split(sizes))
@@ -288,8 +290,9 @@ def test_clip_rounds_to_nearest_even_and_to_inf():
 @pytest.mark.parametrize("in_place", [False, True])
 def test_clip_norm_is_norm_then_clip(kind, per_tensor, in_place):
     """The fused call gives the two calls' bits, at few pieces and many."""
-    for sizes in ([], [0], [3], [4096, 70, 1, 0, 9], SIZES, [30000] * 40, [5] * 17000,
-                  [1 << 22, (1 << 21) + 3, 77]):
+    for sizes in ([], [0], [3], [4096, 70, 1, 0, 9], [4096] * 4, [4097] * 4, [3] * 5, [100] * 16,
+                  [100] * 17, [16384], SIZES, [30000] * 40, [5] * 17000, [4096] * 1024,
+                  [16384] * 1025, [1 << 22, (1 << 21) + 3, 77]):
         types = [(F32, BF, HALF)[k % 3] for k in range(len(sizes))]
         s = Set(sizes[:64], types[:64], [k % 8 for k in range(64)], seed=10)
         tensors = s.t

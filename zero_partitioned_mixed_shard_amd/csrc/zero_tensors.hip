@@ -478,8 +478,10 @@ tensor_join_clip_kernel(const Piece* __restrict__ pieces, void* const* __restric
 }
 
 // Norm, each tensor's norm and (CLIP) the clip of a table of at most kOneBlock
-// rests and no run, in one block: one launch instead of two or three.
-constexpr int kOneBlock = 16;
+// rests and no run, in one block, which joins in the order of
+// tensor_finish_kernel (a wave's tree over at most 64 partials), so to the same
+// bits.
+constexpr int kOneBlock = kFinishThreads / 64;       // a wave for each rest
 template <int KIND, bool CLIP>
 __global__ void __launch_bounds__(kFinishThreads)
 tensor_one_block_kernel(const Piece* __restrict__ rests, int n_rests,
@@ -487,8 +489,7 @@ tensor_one_block_kernel(const Piece* __restrict__ rests, int n_rests,
                         const int64_t* __restrict__ first, int64_t n_tensors, float max_norm,
                         int per_tensor, float inv_scale, const zero_step_control* __restrict__ ctl,
                         int accumulate, zero_step_result* res, float* __restrict__ norms) {
-    __shared__ double part[kOneBlock];
-    static_assert(kOneBlock == kFinishThreads / 64, "a wave for each rest");
+    __shared__ double part[64];
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     double v = 0.0;
     if (w < n_rests) {
@@ -501,18 +502,19 @@ tensor_one_block_kernel(const Piece* __restrict__ rests, int n_rests,
     if (lane == 0) part[w] = v;
     const float inv = ctl ? ctl->inv_scale : inv_scale;
     __syncthreads();
-    v = part[0];
-#pragma unroll
-    for (int k = 1; k < kOneBlock; ++k) v = join<KIND>(v, part[k]);
-    const zero_step_result r = result_of<KIND>(v, inv);
-    if (threadIdx.x == 0) store_result<KIND>(r, accumulate, res);
-    auto norm_of = [&](int64_t t) {
-        double x = 0.0;
-        for (int64_t j = first[t]; j < first[t + 1]; ++j) x = join<KIND>(x, part[j]);
-        return tensor_norm<KIND>(x, inv);
+    auto joined = [&](int a, int n) {                 // by a whole wave
+        return wave_join<KIND>(lane < n ? part[a + lane] : 0.0);
     };
+    auto norm_of = [&](int64_t t) {
+        return tensor_norm<KIND>(joined((int)first[t], (int)(first[t + 1] - first[t])), inv);
+    };
+    const zero_step_result r = result_of<KIND>(joined(0, n_rests), inv);
+    if (threadIdx.x == 0) store_result<KIND>(r, accumulate, res);
     if (norms)
-        for (int64_t t = threadIdx.x; t < n_tensors; t += kFinishThreads) norms[t] = norm_of(t);
+        for (int64_t t = w; t < n_tensors; t += kFinishThreads / 64) {
+            const float x = norm_of(t);
+            if (lane == 0) norms[t] = x;
+        }
     if (!CLIP || r.overflow) return;
     for (int k = 0; k < n_pieces; ++k) {
         const Piece p = pieces[k];
@@ -757,8 +759,11 @@ int finish(int64_t n, const int64_t* first, const int64_t* first2, int64_t n_ten
                         first, first2, nt, inv_scale, ctl, (int)(accumulate != 0), res, norms);
 }
 
-// Whether the norm's calls of a plan take one block.
+// Whether a table's norm takes one block, and its norm and clip together (which
+// that block then does one piece after the other).
+constexpr int kOneBlockPieces = 4;
 bool one_block(const zero_tensor_plan* p) { return p->n_runs == 0 && p->n_rests <= kOneBlock; }
+bool one_block_clip(const zero_tensor_plan* p) { return one_block(p) && p->n_pieces <= kOneBlockPieces; }
 
 template <int KIND, bool CLIP>
 int one_block_impl(const zero_tensor_plan* plan, const void* table, float max_norm,
@@ -812,7 +817,7 @@ template <int KIND>
 int clip_norm_impl(const zero_tensor_plan* plan, const void* table, float max_norm, float inv_scale,
                    const zero_step_control* ctl, zero_step_result* res, float* norms,
                    int32_t per_tensor, double* part, hipStream_t stream) {
-    if (one_block(plan))
+    if (one_block_clip(plan))
         return one_block_impl<KIND, true>(plan, table, max_norm, per_tensor, inv_scale, ctl, 0, res,
                                           norms, stream);
     const int64_t n = plan->n_runs + plan->n_rests;
