@@ -61,8 +61,7 @@ enum zero_status {
     ZERO_OK = 0,
     ZERO_EINVAL = -1,  /* bad argument: null pointer, negative size, unknown dtype ... */
     ZERO_ERANGE = -2,  /* a size or offset overflows int64                              */
-    ZERO_EDEVICE = -3, /* a HIP launch failed                                           */
-    ZERO_ENOMEM = -4   /* host memory ran out (zero_tensor_plan_init only)              */
+    ZERO_EDEVICE = -3  /* a HIP launch failed                                           */
 };
 
 enum zero_dtype {
@@ -490,7 +489,8 @@ enum zero_norm_kind {
  * and the plan is not writable.
  * Errors: ZERO_EINVAL for a NULL argument, a negative count, an unknown type, a
  * NULL or misaligned pointer with a nonzero numel; ZERO_ERANGE for addresses or
- * sizes that overflow, or over 16,777,214 tensors; ZERO_ENOMEM. */
+ * sizes that overflow, over 16,777,214 tensors, or a list of the outputs' addresses
+ * that host memory does not hold. */
 int zero_tensor_plan_init(const zero_tensor_entry* entries, int64_t n_tensors,
                           zero_tensor_plan* plan);
 
@@ -517,7 +517,7 @@ size_t zero_tensor_workspace_bytes(const zero_tensor_plan* plan);
  * the norm, so zero_adamw_step and zero_tensor_clip clip by that norm.  With
  * accumulate != 0, *res is joined with what it held (L2: the sum; MAX: the
  * larger; the flags ORed), so several tables checked in turn on one stream give
- * one result.  The order of every sum is fixed by the plan.  With the flag set,
+ * one result.  The order of every sum goes by the numbers of elements alone.  With the flag set,
  * sumsq and the norms of the tensors concerned are inf or NaN.
  *   table      device, the plan's table
  *   ctl        device zero_step_control, or NULL
@@ -526,6 +526,7 @@ size_t zero_tensor_workspace_bytes(const zero_tensor_plan* plan);
  *   workspace  device scratch of zero_tensor_workspace_bytes(plan), 8-byte
  *              aligned; needs no initialisation, not shared by calls that may
  *              overlap
+ * res, norms and workspace overlap neither each other nor the tensors.
  * Errors: ZERO_EINVAL for NULL pointers, an unknown kind, an inv_scale (without
  * ctl) not finite and > 0, a small or misaligned workspace. */
 int zero_tensor_norm(const zero_tensor_plan* plan, const void* table, int32_t kind,
@@ -563,8 +564,8 @@ int zero_tensor_accumulate(const zero_tensor_plan* plan, const void* table, floa
                            int32_t overwrite, hipStream_t stream);
 
 /* zero_tensor_accumulate and, in the same pass, zero_tensor_norm of the y that
- * it stores (the last micro-batch of a step).  Arguments and errors as
- * theirs. */
+ * it stores (the last micro-batch of a step; the order of its sums goes by the
+ * outputs' addresses too).  Arguments and errors as theirs. */
 int zero_tensor_accumulate_norm(const zero_tensor_plan* plan, const void* table, float weight,
                                 int32_t overwrite, int32_t kind, float inv_scale,
                                 const zero_step_control* ctl, zero_step_result* res, float* norms,

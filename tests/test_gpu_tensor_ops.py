@@ -448,6 +448,7 @@ def test_dense_permutations_and_refusals():
                  lambda: Z.zero_tensor_norm(plan, 1.0, res, workspace(plan), norms=flat[:0]),
                  lambda: Z.zero_tensor_clip(plan, 1.0, res, norms=flat[::2]),
                  lambda: Z.zero_tensor_accumulate(plan, norms=flat),
+                 lambda: Z.zero_tensor_accumulate(plan, accumulate=True),
                  lambda: Z.zero_tensor_accumulate(plan, res=res),
                  lambda: Z.zero_tensor_clip_norm(plan, 1.0, 1.0, res, workspace(plan),
                                                  per_tensor=True)):

@@ -19,7 +19,7 @@ import numpy as np
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libzero_shard.so")
 
-ZERO_OK, ZERO_EINVAL, ZERO_ERANGE, ZERO_EDEVICE, ZERO_ENOMEM = 0, -1, -2, -3, -4
+ZERO_OK, ZERO_EINVAL, ZERO_ERANGE, ZERO_EDEVICE = 0, -1, -2, -3
 ZERO_FP16, ZERO_BF16, ZERO_FP32 = 1, 2, 3
 ZERO_NORM_L2, ZERO_NORM_MAX = 1, 2
 ZERO_MAX_RANKS = 16

@@ -1136,7 +1136,6 @@ const char* zero_status_str(int status) {
         case ZERO_EINVAL: return "invalid argument";
         case ZERO_ERANGE: return "size out of range";
         case ZERO_EDEVICE: return "device launch failed";
-        case ZERO_ENOMEM: return "out of host memory";
         default: return "unknown status";
     }
 }

@@ -17,8 +17,8 @@
 // Numerics: the squares and their sums are fp64 (the square of an fp32 value
 // is exact there, and the sum cannot overflow), the unscale factor is applied
 // to the sum; products and sums of the other calls are fp32, rounded to the
-// output's type once.  Sums are folded in a fixed order: the same plan gives
-// the same bits every time.
+// output's type once.  Sums are folded in a fixed order, which for the norm goes
+// by the tensors' numbers of elements alone.
 
 #include <math.h>
 
@@ -856,7 +856,7 @@ int zero_tensor_plan_init(const zero_tensor_entry* entries, int64_t n_tensors,
     try {
         plan->writable = writable(entries, n_tensors) ? 1 : 0;
     } catch (const std::bad_alloc&) {
-        return ZERO_ENOMEM;
+        return ZERO_ERANGE;
     }
     return ZERO_OK;
 }

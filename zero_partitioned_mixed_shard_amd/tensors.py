@@ -217,7 +217,7 @@ def zero_tensor_accumulate(plan: zero_tensor_plan, weight: float = 1.0, overwrit
     """out = out + weight * tensor (overwrite: out = weight * tensor); with res
     and workspace also the norm of out, in the same pass."""
     if res is None:
-        if norms is not None or workspace is not None or ctl_dev is not None:
+        if norms is not None or workspace is not None or ctl_dev is not None or accumulate:
             raise ValueError("the norm needs res and workspace")
         plan._call(_lib.zero_tensor_accumulate, (float(weight), int(bool(overwrite))), stream)
         return
