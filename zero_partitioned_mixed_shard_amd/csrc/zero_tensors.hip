@@ -42,12 +42,28 @@ struct Piece {
 };
 static_assert(sizeof(Piece) == 16, "one scalar load");
 
-// Elements of a whole piece of the passes that write, and of a rest.
+// Elements of a whole piece of the passes that write, and of a rest: with one
+// 16-byte access per lane and row, a block has all of a piece in flight.
+// 16384-element pieces ran at 5.3 TB/s where these run at 6.2 (accumulation of
+// 9.4e8 bf16 into fp32: 1770 and 1506 us); with 4096 elements as four blocks to a
+// larger record the tables of many small tensors were 15-20 % slower.
 constexpr int kPiece = 4096;
-// Elements of a run.
+// Elements of a run of the norm: 4096-element pieces, a wave each, read 6.7e9 bf16
+// at 6.73 TB/s, runs by whole blocks at 6.97 (and 10,000 ragged tensors at 6.56
+// with rests by waves, 6.37 by blocks).
 constexpr int kRun = 16384;
+// Consecutive units an XCD gets of each: 6.97 -> 7.12 TB/s at 8 for the norm of
+// 6.7e9 bf16 (2 to 4: 6.83); 4.29 -> 4.37 at 32 for norm and clip of 9.4e8 fp16
+// (2 to 8: 4.16-4.22).
+constexpr int kRunGroup = 8, kPieceGroup = 32;
+// Resident blocks per CU (lds_for_blocks).  Norm: 5 read 6.7e9 bf16 0.5 % faster
+// than 8 and a mixed-type table 1.5 %; 4 another 0.7 %, but 10,000 ragged tensors
+// 1 % slower.  Clip: 9.4e8 bf16 in place take 564 us at 5, 589 at 4, 585 at 8.
+// Accumulation: 9.4e8 bf16 into fp32 take 1489 us at 3, 1432-1452 at 2, 1517 at
+// 4, 1571 at 8; fp16 into fp16 12-15 % more at 2 than at 3.
+constexpr int kNormBlocksPerCU = 5, kClipBlocksPerCU = 5, kAddBlocksPerCU = 3;
 // Loads of 16 bytes that a lane has in flight in the norm of a run, and of a
-// rest.
+// rest (8 for the runs: 1 % slower; 4 for the rests: the same).
 constexpr int kRunLoads = 4, kRestLoads = 8;
 constexpr int kWaves = kThreads / 64;
 
@@ -148,6 +164,21 @@ template <int DT>
 __device__ __forceinline__ void store_one(void* p, int e, float v) {
     if constexpr (DT == ZERO_FP32) ((g_f32*)p)[e] = v;
     else ((g_u16*)p)[e] = narrow<DT>(v);
+}
+
+// The unit of work of block b of n: workgroups go to the 8 XCDs in turn, so blocks
+// b, b + 8, ... of a group of 8 G share an XCD, and get G consecutive units.  The
+// records of those then come from that XCD's L2 (handed out in order, every
+// 128-byte line of records went to all 8: 3 % more bytes read by the clip) and
+// the XCD reads memory in longer stretches.  Blocks past the last whole group
+// keep their own.
+template <int G>
+__device__ __forceinline__ int64_t unit_of(int64_t b, int64_t n) {
+    constexpr int64_t group = 8 * G;
+    const int64_t a = b & ~(group - 1);
+    if (a + group > n) return b;
+    const int64_t r = b - a;
+    return a + (r & 7) * G + (r >> 3);
 }
 
 template <int V>
@@ -259,12 +290,13 @@ tensor_norm_kernel(const Piece* __restrict__ runs, int64_t n_runs, int64_t n_res
     const int64_t b = blk0 + blockIdx.x;
     double v = 0.0;
     if (b < n_runs) {
-        const Piece p = runs[b];
+        const int64_t i = unit_of<kRunGroup>(b, n_runs);
+        const Piece p = runs[i];
         by_type(p.src_dtype(), [&](auto s) {
             v = span_norm<KIND, decltype(s)::value, kThreads, kRunLoads, true>(p.src, kRun, threadIdx.x);
         });
         v = block_join<KIND>(v);
-        if (threadIdx.x == 0) part[b] = v;
+        if (threadIdx.x == 0) part[i] = v;
         return;
     }
     const int64_t i = (b - n_runs) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -377,9 +409,6 @@ __device__ __forceinline__ float clip_factor(float max_norm, double norm, float 
     return (float)(c * (double)inv);
 }
 
-// Resident blocks per CU of the passes that write.
-constexpr int kClipBlocksPerCU = 5, kAddBlocksPerCU = 3;
-
 // Elements per lane access of a pass that reads SRC and writes DST: 16 bytes of
 // the wider of the two.
 template <int SRC, int DST>
@@ -434,8 +463,9 @@ __global__ void __launch_bounds__(kThreads)
 tensor_clip_kernel(const Piece* __restrict__ pieces, void* const* __restrict__ dsts, float max_norm,
                    const zero_step_result* __restrict__ res, const float* __restrict__ norms) {
     if (res->overflow) return;                       // skipped step: write nothing
-    const Piece p = pieces[blockIdx.x];
-    scale_by_types<NT, kThreads>(p, dsts[blockIdx.x], [&] {
+    const int64_t i = unit_of<kPieceGroup>(blockIdx.x, gridDim.x);
+    const Piece p = pieces[i];
+    scale_by_types<NT, kThreads>(p, dsts[i], [&] {
         return clip_factor(max_norm, norms ? (double)norms[p.tensor] : sqrt(res->sumsq),
                            res->inv_scale);
     });
@@ -443,7 +473,9 @@ tensor_clip_kernel(const Piece* __restrict__ pieces, void* const* __restrict__ d
 
 // The clip right after the partials of a norm, at most kJoinPartials: every block
 // joins them itself (in the order of tensor_finish_kernel, so to the same
-// bits), which spares that launch; block 0 stores the result.
+// bits), which spares that launch; the block of piece 0 stores the result.
+// 60 tensors of 16384 fp32: 8.9 us against 12.0 with the launch; at 1000 of them
+// (1000 partials) 35.0 against 36.6.
 constexpr int kJoinPartials = 1024;
 static_assert(kJoinPartials == kFinishThreads && kJoinPartials % kThreads == 0,
               "the finishing block's one partial per thread");
@@ -453,8 +485,9 @@ tensor_join_clip_kernel(const Piece* __restrict__ pieces, void* const* __restric
                         float max_norm, const double* __restrict__ part, int n, float inv_scale,
                         const zero_step_control* __restrict__ ctl, zero_step_result* res) {
     __shared__ double joined[kJoinPartials / 64];
-    const Piece p = pieces[blockIdx.x];
-    scale_by_types<false, kThreads>(p, dsts[blockIdx.x], [&] {
+    const int64_t i = unit_of<kPieceGroup>(blockIdx.x, gridDim.x);
+    const Piece p = pieces[i];
+    scale_by_types<false, kThreads>(p, dsts[i], [&] {
         double x[kJoinPartials / kThreads];
 #pragma unroll
         for (int q = 0; q < kJoinPartials / kThreads; ++q) {
@@ -472,7 +505,7 @@ tensor_join_clip_kernel(const Piece* __restrict__ pieces, void* const* __restric
 #pragma unroll
         for (int k = 1; k < kJoinPartials / 64; ++k) v = join<KIND>(v, joined[k]);
         const zero_step_result r = result_of<KIND>(v, inv);
-        if (blockIdx.x == 0 && threadIdx.x == 0) *res = r;
+        if (i == 0 && threadIdx.x == 0) *res = r;
         return r.overflow ? NAN : clip_factor(max_norm, sqrt(r.sumsq), inv);
     });
 }
@@ -577,8 +610,9 @@ template <int KIND, bool FIRST>
 __global__ void __launch_bounds__(kThreads)
 tensor_accumulate_kernel(const Piece* __restrict__ pieces, void* const* __restrict__ dsts, float w,
                          double* __restrict__ part) {
-    const Piece p = pieces[blockIdx.x];
-    void* dst = dsts[blockIdx.x];
+    const int64_t i = unit_of<kPieceGroup>(blockIdx.x, gridDim.x);
+    const Piece p = pieces[i];
+    void* dst = dsts[i];
     Norm<KIND> n;
     by_type(p.src_dtype(), [&](auto s) {
         by_type(p.dst_dtype(), [&](auto d) {
@@ -588,7 +622,7 @@ tensor_accumulate_kernel(const Piece* __restrict__ pieces, void* const* __restri
     });
     if (KIND) {
         const double v = block_join<KIND>(n.value());
-        if (threadIdx.x == 0) part[blockIdx.x] = v;
+        if (threadIdx.x == 0) part[i] = v;
     }
 }
 
@@ -745,7 +779,9 @@ int finish(int64_t n, const int64_t* first, const int64_t* first2, int64_t n_ten
            double* part, hipStream_t stream) {
     const double* last = part;
     const int64_t nt = norms ? n_tensors : 0;
-    const bool wide = n / 1024 > nt;                  // a block for each tensor, or a wave
+    // a block for each tensor, or a wave: one tensor of 2.7e8 elements 84 us against
+    // 92, 32 of 6.7e7 624 against 631, the same where a tensor has fewer partials
+    const bool wide = n / 1024 > nt;
     if (const int64_t blocks = fold_blocks(n)) {
         const int rc = launch(tensor_fold_kernel<KIND>, blocks, 0, stream, part, n, part + n);
         if (rc != ZERO_OK) return rc;
@@ -759,8 +795,9 @@ int finish(int64_t n, const int64_t* first, const int64_t* first2, int64_t n_ten
                         first, first2, nt, inv_scale, ctl, (int)(accumulate != 0), res, norms);
 }
 
-// Whether a table's norm takes one block, and its norm and clip together (which
-// that block then does one piece after the other).
+// Whether a table's norm takes one block (16 tensors of 4096 fp32: 6.1 us against
+// 8.8 for two launches), and its norm and clip together, which that block does
+// one piece after the other (4: 6.6 us against 8.7, 8: 8.8, 16: 13.3 against 8.6).
 constexpr int kOneBlockPieces = 4;
 bool one_block(const zero_tensor_plan* p) { return p->n_runs == 0 && p->n_rests <= kOneBlock; }
 bool one_block_clip(const zero_tensor_plan* p) { return one_block(p) && p->n_pieces <= kOneBlockPieces; }
@@ -781,8 +818,8 @@ template <int KIND>
 int partials_impl(const zero_tensor_plan* plan, const void* table, double* part, hipStream_t stream) {
     const int64_t n_runs = plan->n_runs, n_rests = plan->n_rests;
     return in_launches(n_runs + (n_rests + kWaves - 1) / kWaves, [&](int64_t b, int64_t grid) {
-        return launch(tensor_norm_kernel<KIND>, grid, 0, stream, runs_of(table), n_runs, n_rests, b,
-                      part);
+        return launch(tensor_norm_kernel<KIND>, grid, lds_for_blocks(kNormBlocksPerCU), stream,
+                      runs_of(table), n_runs, n_rests, b, part);
     });
 }
 
@@ -800,8 +837,10 @@ int norm_impl(const zero_tensor_plan* plan, const void* table, float inv_scale,
                         norms, part, stream);
 }
 
-// Whether a table is larger than the last-level cache (256 MB): the inputs of a
-// clip then do not stay in it.
+// Whether a table is larger than the last-level cache (256 MB): the clip then
+// loads its inputs so that they do not stay in it.  Three tables in turn, of 202 MB
+// each: 36.1 us so, 31.5 us with plain loads; of 401 MB: 63.5 and 69.9; one of
+// 3.8 GB: 608 and 697.
 bool streams(const zero_tensor_plan* p) { return p->bytes > int64_t(256) << 20; }
 
 int clip_impl(const zero_tensor_plan* plan, const void* table, float max_norm,
