@@ -472,7 +472,8 @@ typedef struct zero_tensor_plan {
     int64_t n_pieces;    /* pieces that the passes that write work on         */
     int64_t n_runs;      /* pieces that the norm works on: whole ones         */
     int64_t n_rests;     /* and smaller ones at the tensors' ends             */
-    int64_t table_bytes; /* size of the device table                          */
+    int64_t head_bytes;  /* size of the device table's head, and of all of it */
+    int64_t table_bytes;
     int32_t writable;    /* 1: no output overlaps another output, nor an input
                             that is not its own in place; 0: the calls that
                             write refuse this plan (ZERO_EINVAL)              */
@@ -494,13 +495,16 @@ enum zero_norm_kind {
 int zero_tensor_plan_init(const zero_tensor_entry* entries, int64_t n_tensors,
                           zero_tensor_plan* plan);
 
-/* Writes the plan's table, plan->table_bytes bytes, 8-byte aligned, to host
- * memory; the caller copies it to device memory (16-byte aligned) and passes
- * that to the calls, for as long as the tensors stay where they are.
- * Errors: as zero_tensor_plan_init, and ZERO_EINVAL if the plan is not that of
- * these entries. */
-int zero_tensor_plan_table(const zero_tensor_entry* entries, const zero_tensor_plan* plan,
-                           void* table);
+/* Writes the head of the plan's table, plan->head_bytes bytes, to host memory
+ * (8-byte aligned).  The caller copies it to the beginning of plan->table_bytes
+ * bytes of device memory, 16-byte aligned, and zero_tensor_plan_expand writes the
+ * rest of the table there from it; the other calls are passed the whole table,
+ * for as long as the tensors stay where they are.
+ * Errors: head as zero_tensor_plan_init, and ZERO_EINVAL if the plan is not that
+ * of these entries; expand ZERO_EINVAL for NULL or a misaligned table. */
+int zero_tensor_plan_head(const zero_tensor_entry* entries, const zero_tensor_plan* plan,
+                          void* head);
+int zero_tensor_plan_expand(const zero_tensor_plan* plan, void* table, hipStream_t stream);
 
 /* Bytes of device workspace for the calls that take a norm: one 8-byte partial
  * for at most 4096 elements, plus one for 4096 of these where there are over

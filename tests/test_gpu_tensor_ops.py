@@ -108,6 +108,49 @@ def clip_want(x, norm, max_norm, inv):
     return x * (min(c, 1.0) * inv)
 
 
+# ------------------------------------------------------------------- table --
+@pytest.mark.parametrize("seed", range(6))
+def test_table_covers_every_element_once(seed):
+    """The expanded table against a plain cut of every tensor."""
+    rng = np.random.default_rng(seed)
+    count = [0, 1, 5, 40, 300, 3000][seed]
+    sizes = [int(n) for n in rng.choice([0, 1, 7, 4095, 4096, 4097, 16384, 16385, 70001], count)]
+    src, dst = ([(F32, HALF, BF)[k] for k in rng.integers(0, 3, count)] for _ in range(2))
+    flat = torch.zeros(4 * sum(sizes) + 64 * count + 8, dtype=torch.uint8, device="cuda")
+    outs, at = [], 0
+    for n, d in zip(sizes, dst):
+        at += int(rng.integers(0, 8)) * 4
+        outs.append(flat[at:at + n * d.itemsize].view(d))
+        at += -(-n * d.itemsize // 4) * 4
+    tensors = [torch.zeros(n, dtype=d, device="cuda") for n, d in zip(sizes, src)]
+    plan = Z.zero_tensor_plan(tensors, out=outs, device="cuda")
+    assert plan.c.writable == 1
+    code = {F32: Z.ZERO_FP32, HALF: Z.ZERO_FP16, BF: Z.ZERO_BF16}
+    runs, rests, pieces, dsts = [], [], [], []
+    for k, (t, o) in enumerate(zip(tensors, outs)):
+        def record(begin, n):
+            return (t.data_ptr() + begin * t.element_size(), k,
+                    n | code[t.dtype] << 24 | code[o.dtype] << 28)
+        n, b = t.numel(), 0
+        while n - b >= 16384:
+            runs.append(record(b, 16384))
+            b += 16384
+        rests += [record(a, min(4096, n - a)) for a in range(b, n, 4096)]
+        lead = o.data_ptr() % 128 // o.element_size()
+        b = 0
+        while b < n:
+            c = min(n - b, 4096 - (lead if b == 0 else 0))
+            pieces.append(record(b, c))
+            dsts.append(o.data_ptr() + b * o.element_size())
+            b += c
+    raw = plan.table.cpu().numpy()[plan.c.head_bytes:]
+    rec = np.dtype([("src", np.uint64), ("tensor", np.int32), ("info", np.uint32)])
+    every = np.array(runs + rests + pieces, dtype=rec)
+    assert (plan.c.n_runs, plan.c.n_rests, plan.c.n_pieces) == (len(runs), len(rests), len(pieces))
+    assert raw[:every.nbytes].tobytes() == every.tobytes()
+    assert raw[every.nbytes:].tobytes() == np.array(dsts, dtype=np.uint64).tobytes()
+
+
 # ------------------------------------------------------------------- norms --
 @pytest.mark.parametrize("kind", ["l2", "max"])
 @pytest.mark.parametrize("dt", [F32, HALF, BF])

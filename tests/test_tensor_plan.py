@@ -1,5 +1,5 @@
-"""Tensor-table plans on the CPU: sizes, the device table's contents, which
-plans may be written to, and the refusals of every zero_tensor_* call (no device
+"""Tensor-table plans on the CPU: sizes, the head of the device table, which plans
+may be written to, and the refusals of every zero_tensor_* call (no device
 pointer is ever read: a refused call launches nothing)."""
 import ctypes
 
@@ -11,7 +11,6 @@ from zero_partitioned_mixed_shard_amd import tensors as T
 
 FP16, BF16, FP32 = Z.ZERO_FP16, Z.ZERO_BF16, Z.ZERO_FP32
 SIZE = {FP16: 2, BF16: 2, FP32: 4}
-PIECE_T = np.dtype([("src", np.uint64), ("tensor", np.int32), ("info", np.uint32)])
 
 
 def entries(rows):
@@ -29,24 +28,28 @@ def init(rows, n=None):
     return rc, plan
 
 
-def table(rows, plan):
-    buf = np.full(plan.table_bytes // 8 + 2, -7, dtype=np.int64)
-    rc = Z.lib().zero_tensor_plan_table(entries(rows).ctypes.data, ctypes.byref(plan),
-                                        buf.ctypes.data)
-    assert (buf[plan.table_bytes // 8:] == -7).all()
-    return rc, buf
+def head(rows, plan):
+    """The table's head: entries, and every tensor's first run, rest and piece."""
+    buf = np.full(plan.head_bytes // 8 + 2, -7, dtype=np.int64)
+    rc = Z.lib().zero_tensor_plan_head(entries(rows).ctypes.data, ctypes.byref(plan),
+                                       buf.ctypes.data)
+    assert rc == Z.ZERO_OK and (buf[plan.head_bytes // 8:] == -7).all()
+    n = len(rows)
+    assert plan.head_bytes % 16 == 0 and 0 <= plan.head_bytes // 8 - (4 * n + 3 * (n + 1)) <= 1
+    firsts = buf[4 * n:4 * n + 3 * (n + 1)].reshape(3, n + 1)
+    return buf[:4 * n].view(T._ENTRY), *firsts
 
 
 def test_entry_and_plan_sizes():
-    assert T._ENTRY.itemsize == 32 and ctypes.sizeof(T.zero_tensor_plan_t) == 64
+    assert T._ENTRY.itemsize == 32 and ctypes.sizeof(T.zero_tensor_plan_t) == 72
 
 
 @pytest.mark.parametrize("seed", range(20))
-def test_table_covers_every_element_once(seed):
+def test_head_counts_every_tensors_parts(seed):
     rng = np.random.default_rng(seed)
     rows, at = [], 1 << 20
     for _ in range(int(rng.integers(0, 12))):
-        n = int(rng.choice([0, 1, 7, 100, 16383, 16384, 16385, 70000, 1000003]))
+        n = int(rng.choice([0, 1, 7, 100, 4095, 4096, 4097, 16383, 16384, 16385, 70000, 1000003]))
         s, d = (int(x) for x in rng.choice([FP16, BF16, FP32], 2))
         dst = at + n * SIZE[s] + (-(at + n * SIZE[s])) % 4
         rows.append((at, dst, n, s, d))
@@ -56,65 +59,26 @@ def test_table_covers_every_element_once(seed):
     assert rc == Z.ZERO_OK and plan.writable == 1
     assert plan.n_tensors == len(rows) and plan.numel == sum(r[2] for r in rows)
     assert plan.bytes == sum(r[2] * (SIZE[r[3]] + SIZE[r[4]]) for r in rows)
-    rc, buf = table(rows, plan)
-    assert rc == Z.ZERO_OK
-    runs, pieces, dsts, first_run, first_rest, first = parts(buf, plan)
-    for f, a, n in ((first, 0, plan.n_pieces), (first_run, 0, plan.n_runs),
-                    (first_rest, plan.n_runs, plan.n_rests)):
-        assert len(f) == len(rows) + 1 and f[0] == a and f[-1] == a + n
+    assert plan.table_bytes - plan.head_bytes == 16 * (plan.n_runs + plan.n_rests) + 24 * plan.n_pieces
+    e, run, rest, piece = head(rows, plan)
+    assert (e == entries(rows)[:len(rows)]).all()
+    for f, a, n in ((run, 0, plan.n_runs), (rest, plan.n_runs, plan.n_rests),
+                    (piece, 0, plan.n_pieces)):
+        assert f[0] == a and f[-1] == a + n
     for k, (src, dst, n, s, d) in enumerate(rows):
-        done = 0
-        for j in range(first[k], first[k + 1]):
-            p, count = pieces[j], int(pieces[j]["info"]) & 0xFFFFFF
-            assert p["tensor"] == k and p["info"] >> 24 == s | d << 4
-            assert p["src"] == src + done * SIZE[s] and dsts[j] == dst + done * SIZE[d]
-            assert 0 < count <= PIECE
-            # every piece but a tensor's first begins at a multiple of 128 bytes of
-            # the output, and no piece but the first and last is short
-            assert done == 0 or dsts[j] % 128 == 0
-            assert j in (first[k], first[k + 1] - 1) or count == PIECE
-            done += count
-        assert done == n
-        # the norm's go by the number of elements alone: whole runs, then the rest
-        mine = np.concatenate([runs[first_run[k]:first_run[k + 1]],
-                               runs[first_rest[k]:first_rest[k + 1]]])
-        counts = (mine["info"] & 0xFFFFFF).astype(np.int64)
-        whole = first_run[k + 1] - first_run[k]
-        assert whole == n // RUN and (counts[:whole] == RUN).all()
-        assert (counts[whole:-1] == PIECE).all() and counts.sum() == n and (counts > 0).all()
-        assert (mine["tensor"] == k).all() and (mine["info"] >> 24 & 15 == s).all()
-        starts = np.cumsum(counts) - counts
-        assert (mine["src"] == src + (starts * SIZE[s]).astype(np.uint64)).all()
+        # runs of 16384 elements, the rest in rests of 4096: by the count alone
+        assert run[k + 1] - run[k] == n // 16384
+        assert rest[k + 1] - rest[k] == -(-(n % 16384) // 4096)
+        # pieces end at multiples of 128 bytes past the one the output begins in
+        lead = dst % 128 // SIZE[d]
+        assert piece[k + 1] - piece[k] == (-(-(n + lead) // 4096) if n else 0)
 
 
-RUN, PIECE = 16384, 4096
-
-
-def parts(buf, plan):
-    """Runs and rests, pieces, outputs' addresses, and every tensor's first run, rest
-    and piece."""
-    n, r, t = plan.n_pieces, plan.n_runs + plan.n_rests, plan.n_tensors + 1
-    buf = buf[:plan.table_bytes // 8]
-    assert len(buf) == 2 * r + 3 * n + 3 * t
-    a, b = 2 * (r + n), 2 * r + 3 * n
-    return (buf[:2 * r].view(PIECE_T), buf[2 * r:a].view(PIECE_T), buf[a:b].view(np.uint64),
-            buf[b:b + t], buf[b + t:b + 2 * t], buf[b + 2 * t:])
-
-
-def test_large_tensors_have_64_bit_addresses():
+def test_large_tensors():
     n = (1 << 36) + 5
-    rows = [(1 << 40, (1 << 42) + 4, n, BF16, FP32)]
-    rc, plan = init(rows)
-    assert rc == Z.ZERO_OK and plan.numel == n
-    rc, buf = table(rows, plan)
-    runs, pieces, dsts, _, _, _ = parts(buf, plan)
-    start = (plan.n_pieces - 1) * PIECE - 1            # the first piece is one element short
-    assert pieces[-1]["src"] == (1 << 40) + 2 * start and dsts[-1] == (1 << 42) + 4 + 4 * start
-    assert int(pieces[-1]["info"]) & 0xFFFFFF == n - start
-    start = plan.n_runs * RUN
-    assert plan.n_rests == 1 and runs[-1]["src"] == (1 << 40) + 2 * start
-    assert int(runs[-1]["info"]) & 0xFFFFFF == n - start
-    assert runs[-2]["src"] == (1 << 40) + 2 * (start - RUN)
+    rc, plan = init([(1 << 40, (1 << 42) + 4, n, BF16, FP32)])
+    assert rc == Z.ZERO_OK and plan.numel == n and plan.bytes == 6 * n
+    assert (plan.n_runs, plan.n_rests) == (n // 16384, 1) and plan.n_pieces == (1 << 24) + 1
 
 
 @pytest.mark.parametrize("rows,writable", [
@@ -158,14 +122,16 @@ def test_init_refusals():
     assert L.zero_tensor_plan_init(entries([ok]).ctypes.data, 1, None) == Z.ZERO_EINVAL
     assert L.zero_tensor_plan_init(None, 0, ctypes.byref(plan)) == Z.ZERO_OK
     rc, plan = init([ok])
-    buf = np.zeros(plan.table_bytes, np.uint8)
+    buf = np.zeros(plan.head_bytes, np.uint8)
     e = entries([ok])
-    assert L.zero_tensor_plan_table(e.ctypes.data, None, buf.ctypes.data) == Z.ZERO_EINVAL
-    assert L.zero_tensor_plan_table(e.ctypes.data, ctypes.byref(plan), None) == Z.ZERO_EINVAL
-    assert L.zero_tensor_plan_table(None, ctypes.byref(plan), buf.ctypes.data) == Z.ZERO_EINVAL
+    assert L.zero_tensor_plan_head(e.ctypes.data, None, buf.ctypes.data) == Z.ZERO_EINVAL
+    assert L.zero_tensor_plan_head(e.ctypes.data, ctypes.byref(plan), None) == Z.ZERO_EINVAL
+    assert L.zero_tensor_plan_head(None, ctypes.byref(plan), buf.ctypes.data) == Z.ZERO_EINVAL
     other = entries([(4096, 8192, 100_000, FP16, FP32)])   # another plan's entries
-    assert L.zero_tensor_plan_table(other.ctypes.data, ctypes.byref(plan),
-                                    buf.ctypes.data) == Z.ZERO_EINVAL
+    assert L.zero_tensor_plan_head(other.ctypes.data, ctypes.byref(plan),
+                                   buf.ctypes.data) == Z.ZERO_EINVAL
+    for args in ((None, 4096), (ctypes.byref(plan), None), (ctypes.byref(plan), 4096 + 8)):
+        assert L.zero_tensor_plan_expand(*args, None) == Z.ZERO_EINVAL
 
 
 def test_workspace_bytes():

@@ -67,7 +67,8 @@ EXPORTS = (
     "zero_adamw_step_ctl", "zero_step_control_update",
     "zero_range_workspace_bytes", "zero_reduce_check_ranges", "zero_adamw_step_ranges",
     "zero_reduce_check_buckets", "zero_reduce_check_owned_noalloc",
-    "zero_tensor_plan_init", "zero_tensor_plan_table", "zero_tensor_workspace_bytes",
+    "zero_tensor_plan_init", "zero_tensor_plan_head", "zero_tensor_plan_expand",
+    "zero_tensor_workspace_bytes",
     "zero_tensor_norm", "zero_tensor_clip", "zero_tensor_clip_norm", "zero_tensor_accumulate",
     "zero_tensor_accumulate_norm",
 )
@@ -128,7 +129,8 @@ def _load():
                                        P], ctypes.c_int),
         "zero_reduce_check_owned_noalloc": ([P, P, i32, i64, i32, f32, P, i32, P], ctypes.c_int),
         "zero_tensor_plan_init": ([P, i64, P], ctypes.c_int),
-        "zero_tensor_plan_table": ([P, P, P], ctypes.c_int),
+        "zero_tensor_plan_head": ([P, P, P], ctypes.c_int),
+        "zero_tensor_plan_expand": ([P, P, P], ctypes.c_int),
         "zero_tensor_workspace_bytes": ([P], ctypes.c_size_t),
         "zero_tensor_norm": ([P, P, i32, f32, P, P, P, P, ctypes.c_size_t, i32, P], ctypes.c_int),
         "zero_tensor_clip": ([P, P, f32, P, P, P], ctypes.c_int),

@@ -2,8 +2,8 @@
 // zero_tensor_* calls of include/zero_shard.h): the norm of all of them and of
 // each, clipping by it, and accumulation of one table into another.
 //
-// A host-built plan cuts every tensor into pieces of at most kPiece elements
-// and the device table holds a record per piece, so a wave or block learns all
+// A plan cuts every tensor into pieces and the device table holds a record per
+// piece (built there from a short list of the tensors), so a wave or block learns all
 // about its work from one scalar load (no search from a block number to a
 // tensor) and nothing spans two tensors: a piece's partial belongs to one
 // tensor, and a tensor's norm is the sum of its pieces'.
@@ -21,6 +21,7 @@
 // by the tensors' numbers of elements alone.
 
 #include <math.h>
+#include <string.h>
 
 #include <algorithm>
 #include <new>
@@ -626,9 +627,78 @@ tensor_accumulate_kernel(const Piece* __restrict__ pieces, void* const* __restri
     }
 }
 
+// ------------------------------------------------------------ table --------
+__host__ __device__ inline int64_t dtype_bytes(int32_t dt) { return dt == ZERO_FP32 ? 4 : 2; }
+
+// Elements of a tensor's first piece: the others then begin at a multiple of
+// 128 bytes of the output.
+__host__ __device__ inline int64_t first_piece(const zero_tensor_entry& e) {
+    return kPiece - (int64_t)((uintptr_t)e.dst % 128) / dtype_bytes(e.dst_dtype);
+}
+__host__ __device__ inline int64_t runs_in(const zero_tensor_entry& e) { return e.numel / kRun; }
+__host__ __device__ inline int64_t rests_in(const zero_tensor_entry& e) {
+    return (e.numel % kRun + kPiece - 1) / kPiece;
+}
+__host__ __device__ inline int64_t pieces_in(const zero_tensor_entry& e) {
+    if (e.numel == 0) return 0;
+    const int64_t first = first_piece(e);
+    return e.numel <= first ? 1 : 1 + (e.numel - first - 1) / kPiece + 1;
+}
+
+// Last index k of first[0, n] (ascending, first[0] <= u < first[n]) with
+// first[k] <= u: the tensor that holds unit u.
+__device__ __forceinline__ int64_t holder(const int64_t* __restrict__ first, int64_t n, int64_t u) {
+    int64_t lo = 0, hi = n;                           // first[lo] <= u < first[hi]
+    while (hi - lo > 1) {
+        const int64_t mid = lo + (hi - lo) / 2;
+        if (first[mid] <= u) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// A thread for each record of the table.
+__global__ void __launch_bounds__(kThreads)
+tensor_expand_kernel(const zero_tensor_entry* __restrict__ entries,
+                     const int64_t* __restrict__ first_run, const int64_t* __restrict__ first_rest,
+                     const int64_t* __restrict__ first_piece_at, int64_t n, int64_t n_runs,
+                     int64_t n_rests, int64_t n_pieces, int64_t blk0, Piece* __restrict__ runs,
+                     Piece* __restrict__ pieces, void** __restrict__ dsts) {
+    const int64_t u = (blk0 + blockIdx.x) * kThreads + threadIdx.x;
+    const int64_t q = u - n_runs - n_rests;           // piece
+    if (q >= n_pieces) return;
+    const int64_t* first = u < n_runs ? first_run : q < 0 ? first_rest : first_piece_at;
+    const int64_t k = holder(first, n, q < 0 ? u : q);
+    const zero_tensor_entry e = entries[k];
+    const int64_t j = (q < 0 ? u : q) - first[k];     // of the tensor's
+    int64_t begin, most;
+    if (u < n_runs) {
+        begin = j * kRun;
+        most = kRun;
+    } else if (q < 0) {
+        begin = runs_in(e) * kRun + j * kPiece;
+        most = kPiece;
+    } else {
+        const int64_t f = first_piece(e);
+        begin = j == 0 ? 0 : f + (j - 1) * kPiece;
+        most = j == 0 ? f : kPiece;
+    }
+    const int64_t left = e.numel - begin;
+    Piece p;
+    p.src = (const char*)e.src + begin * dtype_bytes(e.src_dtype);
+    p.tensor = (int32_t)k;
+    p.info = (uint32_t)(left < most ? left : most) | (uint32_t)e.src_dtype << 24 |
+             (uint32_t)e.dst_dtype << 28;
+    if (q < 0) {
+        runs[u] = p;
+    } else {
+        pieces[q] = p;
+        dsts[q] = (char*)e.dst + begin * dtype_bytes(e.dst_dtype);
+    }
+}
+
 // ------------------------------------------------------------- host --------
 inline bool valid_table_dtype(int32_t dt) { return valid_dtype(dt) || dt == ZERO_FP32; }
-inline int64_t dtype_bytes(int32_t dt) { return dt == ZERO_FP32 ? 4 : 2; }
 
 // Tensors of a plan: one launch finishes a norm for each.
 constexpr int64_t kMaxTensors = kMaxLaunchBlocks;
@@ -676,12 +746,6 @@ bool writable(const zero_tensor_entry* entries, int64_t n) {
 // size computed from them.
 constexpr int64_t kMaxPieces = int64_t(1) << 40;
 
-// Elements of a tensor's first piece: the others then begin at a multiple of
-// 128 bytes of the output.
-int64_t first_piece(const zero_tensor_entry& e) {
-    return kPiece - (int64_t)((uintptr_t)e.dst % 128) / dtype_bytes(e.dst_dtype);
-}
-
 int plan_sizes(const zero_tensor_entry* entries, int64_t n, zero_tensor_plan* plan) {
     int64_t numel = 0, bytes = 0, pieces = 0, runs = 0, rests = 0;
     for (int64_t k = 0; k < n; ++k) {
@@ -696,16 +760,14 @@ int plan_sizes(const zero_tensor_entry* entries, int64_t n, zero_tensor_plan* pl
         Span s;
         if (!span_of(e.src, e.numel, e.src_dtype, &s) || !span_of(e.dst, e.numel, e.dst_dtype, &s))
             return ZERO_ERANGE;
-        int64_t more = e.numel - std::min(e.numel, first_piece(e));
-        more = 1 + more / kPiece + (more % kPiece != 0);
-        if (more > kMaxPieces - pieces) return ZERO_ERANGE;
-        pieces += more;
+        if (pieces_in(e) > kMaxPieces - pieces) return ZERO_ERANGE;
+        pieces += pieces_in(e);
         if (__builtin_add_overflow(numel, e.numel, &numel) ||
             __builtin_add_overflow(bytes, e.numel * (dtype_bytes(e.src_dtype) + dtype_bytes(e.dst_dtype)),
                                    &bytes))
             return ZERO_ERANGE;
-        runs += e.numel / kRun;
-        rests += (e.numel % kRun + kPiece - 1) / kPiece;
+        runs += runs_in(e);
+        rests += rests_in(e);
     }
     plan->n_tensors = n;
     plan->numel = numel;
@@ -713,8 +775,10 @@ int plan_sizes(const zero_tensor_entry* entries, int64_t n, zero_tensor_plan* pl
     plan->n_pieces = pieces;
     plan->n_runs = runs;
     plan->n_rests = rests;
-    plan->table_bytes = (pieces + runs + rests) * (int64_t)sizeof(Piece) +
-                        pieces * (int64_t)sizeof(void*) + 3 * (n + 1) * (int64_t)sizeof(int64_t);
+    plan->head_bytes = (n * (int64_t)sizeof(zero_tensor_entry) + 3 * (n + 1) * (int64_t)sizeof(int64_t) +
+                        15) / 16 * 16;
+    plan->table_bytes = plan->head_bytes + (pieces + runs + rests) * (int64_t)sizeof(Piece) +
+                        pieces * (int64_t)sizeof(void*);
     plan->writable = 0;
     plan->reserved = 0;
     return ZERO_OK;
@@ -724,27 +788,31 @@ int plan_sizes(const zero_tensor_entry* entries, int64_t n, zero_tensor_plan* pl
 bool valid_plan(const zero_tensor_plan* p, const void* table) {
     return p && p->n_tensors >= 0 && p->n_tensors < kMaxTensors && p->n_pieces >= 0 &&
            p->n_pieces <= kMaxPieces && p->n_runs >= 0 && p->n_rests >= 0 && p->n_runs <= p->n_pieces &&
-           p->n_rests <= p->n_pieces && table && ((uintptr_t)table & 15) == 0;
+           p->n_rests <= p->n_pieces && p->head_bytes >= 0 && table && ((uintptr_t)table & 15) == 0;
 }
 
-// The parts of a table, in its order: the norm's runs and rests, the pieces of
-// the passes that write and their outputs, and for every tensor (and the end)
-// its first run's partial, first rest's partial and first piece.
-const Piece* runs_of(const void* table) { return (const Piece*)table; }
-const Piece* pieces_of(const zero_tensor_plan* p, const void* table) {
-    return runs_of(table) + p->n_runs + p->n_rests;
-}
-void* const* dsts_of(const zero_tensor_plan* p, const void* table) {
-    return (void* const*)(pieces_of(p, table) + p->n_pieces);
-}
+// The parts of a table, in its order.  The head: the entries, and for every tensor
+// (and the end) its first run's partial, first rest's partial and first piece.
+// Then the norm's runs and rests, the pieces of the passes that write and their
+// outputs.
+const zero_tensor_entry* entries_of(const void* table) { return (const zero_tensor_entry*)table; }
 const int64_t* first_runs_of(const zero_tensor_plan* p, const void* table) {
-    return (const int64_t*)(dsts_of(p, table) + p->n_pieces);
+    return (const int64_t*)(entries_of(table) + p->n_tensors);
 }
 const int64_t* first_rests_of(const zero_tensor_plan* p, const void* table) {
     return first_runs_of(p, table) + p->n_tensors + 1;
 }
 const int64_t* first_pieces_of(const zero_tensor_plan* p, const void* table) {
     return first_rests_of(p, table) + p->n_tensors + 1;
+}
+const Piece* runs_of(const zero_tensor_plan* p, const void* table) {
+    return (const Piece*)((const char*)table + p->head_bytes);
+}
+const Piece* pieces_of(const zero_tensor_plan* p, const void* table) {
+    return runs_of(p, table) + p->n_runs + p->n_rests;
+}
+void* const* dsts_of(const zero_tensor_plan* p, const void* table) {
+    return (void* const*)(pieces_of(p, table) + p->n_pieces);
 }
 
 // Partials that the finishing block takes as they are; more are folded first.
@@ -807,7 +875,7 @@ int one_block_impl(const zero_tensor_plan* plan, const void* table, float max_no
                    int32_t per_tensor, float inv_scale, const zero_step_control* ctl,
                    int32_t accumulate, zero_step_result* res, float* norms, hipStream_t stream) {
     return launch_shape(tensor_one_block_kernel<KIND, CLIP>, 1, kFinishThreads, 0u, stream,
-                        runs_of(table), (int)plan->n_rests, pieces_of(plan, table),
+                        runs_of(plan, table), (int)plan->n_rests, pieces_of(plan, table),
                         dsts_of(plan, table), (int)plan->n_pieces, first_rests_of(plan, table),
                         plan->n_tensors, max_norm, (int)(per_tensor != 0), inv_scale, ctl,
                         (int)(accumulate != 0), res, norms);
@@ -819,7 +887,7 @@ int partials_impl(const zero_tensor_plan* plan, const void* table, double* part,
     const int64_t n_runs = plan->n_runs, n_rests = plan->n_rests;
     return in_launches(n_runs + (n_rests + kWaves - 1) / kWaves, [&](int64_t b, int64_t grid) {
         return launch(tensor_norm_kernel<KIND>, grid, lds_for_blocks(kNormBlocksPerCU), stream,
-                      runs_of(table), n_runs, n_rests, b, part);
+                      runs_of(plan, table), n_runs, n_rests, b, part);
     });
 }
 
@@ -900,50 +968,43 @@ int zero_tensor_plan_init(const zero_tensor_entry* entries, int64_t n_tensors,
     return ZERO_OK;
 }
 
-int zero_tensor_plan_table(const zero_tensor_entry* entries, const zero_tensor_plan* plan,
-                           void* table) {
-    if (!plan || !table || plan->n_tensors < 0 || (plan->n_tensors > 0 && !entries)) return ZERO_EINVAL;
+int zero_tensor_plan_head(const zero_tensor_entry* entries, const zero_tensor_plan* plan,
+                          void* head) {
+    if (!plan || !head || plan->n_tensors < 0 || (plan->n_tensors > 0 && !entries)) return ZERO_EINVAL;
     zero_tensor_plan again;
     const int rc = plan_sizes(entries, plan->n_tensors, &again);
     if (rc != ZERO_OK) return rc;
     if (again.n_pieces != plan->n_pieces || again.n_runs != plan->n_runs ||
-        again.n_rests != plan->n_rests)
+        again.n_rests != plan->n_rests || again.head_bytes != plan->head_bytes)
         return ZERO_EINVAL;
-    Piece* run = (Piece*)runs_of(table);
-    Piece* rest = run + plan->n_runs;
-    Piece* piece = (Piece*)pieces_of(plan, table);
-    void** dst = (void**)dsts_of(plan, table);
-    int64_t* first_run = (int64_t*)first_runs_of(plan, table);
-    int64_t* first_rest = (int64_t*)first_rests_of(plan, table);
-    int64_t* first_of_pieces = (int64_t*)first_pieces_of(plan, table);
-    auto part = [](const zero_tensor_entry& e, int64_t k, int64_t begin, int64_t count) {
-        Piece p;
-        p.src = (const char*)e.src + begin * dtype_bytes(e.src_dtype);
-        p.tensor = (int32_t)k;
-        p.info = (uint32_t)count | (uint32_t)e.src_dtype << 24 | (uint32_t)e.dst_dtype << 28;
-        return p;
-    };
-    int64_t r = 0, t = 0, q = 0;
-    for (int64_t k = 0; k < plan->n_tensors; ++k) {
-        const zero_tensor_entry& e = entries[k];
-        first_run[k] = r;
-        first_rest[k] = plan->n_runs + t;
-        first_of_pieces[k] = q;
-        int64_t b = 0;
-        for (; e.numel - b >= kRun; b += kRun) run[r++] = part(e, k, b, kRun);
-        for (; b < e.numel; b += kPiece)
-            rest[t++] = part(e, k, b, std::min((int64_t)kPiece, e.numel - b));
-        b = 0;
-        for (int64_t c; b < e.numel; b += c, ++q) {
-            c = std::min(b == 0 ? first_piece(e) : (int64_t)kPiece, e.numel - b);
-            piece[q] = part(e, k, b, c);
-            dst[q] = (char*)e.dst + b * dtype_bytes(e.dst_dtype);
-        }
+    const int64_t n = plan->n_tensors;
+    memset(head, 0, (size_t)plan->head_bytes);
+    if (n > 0) memcpy(head, entries, (size_t)n * sizeof(zero_tensor_entry));
+    int64_t* first_run = (int64_t*)first_runs_of(plan, head);
+    int64_t* first_rest = (int64_t*)first_rests_of(plan, head);
+    int64_t* first_piece_at = (int64_t*)first_pieces_of(plan, head);
+    int64_t run = 0, rest = plan->n_runs, piece = 0;
+    for (int64_t k = 0;; ++k) {
+        first_run[k] = run;
+        first_rest[k] = rest;
+        first_piece_at[k] = piece;
+        if (k == n) return ZERO_OK;
+        run += runs_in(entries[k]);
+        rest += rests_in(entries[k]);
+        piece += pieces_in(entries[k]);
     }
-    first_run[plan->n_tensors] = r;
-    first_rest[plan->n_tensors] = plan->n_runs + t;
-    first_of_pieces[plan->n_tensors] = q;
-    return ZERO_OK;
+}
+
+int zero_tensor_plan_expand(const zero_tensor_plan* plan, void* table, hipStream_t stream) {
+    if (!valid_plan(plan, table)) return ZERO_EINVAL;
+    const int64_t units = plan->n_runs + plan->n_rests + plan->n_pieces;
+    return in_launches((units + kThreads - 1) / kThreads, [&](int64_t b, int64_t grid) {
+        return launch(tensor_expand_kernel, grid, 0, stream, entries_of(table),
+                      first_runs_of(plan, table), first_rests_of(plan, table),
+                      first_pieces_of(plan, table), plan->n_tensors, plan->n_runs, plan->n_rests,
+                      plan->n_pieces, b, (Piece*)runs_of(plan, table), (Piece*)pieces_of(plan, table),
+                      (void**)dsts_of(plan, table));
+    });
 }
 
 size_t zero_tensor_workspace_bytes(const zero_tensor_plan* plan) {

@@ -34,7 +34,7 @@ class zero_tensor_plan_t(ctypes.Structure):
     _fields_ = [("n_tensors", ctypes.c_int64), ("numel", ctypes.c_int64),
                 ("bytes", ctypes.c_int64), ("n_pieces", ctypes.c_int64), ("n_runs", ctypes.c_int64),
                 ("n_rests", ctypes.c_int64),
-                ("table_bytes", ctypes.c_int64), ("writable", ctypes.c_int32),
+                ("head_bytes", ctypes.c_int64), ("table_bytes", ctypes.c_int64), ("writable", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
 
 
@@ -72,10 +72,11 @@ class zero_tensor_plan:
 
     def __init__(self, tensors: Sequence, out: Optional[Sequence] = None, device=None):
         import torch
-        codes = {torch.float32: ZERO_FP32, torch.float16: ZERO_FP16, torch.bfloat16: ZERO_BF16}
+        types = {torch.float32: ZERO_FP32, torch.float16: ZERO_FP16, torch.bfloat16: ZERO_BF16}
         tensors = list(tensors)
         outs = tensors if out is None else list(out)
-        if len(outs) != len(tensors):
+        n = len(tensors)
+        if len(outs) != n:
             raise ValueError("out: one tensor for each tensor")
         if device is None:
             device = tensors[0].device if tensors else "cuda"
@@ -84,37 +85,46 @@ class zero_tensor_plan:
             raise ValueError("device tensors expected")
         if device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
-        entries = np.zeros(max(1, len(tensors)), dtype=_ENTRY)
-        rows = []
-        for t, o in zip(tensors, outs):
-            for x in ((t,) if o is t else (t, o)):
-                if x.layout != torch.strided:
-                    raise ValueError("tensors must be strided (not sparse)")
-                if x.device != device:
-                    raise ValueError(f"tensors on {device} expected, got one on {x.device}")
-                if x.dtype not in codes:
-                    raise TypeError(f"float32, float16 or bfloat16 tensors expected, got {x.dtype}")
-            order = _order(t)
-            if o is not t and (o.numel() != t.numel() or _order(o) != order or
-                               (order is not None and o.shape != t.shape)):
-                raise ValueError("out: as many elements as the tensor, in the same order")
-            rows.append((t.data_ptr(), o.data_ptr(), t.numel(), codes[t.dtype], codes[o.dtype]))
-        if rows:
-            entries[:] = rows
+        # a pass per property: lists of thousands of tensors are common
+        sides = []
+        for side in ((tensors,) if out is None else (tensors, outs)):
+            if any(t.layout is not torch.strided for t in side):
+                raise ValueError("tensors must be strided (not sparse)")
+            if any(t.get_device() != device.index for t in side):
+                raise ValueError(f"tensors on {device} expected")
+            codes = [types.get(t.dtype) for t in side]
+            if None in codes:
+                bad = side[codes.index(None)].dtype
+                raise TypeError(f"float32, float16 or bfloat16 tensors expected, got {bad}")
+            sides.append(([t.data_ptr() for t in side], [t.numel() for t in side], codes,
+                          [None if t.is_contiguous() else _order(t) for t in side]))
+        _, numels, _, orders = sides[0]
+        if sides[-1][1] != numels or sides[-1][3] != orders or \
+                any(o is not None and t.shape != y.shape for o, t, y in zip(orders, tensors, outs)):
+            raise ValueError("out: as many elements as the tensor, in the same order")
+        entries = np.zeros(max(1, n), dtype=_ENTRY)
+        if n:
+            entries["src"], entries["numel"], entries["src_dtype"] = sides[0][:3]
+            entries["dst"], entries["dst_dtype"] = sides[-1][0], sides[-1][2]
         self.c = zero_tensor_plan_t()
-        n = len(tensors)
         _check(_lib.zero_tensor_plan_init(entries.ctypes.data, n, ctypes.byref(self.c)),
                "zero_tensor_plan_init")
-        host = np.empty(self.c.table_bytes // 8, dtype=np.int64)
-        _check(_lib.zero_tensor_plan_table(entries.ctypes.data, ctypes.byref(self.c),
-                                           host.ctypes.data), "zero_tensor_plan_table")
+        head = np.empty(self.c.head_bytes, dtype=np.uint8)
+        _check(_lib.zero_tensor_plan_head(entries.ctypes.data, ctypes.byref(self.c),
+                                          head.ctypes.data), "zero_tensor_plan_head")
         self.tensors, self.out, self.device, self._index = tensors, outs, device, device.index
         self.n_tensors, self.numel = n, self.c.numel
         self.workspace_bytes = int(_lib.zero_tensor_workspace_bytes(ctypes.byref(self.c)))
         with torch.cuda.device(device):
-            self.table = torch.from_numpy(host).to(device)
-            self._streams = {torch.cuda.current_stream(device).cuda_stream}
-        self._args = (ctypes.byref(self.c), self.table.data_ptr())
+            stream = torch.cuda.current_stream(device)
+            self.table = torch.empty(self.c.table_bytes, dtype=torch.uint8, device=device)
+            self.table[:self.c.head_bytes].copy_(torch.from_numpy(head))
+            self._args = (ctypes.byref(self.c), self.table.data_ptr())
+            _check(_lib.zero_tensor_plan_expand(*self._args, stream.cuda_stream),
+                   "zero_tensor_plan_expand")
+            # complete before any stream's calls; the calls then need no events
+            stream.synchronize()
+            self._streams = {stream.cuda_stream}
 
     def _call(self, fn, args, stream) -> None:
         """fn(plan, table, *args, stream) with the plan's device current."""
