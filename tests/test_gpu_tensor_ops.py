@@ -301,6 +301,26 @@ def test_clip_off_leaves_values(max_norm):
     assert all(torch.equal(t, b) for t, b in zip(out, before))
 
 
+def test_clip_next_to_the_border():
+    """Norms a few roundings around max_norm - 1e-6, where the ratio turns from 1 to
+    below: in place gives the bits of the same clip into other tensors."""
+    x = torch.randn(5000, device="cuda")
+    for max_norm in (1.0, 1e-6, 2e-6, 1e3, 5e-7):
+        top = f32(max_norm) - 1e-6
+        for step in (-1e-3, -3e-16, -1e-16, 0.0, 1e-16, 3e-16, 1e-9, 1e-7, 1e-3):
+            norm = abs(top) * (1.0 + step)
+            mine, out = x.clone(), torch.empty_like(x)
+            res = make_res(norm * norm, 0, 1.0)
+            Z.zero_tensor_clip(Z.zero_tensor_plan([mine]), max_norm, res)
+            Z.zero_tensor_clip(Z.zero_tensor_plan([x], out=[out]), max_norm, res)
+            assert torch.equal(mine, out), (max_norm, step)
+            norms = torch.tensor([norm], device="cuda")
+            mine.copy_(x)
+            Z.zero_tensor_clip(Z.zero_tensor_plan([mine]), max_norm, res, norms=norms)
+            Z.zero_tensor_clip(Z.zero_tensor_plan([x], out=[out]), max_norm, res, norms=norms)
+            assert torch.equal(mine, out), (max_norm, step)
+
+
 def test_clip_each_by_its_own_norm():
     sizes = [1, 100, 0, 16384, 50001]
     s = Set(sizes, [F32, BF, HALF, HALF, F32], [0, 1, 0, 5, 2], seed=9)
