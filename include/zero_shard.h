@@ -541,9 +541,9 @@ int zero_tensor_norm(const zero_tensor_plan* plan, const void* table, int32_t ki
 /* Unscale and clip: y = round(x * f) with f = fp32(res->inv_scale * coef),
  *   coef = max_norm / (norm + 1e-6) if max_norm > 0 and that is below 1, else 1
  * (fp64), where norm is sqrt(res->sumsq) or, with norms != NULL, tensor k's
- * norms[k].  The product is fp32, then rounded once (nearest, ties to even)
- * to y's type.  With res->overflow set nothing is written, and in place with f = 1
- * nothing need be.
+ * norms[k] (inf gives f = 0; an f below fp32's normal range has fewer bits).  The
+ * product is fp32, then rounded once (nearest, ties to even) to y's type.  With
+ * res->overflow set nothing is written, and in place with f = 1 nothing need be.
  *   res    device, in: written by zero_tensor_norm or any check of this library
  *   norms  device, in, fp32[n_tensors], or NULL
  * Errors: ZERO_EINVAL for NULL pointers, a plan that is not writable, a NaN

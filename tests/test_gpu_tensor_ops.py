@@ -268,6 +268,32 @@ def test_norm_past_32_bit_offsets():
     assert [float(t[k]) for k in (5, 1 << 31, n - 1)] == [6.0, -2.0, 1.5]
 
 
+def test_tables_longer_than_one_launch():
+    """More pieces than a grid holds (6.9e10 elements in one tensor): values at the
+    ends and on both sides of the launches' border."""
+    border = ((1 << 24) - 1) * 4096                       # elements of a launch's pieces
+    n = border + 5000
+    if torch.cuda.mem_get_info()[0] < 2 * n + (8 << 30):
+        pytest.skip("not enough device memory")
+    t = torch.zeros(n, dtype=BF, device="cuda")
+    at = [0, border - 1, border, n - 1]
+    for k, v in zip(at, (1.0, -2.0, 4.0, -10.0)):
+        t[k] = v
+    plan = Z.zero_tensor_plan([t])
+    assert plan.c.n_pieces == (1 << 24) + 1
+    ws = workspace(plan)
+    for kind, want in (("l2", 121.0), ("max", 100.0)):
+        res = make_res()
+        Z.zero_tensor_norm(plan, 1.0, res, ws, kind=kind)
+        assert Z.read_result(res).sumsq == want
+    Z.zero_tensor_clip(plan, 0.0, make_res(1.0, 0, 0.5))
+    assert [float(t[k]) for k in at] == [0.5, -1.0, 2.0, -5.0]
+    res = make_res()
+    Z.zero_tensor_accumulate(plan, 1.0, res=res, workspace=ws)
+    assert [float(t[k]) for k in at] == [1.0, -2.0, 4.0, -10.0]
+    assert Z.read_result(res).sumsq == 121.0
+
+
 # -------------------------------------------------------------------- clip --
 @pytest.mark.parametrize("dst", [None, F32, HALF, BF])
 @pytest.mark.parametrize("src", [F32, HALF, BF])
@@ -331,6 +357,22 @@ def test_clip_each_by_its_own_norm():
     Z.zero_tensor_clip(plan, 0.5, make_res(1.0, 0, 0.5), norms=torch.tensor(given, device="cuda"))
     for t, x, n in zip(out, host, given):
         assert_rounded(t, clip_want(x, f32(n), 0.5, 0.5), t.dtype, clip_steps(t.dtype))
+
+
+def test_norms_beyond_fp32():
+    """A tensor whose norm fp32 does not hold: finite in the result, inf among the
+    norms, and clipped to zeros by it; by the result's norm as defined."""
+    t = torch.full((5000,), 3e38, device="cuda")
+    out = torch.ones(5000, device="cuda")
+    plan = Z.zero_tensor_plan([t], out=[out])
+    res, norms = make_res(), torch.zeros(1, device="cuda")
+    Z.zero_tensor_clip_norm(plan, 1.0, 1.0, res, workspace(plan), norms=norms, per_tensor=True)
+    assert Z.read_result(res).overflow == 0 and norms.item() == float("inf")
+    assert bool((out == 0).all())
+    check_norm(res, None, [host64(t)], "l2", 1.0)
+    Z.zero_tensor_clip(plan, 1e6, res)
+    assert_rounded(out, clip_want(host64(t), math.sqrt(Z.read_result(res).sumsq), 1e6, 1.0), F32,
+                   clip_steps(F32))
 
 
 def test_clip_rounds_to_nearest_even_and_to_inf():

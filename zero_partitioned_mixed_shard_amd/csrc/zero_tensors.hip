@@ -3,8 +3,8 @@
 // each, clipping by it, and accumulation of one table into another.
 //
 // A plan cuts every tensor into pieces and the device table holds a record per
-// piece (built there from a short list of the tensors), so a wave or block learns all
-// about its work from one scalar load (no search from a block number to a
+// piece (built there from a short list of the tensors), so a wave or block learns
+// all about its work from one scalar load (no search from a block number to a
 // tensor) and nothing spans two tensors: a piece's partial belongs to one
 // tensor, and a tensor's norm is the sum of its pieces'.
 //
@@ -569,8 +569,10 @@ tensor_one_block_kernel(const Piece* __restrict__ rests, int n_rests,
 }
 
 // ------------------------------------------------------- accumulate --------
-// KIND 0: no norm of the result.
-template <int KIND, bool FIRST, int SRC, int DST, bool NT>
+// KIND 0: no norm of the result.  Loads and stores that do not stay in the caches:
+// 1736 us with plain ones for 9.4e8 bf16 into fp32, against 1501; a table of 83 MB
+// gains 6 % from plain ones, of 221 MB loses 13 %.
+template <int KIND, bool FIRST, int SRC, int DST>
 __device__ __forceinline__ void piece_accumulate(const void* src, void* dst, int count, float w,
                                                  Norm<KIND>& n) {
     constexpr int W = kWidth<SRC, DST>, R = W * kThreads, U = kPiece / R;
@@ -578,9 +580,9 @@ __device__ __forceinline__ void piece_accumulate(const void* src, void* dst, int
     Raw<SRC, W> x[U];
     Raw<DST, W> y[U];
     auto load = [&](int u) {
-        x[u] = load_raw<SRC, W, NT>(src, e + u * R);
+        x[u] = load_raw<SRC, W, true>(src, e + u * R);
         if (FIRST) y[u].clear();
-        else y[u] = load_raw<DST, W, NT>(dst, e + u * R);
+        else y[u] = load_raw<DST, W, true>(dst, e + u * R);
     };
     auto add = [&](int u) {
         Raw<DST, W> z;
@@ -589,7 +591,7 @@ __device__ __forceinline__ void piece_accumulate(const void* src, void* dst, int
             z.set(k, FIRST ? w * x[u].get(k) : fmaf(w, x[u].get(k), y[u].get(k)));
             if (KIND) n.add(z.get(k));               // what a pass over dst would read
         }
-        store_raw<DST, W, NT>(dst, e + u * R, z);
+        store_raw<DST, W, true>(dst, e + u * R, z);
     };
     if (count == kPiece) {
 #pragma unroll
@@ -627,8 +629,8 @@ tensor_accumulate_kernel(const Piece* __restrict__ pieces, void* const* __restri
     Norm<KIND> n;
     by_type(p.src_dtype(), [&](auto s) {
         by_type(p.dst_dtype(), [&](auto d) {
-            piece_accumulate<KIND, FIRST, decltype(s)::value, decltype(d)::value, true>(
-                p.src, dst, p.count(), w, n);
+            piece_accumulate<KIND, FIRST, decltype(s)::value, decltype(d)::value>(p.src, dst, p.count(),
+                                                                                 w, n);
         });
     });
     if (KIND) {
@@ -955,9 +957,20 @@ int accumulate_impl(const zero_tensor_plan* plan, const void* table, float weigh
     const auto kernel = overwrite ? tensor_accumulate_kernel<KIND, true>
                                   : tensor_accumulate_kernel<KIND, false>;
     return in_launches(plan->n_pieces, [&](int64_t b, int64_t grid) {
-        return launch(kernel, grid, lds_for_blocks(kAddBlocksPerCU), stream, pieces_of(plan, table) + b, dsts_of(plan, table) + b, weight,
-                      part + b);
+        return launch(kernel, grid, lds_for_blocks(kAddBlocksPerCU), stream, pieces_of(plan, table) + b,
+                      dsts_of(plan, table) + b, weight, KIND ? part + b : part);
     });
+}
+
+template <int KIND>
+int accumulate_norm_impl(const zero_tensor_plan* plan, const void* table, float weight,
+                         int32_t overwrite, float inv_scale, const zero_step_control* ctl,
+                         int32_t accumulate, zero_step_result* res, float* norms, double* part,
+                         hipStream_t stream) {
+    const int rc = accumulate_impl<KIND>(plan, table, weight, overwrite, part, stream);
+    if (rc != ZERO_OK) return rc;
+    return finish<KIND>(plan->n_pieces, first_pieces_of(plan, table), nullptr, plan->n_tensors,
+                        inv_scale, ctl, accumulate, res, norms, part, stream);
 }
 
 }  // namespace
@@ -1071,20 +1084,15 @@ int zero_tensor_accumulate_norm(const zero_tensor_plan* plan, const void* table,
                                 const zero_step_control* ctl, zero_step_result* res, float* norms,
                                 void* workspace, size_t workspace_bytes, int32_t accumulate,
                                 hipStream_t stream) {
-    int rc = norm_args(plan, table, kind, inv_scale, ctl, res, workspace, workspace_bytes);
+    const int rc = norm_args(plan, table, kind, inv_scale, ctl, res, workspace, workspace_bytes);
     if (rc != ZERO_OK) return rc;
     if (!plan->writable || !__builtin_isfinite(weight)) return ZERO_EINVAL;
     double* part = (double*)workspace;
-    if (kind == ZERO_NORM_L2) {
-        rc = accumulate_impl<ZERO_NORM_L2>(plan, table, weight, overwrite, part, stream);
-        if (rc != ZERO_OK) return rc;
-        return finish<ZERO_NORM_L2>(plan->n_pieces, first_pieces_of(plan, table), nullptr,
-                                    plan->n_tensors, inv_scale, ctl, accumulate, res, norms, part, stream);
-    }
-    rc = accumulate_impl<ZERO_NORM_MAX>(plan, table, weight, overwrite, part, stream);
-    if (rc != ZERO_OK) return rc;
-    return finish<ZERO_NORM_MAX>(plan->n_pieces, first_pieces_of(plan, table), nullptr,
-                                    plan->n_tensors, inv_scale, ctl, accumulate, res, norms, part, stream);
+    return kind == ZERO_NORM_L2
+               ? accumulate_norm_impl<ZERO_NORM_L2>(plan, table, weight, overwrite, inv_scale, ctl,
+                                                    accumulate, res, norms, part, stream)
+               : accumulate_norm_impl<ZERO_NORM_MAX>(plan, table, weight, overwrite, inv_scale, ctl,
+                                                     accumulate, res, norms, part, stream);
 }
 
 }  // extern "C"
