@@ -477,7 +477,7 @@ typedef struct zero_tensor_plan {
     int32_t writable;    /* 1: no output overlaps another output, nor an input
                             that is not its own in place; 0: the calls that
                             write refuse this plan (ZERO_EINVAL)              */
-    int32_t reserved;
+    int32_t fp32_out;    /* 1: most elements' outputs are fp32                */
 } zero_tensor_plan;
 
 enum zero_norm_kind {
@@ -521,7 +521,8 @@ size_t zero_tensor_workspace_bytes(const zero_tensor_plan* plan);
  * the norm, so zero_adamw_step and zero_tensor_clip clip by that norm.  With
  * accumulate != 0, *res is joined with what it held (L2: the sum; MAX: the
  * larger; the flags ORed), so several tables checked in turn on one stream give
- * one result.  The order of every sum goes by the numbers of elements alone.  With the flag set,
+ * one result.  The order of every sum goes by the numbers of elements alone: the
+ * same values give the same bits wherever the tensors lie.  With the flag set,
  * sumsq and the norms of the tensors concerned are inf or NaN.
  *   table      device, the plan's table
  *   ctl        device zero_step_control, or NULL

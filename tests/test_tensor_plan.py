@@ -59,6 +59,7 @@ def test_head_counts_every_tensors_parts(seed):
     assert rc == Z.ZERO_OK and plan.writable == 1
     assert plan.n_tensors == len(rows) and plan.numel == sum(r[2] for r in rows)
     assert plan.bytes == sum(r[2] * (SIZE[r[3]] + SIZE[r[4]]) for r in rows)
+    assert plan.fp32_out == (sum(r[2] for r in rows if r[4] == FP32) > plan.numel // 2)
     assert plan.table_bytes - plan.head_bytes == 16 * (plan.n_runs + plan.n_rests) + 24 * plan.n_pieces
     e, run, rest, piece = head(rows, plan)
     assert (e == entries(rows)[:len(rows)]).all()

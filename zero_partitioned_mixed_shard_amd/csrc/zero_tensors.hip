@@ -60,8 +60,7 @@ constexpr int kRunGroup = 8, kPieceGroup = 32;
 // Resident blocks per CU (lds_for_blocks).  Norm: 5 read 6.7e9 bf16 0.5 % faster
 // than 8 and a mixed-type table 1.5 %; 4 another 0.7 %, but 10,000 ragged tensors
 // 1 % slower.  Clip: 9.4e8 bf16 in place take 564 us at 5, 589 at 4, 585 at 8.
-// Accumulation: 9.4e8 bf16 into fp32 take 1489 us at 3, 1432-1452 at 2, 1517 at
-// 4, 1571 at 8; fp16 into fp16 12-15 % more at 2 than at 3.
+// Accumulation: 3, and 2 for large tables with fp32 outputs (add_blocks).
 constexpr int kNormBlocksPerCU = 5, kClipBlocksPerCU = 5, kAddBlocksPerCU = 3;
 // Loads of 16 bytes that a lane has in flight in the norm of a run, and of a
 // rest (8 for the runs: 1 % slower; 4 for the rests: the same).
@@ -759,7 +758,7 @@ bool writable(const zero_tensor_entry* entries, int64_t n) {
 constexpr int64_t kMaxPieces = int64_t(1) << 40;
 
 int plan_sizes(const zero_tensor_entry* entries, int64_t n, zero_tensor_plan* plan) {
-    int64_t numel = 0, bytes = 0, pieces = 0, runs = 0, rests = 0;
+    int64_t numel = 0, bytes = 0, fp32_out = 0, pieces = 0, runs = 0, rests = 0;
     for (int64_t k = 0; k < n; ++k) {
         const zero_tensor_entry& e = entries[k];
         if (e.numel < 0 || !valid_table_dtype(e.src_dtype) || !valid_table_dtype(e.dst_dtype))
@@ -778,6 +777,7 @@ int plan_sizes(const zero_tensor_entry* entries, int64_t n, zero_tensor_plan* pl
             __builtin_add_overflow(bytes, e.numel * (dtype_bytes(e.src_dtype) + dtype_bytes(e.dst_dtype)),
                                    &bytes))
             return ZERO_ERANGE;
+        if (e.dst_dtype == ZERO_FP32) fp32_out += e.numel;
         runs += runs_in(e);
         rests += rests_in(e);
     }
@@ -792,7 +792,7 @@ int plan_sizes(const zero_tensor_entry* entries, int64_t n, zero_tensor_plan* pl
     plan->table_bytes = plan->head_bytes + (pieces + runs + rests) * (int64_t)sizeof(Piece) +
                         pieces * (int64_t)sizeof(void*);
     plan->writable = 0;
-    plan->reserved = 0;
+    plan->fp32_out = fp32_out > numel / 2 ? 1 : 0;
     return ZERO_OK;
 }
 
@@ -951,13 +951,21 @@ int clip_norm_impl(const zero_tensor_plan* plan, const void* table, float max_no
     return clip_impl(plan, table, max_norm, res, per_tensor ? norms : nullptr, stream);
 }
 
+// Resident blocks per CU of an accumulation.  bf16 into fp32, 9.4e8 elements: 1489 us
+// at 3, 1432-1458 at 2, 1517 at 4, 1571 at 8; 5.1e8: 714 at 3, 704 at 2; 1.7e8: 230
+// at both; 4001 ragged tensors of 8.3e7: 134 at 3, 140 at 2.  fp16 into fp16: 12-15
+// % more at 2 than at 3.
+int add_blocks(const zero_tensor_plan* p) {
+    return p->fp32_out && p->bytes > int64_t(2) << 30 ? 2 : kAddBlocksPerCU;
+}
+
 template <int KIND>
 int accumulate_impl(const zero_tensor_plan* plan, const void* table, float weight,
                     int32_t overwrite, double* part, hipStream_t stream) {
     const auto kernel = overwrite ? tensor_accumulate_kernel<KIND, true>
                                   : tensor_accumulate_kernel<KIND, false>;
     return in_launches(plan->n_pieces, [&](int64_t b, int64_t grid) {
-        return launch(kernel, grid, lds_for_blocks(kAddBlocksPerCU), stream, pieces_of(plan, table) + b,
+        return launch(kernel, grid, lds_for_blocks(add_blocks(plan)), stream, pieces_of(plan, table) + b,
                       dsts_of(plan, table) + b, weight, KIND ? part + b : part);
     });
 }
