@@ -429,6 +429,14 @@ def test_clip_norm_is_norm_then_clip(kind, per_tensor, in_place):
             norm = norms[1][k].item() if per_tensor else total
             assert_rounded(outs[1][k], clip_want(host[k], norm, f32(0.05), inv), outs[1][k].dtype,
                            clip_steps(outs[1][k].dtype))
+        if not per_tensor and not in_place:               # without the tensors' norms: same bits
+            bare = make_res()
+            again = [t.clone().zero_() for t in outs[1]]
+            plan = Z.zero_tensor_plan(tensors, out=again, device="cuda")
+            Z.zero_tensor_clip_norm(plan, 0.05, inv, bare, workspace(plan), kind=kind)
+            assert torch.equal(bare, res[0])
+            for a, b in zip(outs[0], again):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
 @pytest.mark.parametrize("sizes", [[40], [9, 70000, 5], [1 << 20, 3]])
@@ -442,6 +450,87 @@ def test_clip_norm_overflow_writes_nothing(sizes, per_tensor):
     Z.zero_tensor_clip_norm(plan, 1.0, 1.0, res, workspace(plan), norms=norms, per_tensor=per_tensor)
     assert Z.read_result(res).overflow == 1
     assert all(bool((o == 3.0).all()) for o in out)
+    if not per_tensor:
+        for kind in ("l2", "max"):
+            res = make_res()
+            Z.zero_tensor_clip_norm(plan, 1.0, 1.0, res, workspace(plan), kind=kind)
+            assert Z.read_result(res).overflow == 1
+            assert all(bool((o == 3.0).all()) for o in out)
+
+
+@pytest.mark.parametrize("sizes", [[40, 3], [900] * 12, [9, 70000, 5], [3000] * 1100, [1 << 20, 3]])
+def test_unscale_factor_from_the_step_control(sizes):
+    """Every call and path with the factor read on the device gives the bits of the
+    same call with it as an argument."""
+    tensors = list(torch.randn(sum(sizes), device="cuda").split(sizes))
+    ctl = Z.control_to_device(Z.zero_step_control_init(8.0, 1.0, 1000, 3.0, 0.9, 0.999))
+    inv = Z.read_control(ctl).inv_scale
+    assert inv == f32(1.0 / 24.0)
+    for kind in ("l2", "max"):
+        for norms in (None, torch.zeros(len(sizes), device="cuda")):
+            got = []
+            for args in ((inv, {}), (1.0, {"ctl_dev": ctl})):
+                out = [torch.zeros_like(t) for t in tensors]
+                acc = [torch.zeros_like(t) for t in tensors]
+                plan, add = (Z.zero_tensor_plan(tensors, out=o) for o in (out, acc))
+                res, ws = [make_res() for _ in range(3)], workspace(plan)
+                kw = dict(kind=kind, norms=norms, **args[1])
+                Z.zero_tensor_norm(plan, args[0], res[0], ws, **kw)
+                Z.zero_tensor_clip_norm(plan, 0.1, args[0], res[1], ws, **kw)
+                Z.zero_tensor_accumulate(add, 0.5, overwrite=True, res=res[2], workspace=ws,
+                                         inv_scale=args[0], **kw)
+                got.append(res + out + acc + ([norms.clone()] if norms is not None else []))
+            for a, b in zip(*got):
+                assert torch.equal(a, b)
+            assert torch.equal(got[0][0], got[0][1])
+            check_norm(got[0][0], None, [host64(t) for t in tensors], kind, inv)
+
+
+def test_clip_by_the_flat_checks_result():
+    """Tensors clipped by the norm that the flat buffer's check found."""
+    sizes = [700, 33, 20000]
+    flat = torch.randn(sum(sizes), device="cuda").to(BF)
+    pieces = list(flat.split(sizes))
+    out = [torch.empty(n, device="cuda") for n in sizes]
+    res = make_res()
+    ws = torch.empty(-(-Z.zero_check_workspace_bytes(flat.numel()) // 8), dtype=torch.float64,
+                     device="cuda")
+    Z.zero_unscale_check_norm(flat, 0.125, res, ws)
+    Z.zero_tensor_clip(Z.zero_tensor_plan(pieces, out=out), 1.0, res)
+    host = host64(flat)
+    assert_rounded(torch.cat(out), clip_want(host, float(np.linalg.norm(host)) * 0.125, 1.0, 0.125),
+                   F32, clip_steps(F32) + 21000 * 2.0 ** -53)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_tables(seed):
+    """Tables of random lengths, types and places: norm, clip_norm and accumulation
+    against 64 bits, guard bands around every output."""
+    rng = np.random.default_rng(100 + seed)
+    count = int(2 ** rng.uniform(0, 8))
+    sizes = [int(2 ** rng.uniform(0, 17)) - int(rng.integers(0, 2)) for _ in range(count)]
+    pick = [F32, HALF, BF]
+    src = Set(sizes, [pick[k] for k in rng.integers(0, 3, count)], rng.integers(0, 8, count), seed=seed,
+              scale=10.0 ** rng.uniform(-3, 1))
+    dst = Set(sizes, [pick[k] for k in rng.integers(0, 3, count)], rng.integers(0, 8, count),
+              seed=1000 + seed)
+    plan = Z.zero_tensor_plan(src.t, out=dst.t)
+    x, y = [host64(t) for t in src.t], [host64(t) for t in dst.t]
+    kind, inv, w = ("l2", "max")[seed % 2], f32(2.0 ** rng.uniform(-6, 2)), f32(rng.uniform(-2, 2))
+    res, norms, ws = make_res(), torch.zeros(count, device="cuda"), workspace(plan)
+    Z.zero_tensor_accumulate(plan, w, res=res, workspace=ws, inv_scale=inv, kind=kind, norms=norms)
+    check_norm(res, norms, [host64(t) for t in dst.t], kind, inv)
+    for t, a, b in zip(dst.t, x, y):
+        assert_rounded(t, w * a + b, t.dtype, 2.0 ** -50 + (0 if t.dtype == F32 else 2.0 ** -24))
+    limit = f32(10.0 ** rng.uniform(-2, 2))
+    each = bool(rng.integers(0, 2))
+    Z.zero_tensor_clip_norm(plan, limit, inv, res, ws, kind=kind, norms=norms, per_tensor=each)
+    check_norm(res, norms, x, kind, inv)
+    total = math.sqrt(Z.read_result(res).sumsq)
+    for t, a, n in zip(dst.t, x, norms.tolist()):
+        assert_rounded(t, clip_want(a, n if each else total, limit, inv), t.dtype, clip_steps(t.dtype))
+    src.assert_guards()
+    dst.assert_guards()
 
 
 def test_clip_norm_matches_torch_clip_grad_norm():
@@ -532,6 +621,8 @@ def test_dense_permutations_and_refusals():
         Z.zero_tensor_plan([base, torch.zeros(3)])
     with pytest.raises(ValueError, match="strided"):
         Z.zero_tensor_plan([torch.eye(3, device="cuda").to_sparse()])
+    with pytest.raises(ValueError, match="negated"):
+        Z.zero_tensor_plan([torch.ones(1, dtype=torch.complex64, device="cuda").conj().imag])
     flat = torch.zeros(100, device="cuda")
     twice = Z.zero_tensor_plan([flat, flat[50:]])         # read only
     res = make_res()

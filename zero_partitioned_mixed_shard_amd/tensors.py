@@ -88,8 +88,9 @@ class zero_tensor_plan:
         # a pass per property: lists of thousands of tensors are common
         sides = []
         for side in ((tensors,) if out is None else (tensors, outs)):
-            if any(t.layout is not torch.strided for t in side):
-                raise ValueError("tensors must be strided (not sparse)")
+            if any(t.layout is not torch.strided or t.is_neg() for t in side):
+                raise ValueError("tensors must be strided (not sparse) and hold their own values "
+                                 "(no negated views)")
             if any(t.get_device() != device.index for t in side):
                 raise ValueError(f"tensors on {device} expected")
             codes = [types.get(t.dtype) for t in side]
