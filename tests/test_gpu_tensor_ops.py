@@ -669,6 +669,30 @@ def test_other_streams():
     Z.zero_tensor_norm(plan, 1.0, res[1], ws[1], stream=streams[1].cuda_stream)
     torch.cuda.synchronize()
     assert all(torch.equal(r, want) for r in res)
+    with torch.cuda.stream(streams[0]):                   # built there, called on the default one
+        plan = Z.zero_tensor_plan(tensors)
+    Z.zero_tensor_norm(plan, 1.0, res[0].zero_(), ws[0])
+    Z.zero_tensor_norm(plan, 1.0, res[1].zero_(), ws[1], stream=0)
+    torch.cuda.synchronize()
+    assert all(torch.equal(r, want) for r in res)
+
+
+def test_no_plan_inside_a_capture():
+    t = torch.ones(1000, device="cuda")
+    plan, res = Z.zero_tensor_plan([t]), make_res()
+    ws, said = workspace(plan), []
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Z.zero_tensor_norm(plan, 1.0, res, ws)
+        try:
+            Z.zero_tensor_plan([t])
+        except RuntimeError as e:
+            said.append(str(e))
+    assert said == ["build the plan before the capture"]
+    for k in (1.0, 2.0, 3.0):                             # the capture is whole
+        t.fill_(k)
+        graph.replay()
+        assert Z.read_result(res).sumsq == 1000.0 * k * k
 
 
 @pytest.mark.parametrize("per_tensor", [False, True])

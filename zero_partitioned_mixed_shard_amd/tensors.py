@@ -32,10 +32,10 @@ _KINDS = {"l2": ZERO_NORM_L2, "max": ZERO_NORM_MAX}
 
 class zero_tensor_plan_t(ctypes.Structure):
     _fields_ = [("n_tensors", ctypes.c_int64), ("numel", ctypes.c_int64),
-                ("bytes", ctypes.c_int64), ("n_pieces", ctypes.c_int64), ("n_runs", ctypes.c_int64),
-                ("n_rests", ctypes.c_int64),
-                ("head_bytes", ctypes.c_int64), ("table_bytes", ctypes.c_int64), ("writable", ctypes.c_int32),
-                ("fp32_out", ctypes.c_int32)]
+                ("bytes", ctypes.c_int64), ("n_pieces", ctypes.c_int64),
+                ("n_runs", ctypes.c_int64), ("n_rests", ctypes.c_int64),
+                ("head_bytes", ctypes.c_int64), ("table_bytes", ctypes.c_int64),
+                ("writable", ctypes.c_int32), ("fp32_out", ctypes.c_int32)]
 
 
 def _order(t):
@@ -66,8 +66,10 @@ class zero_tensor_plan:
     device    the table's device (by default the tensors'; needed for an empty
               list)
 
-    The plan keeps the tensors.  A plan over tensors that overlap can be read
-    only: the calls that write raise ZeroError.
+    The plan keeps the tensors (where calls run on another stream than the tensors'
+    own, keep the plan until that is done).  A plan over tensors that overlap can
+    be read only: the calls that write raise ZeroError.  Building one waits for
+    the current stream.
     """
 
     def __init__(self, tensors: Sequence, out: Optional[Sequence] = None, device=None):
@@ -85,6 +87,8 @@ class zero_tensor_plan:
             raise ValueError("device tensors expected")
         if device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("build the plan before the capture")
         # a pass per property: lists of thousands of tensors are common
         sides = []
         for side in ((tensors,) if out is None else (tensors, outs)):
