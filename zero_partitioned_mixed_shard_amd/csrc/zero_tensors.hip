@@ -410,7 +410,9 @@ __device__ __forceinline__ float clip_factor(float max_norm, double norm, float 
 }
 
 // Elements per lane access of a pass that reads SRC and writes DST: 16 bytes of
-// the wider of the two.
+// the wider of the two, so that a wave's access is one stretch (with 8 elements,
+// two accesses 16 bytes apart on the fp32 side, accumulations into fp32 took 1822
+// us for 1765 and, over ragged tables, 216 for 196).
 template <int SRC, int DST>
 constexpr int kWidth = kBytes<SRC> == 4 || kBytes<DST> == 4 ? 4 : 8;
 
@@ -827,7 +829,8 @@ void* const* dsts_of(const zero_tensor_plan* p, const void* table) {
     return (void* const*)(pieces_of(p, table) + p->n_pieces);
 }
 
-// Partials that the finishing block takes as they are; more are folded first.
+// Partials that the finishing block takes as they are; more are folded first (20,000
+// of them: a norm of 17.0 us, 17.6 with a fold; 40,000: 30.1 without, 28.8 with).
 constexpr int64_t kFinish = 2 * kInFlight * kFinishThreads;
 int64_t fold_blocks(int64_t n) { return n <= kFinish ? 0 : (n + kFoldEach - 1) / kFoldEach; }
 
