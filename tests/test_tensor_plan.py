@@ -190,6 +190,11 @@ def test_binding_refuses_host_tensors():
     for t in (torch.zeros(4), torch.zeros(4, dtype=torch.float64)):
         with pytest.raises(ValueError, match="device"):
             Z.zero_tensor_plan([t])
+    for bad in ([None], [torch.zeros(4), None], [np.zeros(4)]):
+        with pytest.raises(TypeError, match="tensors expected"):
+            Z.zero_tensor_plan(bad)
+    with pytest.raises(TypeError, match="tensors expected"):
+        Z.zero_tensor_plan([torch.zeros(4)], out=[None])
 
 
 def test_dense_orders():

@@ -80,6 +80,8 @@ class zero_tensor_plan:
         n = len(tensors)
         if len(outs) != n:
             raise ValueError("out: one tensor for each tensor")
+        if not all(isinstance(t, torch.Tensor) for t in tensors + ([] if out is None else outs)):
+            raise TypeError("tensors expected (leave parameters without a gradient out of the list)")
         if device is None:
             device = tensors[0].device if tensors else "cuda"
         device = torch.device(device)
