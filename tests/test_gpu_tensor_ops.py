@@ -327,6 +327,23 @@ def test_clip_off_leaves_values(max_norm):
     assert all(torch.equal(t, b) for t, b in zip(out, before))
 
 
+@pytest.mark.parametrize("sizes", [[70, 5], [900] * 12, [9, 70000, 5], [3000] * 1100])
+def test_clip_norm_off_leaves_values(sizes):
+    """In place with a factor of 1, on every path: the same bits, and the norm."""
+    tensors = list(torch.randn(sum(sizes), device="cuda").split(sizes))
+    before = [t.clone() for t in tensors]
+    plan = Z.zero_tensor_plan(tensors)
+    for max_norm in (0.0, 1e9):
+        for norms in (None, torch.zeros(len(sizes), device="cuda")):
+            res = make_res()
+            Z.zero_tensor_clip_norm(plan, max_norm, 1.0, res, workspace(plan), norms=norms,
+                                    per_tensor=norms is not None)
+            assert all(torch.equal(t, b) for t, b in zip(tensors, before))
+            check_norm(res, norms, [host64(t) for t in tensors], "l2", 1.0)
+    Z.zero_tensor_clip_norm(plan, 0.0, 0.5, res, workspace(plan))   # and halved
+    assert all(torch.equal(t, b * 0.5) for t, b in zip(tensors, before))
+
+
 def test_clip_next_to_the_border():
     """Norms a few roundings around max_norm - 1e-6, where the ratio turns from 1 to
     below: in place gives the bits of the same clip into other tensors."""
