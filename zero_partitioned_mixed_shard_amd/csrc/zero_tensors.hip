@@ -53,14 +53,15 @@ constexpr int kPiece = 4096;
 // at 6.73 TB/s, runs by whole blocks at 6.97 (and 10,000 ragged tensors at 6.56
 // with rests by waves, 6.37 by blocks).
 constexpr int kRun = 16384;
-// Consecutive units an XCD gets of each: 6.97 -> 7.12 TB/s at 8 for the norm of
-// 6.7e9 bf16 (2 to 4: 6.83); 4.29 -> 4.37 at 32 for norm and clip of 9.4e8 fp16
-// (2 to 8: 4.16-4.22).
-constexpr int kRunGroup = 8, kPieceGroup = 32;
-// Resident blocks per CU (lds_for_blocks).  Norm: 5 read 6.7e9 bf16 0.5 % faster
-// than 8 and a mixed-type table 1.5 %; 4 another 0.7 %, but 10,000 ragged tensors
-// 1 % slower.  Clip: 9.4e8 bf16 in place take 564 us at 5, 589 at 4, 585 at 8.
-// Accumulation: 3, and 2 for large tables with fp32 outputs (add_blocks).
+// Consecutive units an XCD gets of each.  Norm of 6.7e9 bf16, at 3 blocks per CU:
+// 1800 us at 16, 1828 at 8, 1795 at 32, which costs ragged tables 1 %; at 1 (with
+// 8 blocks per CU) 1937, and 1973 at 2 and 4.  Norm and clip of 9.4e8 fp16: 860 us
+// at 32, 877 at 1, 891-905 at 2 to 8.
+constexpr int kRunGroup = 16, kPieceGroup = 32;
+// Resident blocks per CU (lds_for_blocks).  Clip: 9.4e8 bf16 in place take 564 us
+// at 5, 589 at 4, 585 at 8.  The norm has 5, and 3 for large tables of aligned
+// 16-bit tensors (norm_blocks); accumulation 3, and 2 for large tables with fp32
+// outputs (add_blocks).
 constexpr int kNormBlocksPerCU = 5, kClipBlocksPerCU = 5, kAddBlocksPerCU = 3;
 // Loads of 16 bytes that a lane has in flight in the norm of a run, and of a
 // rest (8 for the runs: 1 % slower; 4 for the rests: the same).
@@ -763,7 +764,7 @@ bool writable(const zero_tensor_entry* entries, int64_t n) {
 constexpr int64_t kMaxPieces = int64_t(1) << 40;
 
 int plan_sizes(const zero_tensor_entry* entries, int64_t n, zero_tensor_plan* plan) {
-    int64_t numel = 0, bytes = 0, fp32_out = 0, pieces = 0, runs = 0, rests = 0;
+    int64_t numel = 0, bytes = 0, fp32_out = 0, aligned16 = 0, pieces = 0, runs = 0, rests = 0;
     for (int64_t k = 0; k < n; ++k) {
         const zero_tensor_entry& e = entries[k];
         if (e.numel < 0 || !valid_table_dtype(e.src_dtype) || !valid_table_dtype(e.dst_dtype))
@@ -783,6 +784,7 @@ int plan_sizes(const zero_tensor_entry* entries, int64_t n, zero_tensor_plan* pl
                                    &bytes))
             return ZERO_ERANGE;
         if (e.dst_dtype == ZERO_FP32) fp32_out += e.numel;
+        if (e.src_dtype != ZERO_FP32 && (uintptr_t)e.src % 16 == 0) aligned16 += e.numel;
         runs += runs_in(e);
         rests += rests_in(e);
     }
@@ -798,6 +800,8 @@ int plan_sizes(const zero_tensor_entry* entries, int64_t n, zero_tensor_plan* pl
                         pieces * (int64_t)sizeof(void*);
     plan->writable = 0;
     plan->fp32_out = fp32_out > numel / 2 ? 1 : 0;
+    plan->aligned16 = numel > 0 && aligned16 >= numel / 8 * 7 ? 1 : 0;
+    plan->reserved = 0;
     return ZERO_OK;
 }
 
@@ -899,12 +903,20 @@ int one_block_impl(const zero_tensor_plan* plan, const void* table, float max_no
                         (int)(accumulate != 0), res, norms);
 }
 
+// Resident blocks per CU of the norm.  Aligned 16-bit tensors: 6.7e9 elements take
+// 1800 us at 3, 1872 at 5, 1886 at 8; 4.4e8 128 and 132; 2.9e8 85.5 and 87.3, 1.4e8
+// the same at both, 7.4e7 26.8 and 26.1.  10,000 packed tensors, whose rows begin
+// anywhere: 363 at 3, 339 at 5; fp32 2-3 % more at 3.
+int norm_blocks(const zero_tensor_plan* p) {
+    return p->aligned16 && p->n_runs >= 16384 ? 3 : kNormBlocksPerCU;
+}
+
 // The partials of the norm, runs first.
 template <int KIND>
 int partials_impl(const zero_tensor_plan* plan, const void* table, double* part, hipStream_t stream) {
     const int64_t n_runs = plan->n_runs, n_rests = plan->n_rests;
     return in_launches(n_runs + (n_rests + kWaves - 1) / kWaves, [&](int64_t b, int64_t grid) {
-        return launch(tensor_norm_kernel<KIND>, grid, lds_for_blocks(kNormBlocksPerCU), stream,
+        return launch(tensor_norm_kernel<KIND>, grid, lds_for_blocks(norm_blocks(plan)), stream,
                       runs_of(plan, table), n_runs, n_rests, b, part);
     });
 }

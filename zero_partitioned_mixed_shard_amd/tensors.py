@@ -35,7 +35,8 @@ class zero_tensor_plan_t(ctypes.Structure):
                 ("bytes", ctypes.c_int64), ("n_pieces", ctypes.c_int64),
                 ("n_runs", ctypes.c_int64), ("n_rests", ctypes.c_int64),
                 ("head_bytes", ctypes.c_int64), ("table_bytes", ctypes.c_int64),
-                ("writable", ctypes.c_int32), ("fp32_out", ctypes.c_int32)]
+                ("writable", ctypes.c_int32), ("fp32_out", ctypes.c_int32),
+                ("aligned16", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 def _order(t):
