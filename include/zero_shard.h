@@ -478,8 +478,8 @@ typedef struct zero_tensor_plan {
                             that is not its own in place; 0: the calls that
                             write refuse this plan (ZERO_EINVAL)              */
     int32_t fp32_out;    /* 1: most elements' outputs are fp32                */
-    int32_t aligned16;   /* 1: at least 7/8 of the elements are in 16-bit
-                            inputs at multiples of 16 bytes                   */
+    int32_t even16;      /* 1: at least 7/8 of the elements are in 16-bit
+                            inputs at multiples of 4 bytes                    */
     int32_t reserved;
 } zero_tensor_plan;
 

@@ -173,6 +173,26 @@ def test_norm_sizes_and_alignments(dt, kind):
 
 
 @pytest.mark.parametrize("kind", ["l2", "max"])
+@pytest.mark.parametrize("dt", [F32, HALF, BF])
+def test_norm_bits_do_not_depend_on_the_place(dt, kind):
+    """The same values at every start in a 16-byte access: the same bits, and nothing
+    read beyond them counts (NaN on both sides)."""
+    sizes = [16384 * 3 + 4099, 16384, 5, 16385]
+    values = [torch.randn(n, device="cuda").to(dt) for n in sizes]
+    first = None
+    for off in range(9):
+        bufs = [torch.full((n + 32,), float("nan"), dtype=dt, device="cuda") for n in sizes]
+        tensors = [b[8 + off:8 + off + n].copy_(v) for b, v, n in zip(bufs, values, sizes)]
+        plan = Z.zero_tensor_plan(tensors)
+        res, norms = make_res(), torch.zeros(len(sizes), device="cuda")
+        Z.zero_tensor_norm(plan, 1.0, res, workspace(plan), kind=kind, norms=norms)
+        if first is None:
+            first = res.clone(), norms.clone()
+            check_norm(res, norms, [host64(v) for v in values], kind, 1.0)
+        assert torch.equal(res, first[0]) and torch.equal(norms, first[1]), off
+
+
+@pytest.mark.parametrize("kind", ["l2", "max"])
 def test_norm_mixed_types_and_empty_tables(kind):
     for sizes in ([], [0], [0, 0, 3], [300, 0, 70001, 1, 0, 16384, 2]):
         types = [(F32, HALF, BF)[k % 3] for k in range(len(sizes))]

@@ -60,8 +60,8 @@ def test_head_counts_every_tensors_parts(seed):
     assert plan.n_tensors == len(rows) and plan.numel == sum(r[2] for r in rows)
     assert plan.bytes == sum(r[2] * (SIZE[r[3]] + SIZE[r[4]]) for r in rows)
     assert plan.fp32_out == (sum(r[2] for r in rows if r[4] == FP32) > plan.numel // 2)
-    even = sum(r[2] for r in rows if r[3] != FP32 and r[0] % 16 == 0)
-    assert plan.aligned16 == (plan.numel > 0 and even >= plan.numel // 8 * 7)
+    even = sum(r[2] for r in rows if r[3] != FP32 and r[0] % 4 == 0)
+    assert plan.even16 == (plan.numel > 0 and even >= plan.numel // 8 * 7)
     assert plan.table_bytes - plan.head_bytes == 16 * (plan.n_runs + plan.n_rests) + 24 * plan.n_pieces
     e, run, rest, piece = head(rows, plan)
     assert (e == entries(rows)[:len(rows)]).all()

@@ -12,7 +12,8 @@
 // element).  Tensors start at any element, so lanes use 16-byte (or 8-byte)
 // accesses that are aligned to the element only, which gfx950 global memory
 // takes as they are; pieces are cut so that all but a tensor's first begin at a
-// multiple of 128 bytes of its output.
+// multiple of 128 bytes of its output, and the norm, whose rate suffers, shifts
+// 16-bit data that begins between dwords (run_norm).
 //
 // Numerics: the squares and their sums are fp64 (the square of an fp32 value
 // is exact there, and the sum cannot overflow), the unscale factor is applied
@@ -78,6 +79,7 @@ typedef __attribute__((address_space(1))) const u32x4_a2 g_cu32x4_a2;
 typedef __attribute__((address_space(1))) u32x4_a2 g_u32x4_a2;
 typedef __attribute__((address_space(1))) const u32x2_a2 g_cu32x2_a2;
 typedef __attribute__((address_space(1))) u32x2_a2 g_u32x2_a2;
+typedef __attribute__((address_space(1))) const uint32_t g_cu32;
 typedef __attribute__((address_space(1))) const uint16_t g_cu16;
 typedef __attribute__((address_space(1))) uint16_t g_u16;
 typedef __attribute__((address_space(1))) const float g_cf32;
@@ -211,6 +213,11 @@ struct Norm {
             m = b > m ? b : m;
         }
     }
+    template <int DT, int W>
+    __device__ __forceinline__ void add(const Raw<DT, W>& r) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) add(r.get(k));
+    }
     __device__ __forceinline__ double value() const {
         return KIND == ZERO_NORM_L2 ? s : (double)__uint_as_float(m);
     }
@@ -245,40 +252,70 @@ __device__ __forceinline__ double block_join(double v) {
     return v;
 }
 
-// Thread t's share, of T, of the norm of a run (WHOLE: exactly kRun elements) or
-// a rest, U loads of 16 bytes in flight.
-template <int KIND, int DT, int T, int U, bool WHOLE>
-__device__ __forceinline__ double span_norm(const void* src, int count, int t) {
+// Thread t's share, of T, of the norm of a rest, U loads of 16 bytes in flight.
+template <int KIND, int DT, int T, int U>
+__device__ __forceinline__ double rest_norm(const void* src, int count, int t) {
     constexpr int W = 16 / kBytes<DT>, R = T * W;
-    static_assert(kRun % (U * R) == 0, "whole batches");
     Norm<KIND> n;
     const int e = t * W;
-    auto add = [&](const Raw<DT, W>(&r)[U]) {
+    for (int b = 0; b < count; b += U * R) {
+        Raw<DT, W> r[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int k = 0; k < W; ++k) n.add(r[u].get(k));
-    };
-    if (WHOLE) {
-#pragma unroll
-        for (int b = 0; b < kRun; b += U * R) {
-            Raw<DT, W> r[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) r[u] = load_raw<DT, W, true>(src, b + e + u * R);
-            add(r);
+        for (int u = 0; u < U; ++u) {
+            r[u].clear();
+            if (b + e + u * R + W <= count) r[u] = load_raw<DT, W, true>(src, b + e + u * R);
         }
-    } else {
-        for (int b = 0; b < count; b += U * R) {
-            Raw<DT, W> r[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) n.add(r[u]);
+    }
+    const int last = count / W * W + t;
+    if (last < count) n.add(load_one<DT>(src, last));
+    return n.value();
+}
+
+// The thread's share of the norm of a run (exactly kRun elements), a block's work: a
+// wave takes kRunLoads rows of 64 accesses, one after the other in memory, in each
+// batch.  ODD: a 16-bit run that begins in the middle of a dword.  Accesses that
+// are not aligned to a dword run at three quarters of the rate (1.07e9 fp16: 390 us,
+// 300 at every other start and this way), so the dwords that hold the elements are
+// read and shifted by one element, which puts every element where it would be
+// otherwise.  A lane's last dword is the next lane's first, the last lane's is the
+// next row's first, and only the batch's last is read for itself.  The dwords at
+// the ends hold an element of the run each, so no access leaves the tensor's
+// dwords.
+template <int KIND, int DT, bool ODD>
+__device__ __forceinline__ double run_norm(const void* src) {
+    constexpr int W = 16 / kBytes<DT>, S = 64 * W, U = kRunLoads, B = kWaves * U * S;
+    static_assert(kRun % B == 0, "whole batches");
+    const int lane = threadIdx.x & 63;
+    g_cbyte* p = (g_cbyte*)src - (ODD ? 2 : 0);
+    const int e = (threadIdx.x >> 6) * U * S + lane * W;
+    Norm<KIND> n;
+#pragma unroll
+    for (int b = 0; b < kRun; b += B) {
+        Raw<DT, W> r[U];
+        uint32_t tail = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) r[u] = load_raw<DT, W, true>((const void*)p, b + e + u * S);
+        if constexpr (ODD) {
+            if (lane == 63) tail = *(g_cu32*)(p + (b + e + (U - 1) * S + W) * 2);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                r[u].clear();
-                if (b + e + u * R + W <= count) r[u] = load_raw<DT, W, true>(src, b + e + u * R);
+                // the next lane's first dword (a DPP wave shift), or the next row's
+                const uint32_t next = (uint32_t)__builtin_amdgcn_update_dpp(
+                    0, (int)r[u].w[0], 0x130 /* wave_shl:1 */, 0xF, 0xF, false);
+                const uint32_t row = u + 1 < U
+                    ? (uint32_t)__builtin_amdgcn_readfirstlane((int)r[u + 1 < U ? u + 1 : u].w[0])
+                    : tail;
+                const uint32_t last = lane == 63 ? row : next;
+#pragma unroll
+                for (int k = 0; k < W / 2; ++k)
+                    r[u].w[k] = __builtin_amdgcn_alignbit(k + 1 < W / 2 ? r[u].w[k + 1] : last,
+                                                          r[u].w[k], 16);
             }
-            add(r);
         }
-        const int last = count / W * W + t;
-        if (last < count) n.add(load_one<DT>(src, last));
+#pragma unroll
+        for (int u = 0; u < U; ++u) n.add(r[u]);
     }
     return n.value();
 }
@@ -294,7 +331,13 @@ tensor_norm_kernel(const Piece* __restrict__ runs, int64_t n_runs, int64_t n_res
         const int64_t i = unit_of<kRunGroup>(b, n_runs);
         const Piece p = runs[i];
         by_type(p.src_dtype(), [&](auto s) {
-            v = span_norm<KIND, decltype(s)::value, kThreads, kRunLoads, true>(p.src, kRun, threadIdx.x);
+            constexpr int DT = decltype(s)::value;
+            if constexpr (DT != ZERO_FP32)
+                if ((uintptr_t)p.src & 2) {
+                    v = run_norm<KIND, DT, true>(p.src);
+                    return;
+                }
+            v = run_norm<KIND, DT, false>(p.src);
         });
         v = block_join<KIND>(v);
         if (threadIdx.x == 0) part[i] = v;
@@ -305,7 +348,7 @@ tensor_norm_kernel(const Piece* __restrict__ runs, int64_t n_runs, int64_t n_res
     const Piece p = runs[n_runs + i];
     const int lane = threadIdx.x & 63;
     by_type(p.src_dtype(), [&](auto s) {
-        v = span_norm<KIND, decltype(s)::value, 64, kRestLoads, false>(p.src, p.count(), lane);
+        v = rest_norm<KIND, decltype(s)::value, 64, kRestLoads>(p.src, p.count(), lane);
     });
     v = wave_join<KIND>(v);
     if (lane == 0) part[n_runs + i] = v;
@@ -544,7 +587,7 @@ tensor_one_block_kernel(const Piece* __restrict__ rests, int n_rests,
     if (w < n_rests) {
         const Piece p = rests[w];
         by_type(p.src_dtype(), [&](auto s) {
-            v = span_norm<KIND, decltype(s)::value, 64, kRestLoads, false>(p.src, p.count(), lane);
+            v = rest_norm<KIND, decltype(s)::value, 64, kRestLoads>(p.src, p.count(), lane);
         });
     }
     v = wave_join<KIND>(v);
@@ -764,7 +807,7 @@ bool writable(const zero_tensor_entry* entries, int64_t n) {
 constexpr int64_t kMaxPieces = int64_t(1) << 40;
 
 int plan_sizes(const zero_tensor_entry* entries, int64_t n, zero_tensor_plan* plan) {
-    int64_t numel = 0, bytes = 0, fp32_out = 0, aligned16 = 0, pieces = 0, runs = 0, rests = 0;
+    int64_t numel = 0, bytes = 0, fp32_out = 0, even16 = 0, pieces = 0, runs = 0, rests = 0;
     for (int64_t k = 0; k < n; ++k) {
         const zero_tensor_entry& e = entries[k];
         if (e.numel < 0 || !valid_table_dtype(e.src_dtype) || !valid_table_dtype(e.dst_dtype))
@@ -784,7 +827,7 @@ int plan_sizes(const zero_tensor_entry* entries, int64_t n, zero_tensor_plan* pl
                                    &bytes))
             return ZERO_ERANGE;
         if (e.dst_dtype == ZERO_FP32) fp32_out += e.numel;
-        if (e.src_dtype != ZERO_FP32 && (uintptr_t)e.src % 16 == 0) aligned16 += e.numel;
+        if (e.src_dtype != ZERO_FP32 && (uintptr_t)e.src % 4 == 0) even16 += e.numel;
         runs += runs_in(e);
         rests += rests_in(e);
     }
@@ -800,7 +843,7 @@ int plan_sizes(const zero_tensor_entry* entries, int64_t n, zero_tensor_plan* pl
                         pieces * (int64_t)sizeof(void*);
     plan->writable = 0;
     plan->fp32_out = fp32_out > numel / 2 ? 1 : 0;
-    plan->aligned16 = numel > 0 && aligned16 >= numel / 8 * 7 ? 1 : 0;
+    plan->even16 = numel > 0 && even16 >= numel / 8 * 7 ? 1 : 0;
     plan->reserved = 0;
     return ZERO_OK;
 }
@@ -903,12 +946,12 @@ int one_block_impl(const zero_tensor_plan* plan, const void* table, float max_no
                         (int)(accumulate != 0), res, norms);
 }
 
-// Resident blocks per CU of the norm.  Aligned 16-bit tensors: 6.7e9 elements take
-// 1800 us at 3, 1872 at 5, 1886 at 8; 4.4e8 128 and 132; 2.9e8 85.5 and 87.3, 1.4e8
-// the same at both, 7.4e7 26.8 and 26.1.  10,000 packed tensors, whose rows begin
-// anywhere: 363 at 3, 339 at 5; fp32 2-3 % more at 3.
+// Resident blocks per CU of the norm.  16-bit tensors that begin at a dword: 6.7e9
+// elements take 1800 us at 3, 1872 at 5, 1886 at 8; 4.4e8 127 and 131; 1.4e8 the same
+// at 3 and 5, and below 2e8 3 gains nothing.  10,000 packed tensors, half of which
+// begin between dwords: 333 at 3, 314 at 5; fp32 1 % more at 3.
 int norm_blocks(const zero_tensor_plan* p) {
-    return p->aligned16 && p->n_runs >= 16384 ? 3 : kNormBlocksPerCU;
+    return p->even16 && p->n_runs >= 16384 ? 3 : kNormBlocksPerCU;
 }
 
 // The partials of the norm, runs first.
