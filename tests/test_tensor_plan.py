@@ -137,6 +137,30 @@ def test_init_refusals():
         assert L.zero_tensor_plan_expand(*args, None) == Z.ZERO_EINVAL
 
 
+def test_head_refuses_another_plans_entries():
+    """Entries with the same counts as the plan's but not its: types, starts, and outputs
+    that overlap (a plan that may be written through would stand for them)."""
+    L = Z.lib()
+    mine = [(4096, 8192, 100, FP16, FP16), (4400, 12288, 100, FP16, FP16)]
+    rc, plan = init(mine)
+    assert rc == Z.ZERO_OK and plan.writable == 1 and plan.even16 == 1
+    buf = np.zeros(plan.head_bytes, np.uint8)
+
+    def refused(rows):
+        return L.zero_tensor_plan_head(entries(rows).ctypes.data, ctypes.byref(plan),
+                                       buf.ctypes.data) == Z.ZERO_EINVAL and not buf.any()
+
+    assert refused([mine[0], (4400, 8200, 100, FP16, FP16)])              # outputs overlap
+    assert refused([mine[0], (8192, 12288, 100, FP16, FP16)])             # an input under an output
+    assert refused([(4098, *mine[0][1:]), mine[1]])                       # starts between dwords
+    assert refused([(4096, 8192, 100, FP16, FP32), mine[1]])              # another type
+    assert refused([(4096, 8192, 99, FP16, FP16), mine[1]])               # another size
+    plan.n_tensors = 1 << 24
+    assert refused(mine)
+    plan.n_tensors = 2
+    assert not refused(mine) and buf.any()
+
+
 def test_workspace_bytes():
     assert Z.lib().zero_tensor_workspace_bytes(None) == 0
     for rows in ([], [(4096, 4096, 1, FP16, FP16)], [(4096, 4096, 1 << 33, FP16, FP16)],

@@ -776,7 +776,9 @@ bool span_of(const void* p, int64_t numel, int32_t dtype, Span* s) {
 }
 
 bool overlaps(const std::vector<Span>& sorted, const Span& s) {
-    // `sorted`: disjoint spans in order; the first that ends after s begins
+    // `sorted`: disjoint spans in order; most inputs lie beyond all outputs, others are
+    // compared with the first that ends after s begins
+    if (sorted.empty() || s.end <= sorted.front().begin || sorted.back().end <= s.begin) return false;
     auto it = std::upper_bound(sorted.begin(), sorted.end(), s.begin,
                                [](uintptr_t a, const Span& b) { return a < b.end; });
     return it != sorted.end() && it->begin < s.end;
@@ -791,7 +793,8 @@ bool writable(const zero_tensor_entry* entries, int64_t n) {
     for (int64_t k = 0; k < n; ++k)
         if (entries[k].numel > 0 && span_of(entries[k].dst, entries[k].numel, entries[k].dst_dtype, &s))
             out.push_back(s);
-    std::sort(out.begin(), out.end(), [](const Span& a, const Span& b) { return a.begin < b.begin; });
+    const auto before = [](const Span& a, const Span& b) { return a.begin < b.begin; };
+    if (!std::is_sorted(out.begin(), out.end(), before)) std::sort(out.begin(), out.end(), before);
     for (size_t k = 1; k < out.size(); ++k)
         if (out[k].begin < out[k - 1].end) return false;
     for (int64_t k = 0; k < n; ++k) {
@@ -806,7 +809,7 @@ bool writable(const zero_tensor_entry* entries, int64_t n) {
 // size computed from them.
 constexpr int64_t kMaxPieces = int64_t(1) << 40;
 
-int plan_sizes(const zero_tensor_entry* entries, int64_t n, zero_tensor_plan* plan) {
+int plan_of(const zero_tensor_entry* entries, int64_t n, zero_tensor_plan* plan) {
     int64_t numel = 0, bytes = 0, fp32_out = 0, even16 = 0, pieces = 0, runs = 0, rests = 0;
     for (int64_t k = 0; k < n; ++k) {
         const zero_tensor_entry& e = entries[k];
@@ -841,10 +844,14 @@ int plan_sizes(const zero_tensor_entry* entries, int64_t n, zero_tensor_plan* pl
                         15) / 16 * 16;
     plan->table_bytes = plan->head_bytes + (pieces + runs + rests) * (int64_t)sizeof(Piece) +
                         pieces * (int64_t)sizeof(void*);
-    plan->writable = 0;
     plan->fp32_out = fp32_out > numel / 2 ? 1 : 0;
     plan->even16 = numel > 0 && even16 >= numel / 8 * 7 ? 1 : 0;
     plan->reserved = 0;
+    try {
+        plan->writable = writable(entries, n) ? 1 : 0;
+    } catch (const std::bad_alloc&) {
+        return ZERO_ERANGE;
+    }
     return ZERO_OK;
 }
 
@@ -1050,25 +1057,20 @@ int zero_tensor_plan_init(const zero_tensor_entry* entries, int64_t n_tensors,
                           zero_tensor_plan* plan) {
     if (!plan || n_tensors < 0 || (n_tensors > 0 && !entries)) return ZERO_EINVAL;
     if (n_tensors >= kMaxTensors) return ZERO_ERANGE;
-    const int rc = plan_sizes(entries, n_tensors, plan);
-    if (rc != ZERO_OK) return rc;
-    try {
-        plan->writable = writable(entries, n_tensors) ? 1 : 0;
-    } catch (const std::bad_alloc&) {
-        return ZERO_ERANGE;
-    }
-    return ZERO_OK;
+    return plan_of(entries, n_tensors, plan);
 }
 
 int zero_tensor_plan_head(const zero_tensor_entry* entries, const zero_tensor_plan* plan,
                           void* head) {
     if (!plan || !head || plan->n_tensors < 0 || (plan->n_tensors > 0 && !entries)) return ZERO_EINVAL;
     zero_tensor_plan again;
-    const int rc = plan_sizes(entries, plan->n_tensors, &again);
+    if (plan->n_tensors >= kMaxTensors) return ZERO_EINVAL;
+    const int rc = plan_of(entries, plan->n_tensors, &again);
     if (rc != ZERO_OK) return rc;
-    if (again.n_pieces != plan->n_pieces || again.n_runs != plan->n_runs ||
-        again.n_rests != plan->n_rests || again.head_bytes != plan->head_bytes)
-        return ZERO_EINVAL;
+    // whole: equal counts alone would let a plan that may be written through stand
+    // for entries whose outputs overlap
+    static_assert(sizeof(zero_tensor_plan) == 80, "no padding");
+    if (memcmp(&again, plan, sizeof again) != 0) return ZERO_EINVAL;
     const int64_t n = plan->n_tensors;
     memset(head, 0, (size_t)plan->head_bytes);
     if (n > 0) memcpy(head, entries, (size_t)n * sizeof(zero_tensor_entry));
