@@ -570,7 +570,7 @@ tensor_join_clip_kernel(const Piece* __restrict__ pieces, void* const* __restric
 }
 
 // Norm, each tensor's norm and (CLIP) the clip of a table of at most kOneBlock
-// rests and no run, in one block, which joins in the order of
+// rests and no run (and, with norms, few tensors), in one block, which joins in the order of
 // tensor_finish_kernel (a wave's tree over at most 64 partials), so to the same
 // bits.
 constexpr int kOneBlock = kFinishThreads / 64;       // a wave for each rest
@@ -938,9 +938,18 @@ int finish(int64_t n, const int64_t* first, const int64_t* first2, int64_t n_ten
 // Whether a table's norm takes one block (16 tensors of 4096 fp32: 6.1 us against
 // 8.8 for two launches), and its norm and clip together, which that block does
 // one piece after the other (4: 6.6 us against 8.7, 8: 8.8, 16: 13.3 against 8.6).
+// Its 16 waves take the tensors' own norms in turn, so these are few too (empty tensors
+// count here alone).  Norm and every tensor's of 128 of which one holds elements: 7.6
+// us against 9.0, 256: 12.1 against 8.7, 200,000: 8250 against 45; with the clip 8.5
+// against 12.5, and 13.1 against 12.4 at 256.
 constexpr int kOneBlockPieces = 4;
-bool one_block(const zero_tensor_plan* p) { return p->n_runs == 0 && p->n_rests <= kOneBlock; }
-bool one_block_clip(const zero_tensor_plan* p) { return one_block(p) && p->n_pieces <= kOneBlockPieces; }
+constexpr int64_t kOneBlockTensors = 128;
+bool one_block(const zero_tensor_plan* p, const float* norms) {
+    return p->n_runs == 0 && p->n_rests <= kOneBlock && (!norms || p->n_tensors <= kOneBlockTensors);
+}
+bool one_block_clip(const zero_tensor_plan* p, const float* norms) {
+    return one_block(p, norms) && p->n_pieces <= kOneBlockPieces;
+}
 
 template <int KIND, bool CLIP>
 int one_block_impl(const zero_tensor_plan* plan, const void* table, float max_norm,
@@ -975,7 +984,7 @@ template <int KIND>
 int norm_impl(const zero_tensor_plan* plan, const void* table, float inv_scale,
               const zero_step_control* ctl, int32_t accumulate, zero_step_result* res, float* norms,
               double* part, hipStream_t stream) {
-    if (one_block(plan))
+    if (one_block(plan, norms))
         return one_block_impl<KIND, false>(plan, table, 0.0f, 0, inv_scale, ctl, accumulate, res, norms,
                                            stream);
     const int rc = partials_impl<KIND>(plan, table, part, stream);
@@ -1004,7 +1013,7 @@ template <int KIND>
 int clip_norm_impl(const zero_tensor_plan* plan, const void* table, float max_norm, float inv_scale,
                    const zero_step_control* ctl, zero_step_result* res, float* norms,
                    int32_t per_tensor, double* part, hipStream_t stream) {
-    if (one_block_clip(plan))
+    if (one_block_clip(plan, norms))
         return one_block_impl<KIND, true>(plan, table, max_norm, per_tensor, inv_scale, ctl, 0, res,
                                           norms, stream);
     const int64_t n = plan->n_runs + plan->n_rests;
