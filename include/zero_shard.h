@@ -480,7 +480,7 @@ typedef struct zero_tensor_plan {
     int32_t fp32_out;    /* 1: most elements' outputs are fp32                */
     int32_t even16;      /* 1: at least 7/8 of the elements are in 16-bit
                             inputs at multiples of 4 bytes                    */
-    int32_t reserved;
+    int32_t largest;     /* elements of the largest tensor / 4096 (at most INT32_MAX)  */
 } zero_tensor_plan;
 
 enum zero_norm_kind {

@@ -889,3 +889,57 @@ def test_many_empty_tensors_are_not_one_blocks_work():
     ms = call_ms(lambda: Z.zero_tensor_clip_norm(plan, 1e9, 1.0, res, ws, norms=norms,
                                                  per_tensor=True))
     assert bool((tensors[-1] == 2.0).all()) and ms < 2.0
+
+
+@pytest.mark.parametrize("kind", ["l2", "max"])
+@pytest.mark.parametrize("few", [3, 128, 129, 600])
+def test_tensors_of_many_partials(few, kind):
+    """A tensor of over 1024 partials, whose norm a block joins where there are few tensors
+    and a wave otherwise (1027 partials of the norm and 4108 of the accumulation: up to
+    128 and 513 tensors): every call that gives norms, against 64 bits."""
+    sizes = [5] * few
+    sizes[1], sizes[-1] = 1027 * 16384 + 4099, 0
+    flat = torch.randn(sum(sizes) + 1, generator=torch.Generator(device="cuda").manual_seed(few),
+                       device="cuda").to(BF)[1:]
+    tensors = list(flat.split(sizes))
+    host = [host64(t) for t in tensors]
+    out = torch.zeros(sum(sizes), device="cuda")
+    plan = Z.zero_tensor_plan(tensors, out=list(out.split(sizes)))
+    ws, inv = workspace(plan), f32(0.3)
+    res, norms = make_res(), torch.full((few,), -1.0, device="cuda")
+    Z.zero_tensor_norm(plan, inv, res, ws, kind=kind, norms=norms)
+    check_norm(res, norms, host, kind, inv)
+    again, each = make_res(), torch.full((few,), -1.0, device="cuda")
+    Z.zero_tensor_clip_norm(plan, 0.5, inv, again, ws, kind=kind, norms=each, per_tensor=True)
+    assert torch.equal(again, res) and torch.equal(each, norms)
+    for y, x, n in zip(out.split(sizes), host, each.tolist()):
+        assert_rounded(y, clip_want(x, n, 0.5, inv), F32, clip_steps(F32))
+    Z.zero_tensor_accumulate(plan, 1.0, overwrite=True, res=res, workspace=ws, inv_scale=inv,
+                             kind=kind, norms=norms)
+    assert torch.equal(out, flat.float())
+    check_norm(res, norms, host, kind, inv)
+    flat[sizes[0] + 12_345_678] = float("nan")
+    Z.zero_tensor_norm(plan, inv, res, ws, kind=kind, norms=norms)
+    assert Z.read_result(res).overflow == 1
+    assert [k for k, x in enumerate(norms.tolist()) if not math.isfinite(x)] == [1]
+
+
+def test_a_large_tensor_beside_many_small_ones():
+    """The norms of 4.3e9 elements (262,144 partials, 1,048,576 of the accumulation) beside
+    5000 tensors: joined by blocks, though the average tensor has few partials."""
+    n, few = 1 << 32, 5000
+    if torch.cuda.mem_get_info()[0] < 2 * n + (4 << 30):
+        pytest.skip("not enough device memory")
+    flat = torch.zeros(n + 64 * few, dtype=BF, device="cuda")
+    flat[5], flat[n - 1], flat[n], flat[-1] = 3.0, -4.0, 12.0, 2.0
+    plan = Z.zero_tensor_plan(list(flat.split([n] + [64] * few)))
+    ws = workspace(plan)
+    for add, scale in ((False, 1.0), (True, 2.0)):
+        res, norms = make_res(), torch.full((few + 1,), -1.0, device="cuda")
+        if add:
+            Z.zero_tensor_accumulate(plan, 1.0, res=res, workspace=ws, norms=norms)
+        else:
+            Z.zero_tensor_norm(plan, 1.0, res, ws, norms=norms)
+        assert Z.read_result(res).sumsq == 173.0 * scale * scale
+        assert [norms[k].item() / scale for k in (0, 1, -1)] == [5.0, 12.0, 2.0]
+        assert not norms[2:-1].any()

@@ -84,6 +84,15 @@ def test_large_tensors():
     assert (plan.n_runs, plan.n_rests) == (n // 16384, 1) and plan.n_pieces == (1 << 24) + 1
 
 
+def test_largest_tensor():
+    """The largest tensor decides how the tensors' norms are joined."""
+    for numels in ([], [0], [4095], [5, 1 << 30, 70000, 0], [1 << 40], [1 << 45, 1 << 44]):
+        rows = [(1 << 50, (k + 1) << 51, n, BF16, BF16) for k, n in enumerate(numels)]
+        rc, plan = init(rows)
+        assert rc == Z.ZERO_OK
+        assert plan.largest == min(max(numels, default=0) // 4096, 2 ** 31 - 1)
+
+
 @pytest.mark.parametrize("rows,writable", [
     ([(4096, 4096, 10, FP16, FP16)], 1),                                   # in place
     ([(4096, 4096, 10, FP16, BF16)], 0),                                   # in place, other type

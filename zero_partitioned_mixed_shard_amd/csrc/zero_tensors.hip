@@ -810,7 +810,7 @@ bool writable(const zero_tensor_entry* entries, int64_t n) {
 constexpr int64_t kMaxPieces = int64_t(1) << 40;
 
 int plan_of(const zero_tensor_entry* entries, int64_t n, zero_tensor_plan* plan) {
-    int64_t numel = 0, bytes = 0, fp32_out = 0, even16 = 0, pieces = 0, runs = 0, rests = 0;
+    int64_t numel = 0, bytes = 0, fp32_out = 0, even16 = 0, pieces = 0, runs = 0, rests = 0, largest = 0;
     for (int64_t k = 0; k < n; ++k) {
         const zero_tensor_entry& e = entries[k];
         if (e.numel < 0 || !valid_table_dtype(e.src_dtype) || !valid_table_dtype(e.dst_dtype))
@@ -833,6 +833,7 @@ int plan_of(const zero_tensor_entry* entries, int64_t n, zero_tensor_plan* plan)
         if (e.src_dtype != ZERO_FP32 && (uintptr_t)e.src % 4 == 0) even16 += e.numel;
         runs += runs_in(e);
         rests += rests_in(e);
+        largest = std::max(largest, e.numel / kPiece);
     }
     plan->n_tensors = n;
     plan->numel = numel;
@@ -846,7 +847,7 @@ int plan_of(const zero_tensor_entry* entries, int64_t n, zero_tensor_plan* plan)
                         pieces * (int64_t)sizeof(void*);
     plan->fp32_out = fp32_out > numel / 2 ? 1 : 0;
     plan->even16 = numel > 0 && even16 >= numel / 8 * 7 ? 1 : 0;
-    plan->reserved = 0;
+    plan->largest = (int32_t)std::min<int64_t>(largest, INT32_MAX);
     try {
         plan->writable = writable(entries, n) ? 1 : 0;
     } catch (const std::bad_alloc&) {
@@ -912,16 +913,22 @@ int norm_args(const zero_tensor_plan* plan, const void* table, int32_t kind, flo
     return ZERO_OK;
 }
 
-// Joins the n partials at the workspace's start into *res and norms.
+// Joins the n partials at the workspace's start into *res and norms; `most`: those of
+// the largest tensor.
 template <int KIND>
-int finish(int64_t n, const int64_t* first, const int64_t* first2, int64_t n_tensors, float inv_scale,
-           const zero_step_control* ctl, int32_t accumulate, zero_step_result* res, float* norms,
-           double* part, hipStream_t stream) {
+int finish(int64_t n, int64_t most, const int64_t* first, const int64_t* first2, int64_t n_tensors,
+           float inv_scale, const zero_step_control* ctl, int32_t accumulate, zero_step_result* res,
+           float* norms, double* part, hipStream_t stream) {
     const double* last = part;
     const int64_t nt = norms ? n_tensors : 0;
-    // a block for each tensor, or a wave: one tensor of 2.7e8 elements 84 us against
-    // 92, 32 of 6.7e7 624 against 631, the same where a tensor has fewer partials
-    const bool wide = n / 1024 > nt;
+    // A block for each tensor, or a wave.  A wave takes 1024 of a tensor's partials a round
+    // (0.5 us each), so the largest tensor decides; blocks take 3.6 us more per 1000
+    // tensors.  Norm with each tensor's, block and wave: 1.1e9 bf16 beside 100 tensors
+    // of 64: 299 and 334 us, beside 5000: 318 and 337, beside 20,000: 388 and 346; 2.7e8
+    // beside 1000: 81 and 87; 6.7e7 beside 1000: 26.9 and 25.2.  (The last condition: a
+    // launch's threads are counted in 32 bits.)
+    const bool wide = most > 1024 && most > 8 * nt &&
+                      nt < kMaxLaunchBlocks / (kFinishThreads / kThreads);
     if (const int64_t blocks = fold_blocks(n)) {
         const int rc = launch(tensor_fold_kernel<KIND>, blocks, 0, stream, part, n, part + n);
         if (rc != ZERO_OK) return rc;
@@ -989,9 +996,9 @@ int norm_impl(const zero_tensor_plan* plan, const void* table, float inv_scale,
                                            stream);
     const int rc = partials_impl<KIND>(plan, table, part, stream);
     if (rc != ZERO_OK) return rc;
-    return finish<KIND>(plan->n_runs + plan->n_rests, first_runs_of(plan, table),
-                        first_rests_of(plan, table), plan->n_tensors, inv_scale, ctl, accumulate, res,
-                        norms, part, stream);
+    return finish<KIND>(plan->n_runs + plan->n_rests, plan->largest / (kRun / kPiece),
+                        first_runs_of(plan, table), first_rests_of(plan, table), plan->n_tensors,
+                        inv_scale, ctl, accumulate, res, norms, part, stream);
 }
 
 // Whether a table is larger than the last-level cache (256 MB): the clip then
@@ -1054,8 +1061,8 @@ int accumulate_norm_impl(const zero_tensor_plan* plan, const void* table, float 
                          hipStream_t stream) {
     const int rc = accumulate_impl<KIND>(plan, table, weight, overwrite, part, stream);
     if (rc != ZERO_OK) return rc;
-    return finish<KIND>(plan->n_pieces, first_pieces_of(plan, table), nullptr, plan->n_tensors,
-                        inv_scale, ctl, accumulate, res, norms, part, stream);
+    return finish<KIND>(plan->n_pieces, plan->largest, first_pieces_of(plan, table), nullptr,
+                        plan->n_tensors, inv_scale, ctl, accumulate, res, norms, part, stream);
 }
 
 }  // namespace

@@ -36,7 +36,7 @@ class zero_tensor_plan_t(ctypes.Structure):
                 ("n_runs", ctypes.c_int64), ("n_rests", ctypes.c_int64),
                 ("head_bytes", ctypes.c_int64), ("table_bytes", ctypes.c_int64),
                 ("writable", ctypes.c_int32), ("fp32_out", ctypes.c_int32),
-                ("even16", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+                ("even16", ctypes.c_int32), ("largest", ctypes.c_int32)]
 
 
 def _order(t):
