@@ -232,6 +232,38 @@ def test_binding_refuses_host_tensors():
         Z.zero_tensor_plan([torch.zeros(4)], out=[None])
 
 
+@pytest.mark.parametrize("capturing", [0, 1, 2])
+def test_no_plan_inside_a_capture_on_either_device(monkeypatch, capturing):
+    """A plan for device 1 built with device 0 current: refused where the current stream
+    of either captures, not for another device's."""
+    import torch
+    current = [0]
+
+    class device:
+        def __init__(self, d):
+            self.d = torch.device(d).index
+
+        def __enter__(self):
+            self.was, current[0] = current[0], self.d
+
+        def __exit__(self, *exc):
+            current[0] = self.was
+
+    class Built(Exception):
+        pass
+
+    def build(*args, **kw):
+        raise Built
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: current[0] == capturing)
+    monkeypatch.setattr(torch.cuda, "current_stream", build)
+    want = Built if capturing == 2 else RuntimeError
+    with pytest.raises(want, match=None if capturing == 2 else "before the capture"):
+        Z.zero_tensor_plan([], device="cuda:1")
+    assert current == [0]
+
+
 def test_dense_orders():
     import torch
     x = torch.zeros(4, 6, 5)

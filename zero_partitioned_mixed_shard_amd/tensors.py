@@ -90,8 +90,12 @@ class zero_tensor_plan:
             raise ValueError("device tensors expected")
         if device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("build the plan before the capture")
+        # neither in a capture on the plan's device, whose stream it works on and waits
+        # for, nor in one on the current device, which an allocation may break
+        capturing = torch.cuda.is_current_stream_capturing()
+        with torch.cuda.device(device):
+            if capturing or torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("build the plan before the capture")
         # a pass per property: lists of thousands of tensors are common
         sides = []
         for side in ((tensors,) if out is None else (tensors, outs)):
