@@ -12,6 +12,7 @@ smallest step):
           to the output's type (for fp32 the product's is that one)
   add     one fused multiply-add in fp32: 2^-24, then one to the output's type
 """
+import ctypes
 import math
 import struct
 
@@ -943,3 +944,40 @@ def test_a_large_tensor_beside_many_small_ones():
         assert Z.read_result(res).sumsq == 173.0 * scale * scale
         assert [norms[k].item() / scale for k in (0, 1, -1)] == [5.0, 12.0, 2.0]
         assert not norms[2:-1].any()
+
+
+def test_a_stream_destroyed_before_the_plan():
+    """Calls on a stream that the caller made, by its handle and as torch's current
+    stream, which is then destroyed: the plan goes later, and its memory is used again."""
+    paths = [ln.split()[-1] for ln in open("/proc/self/maps") if "libamdhip64" in ln]
+    hip = ctypes.CDLL(paths[0])
+    hip.hipStreamDestroy.argtypes = [ctypes.c_void_p]
+    tensors = [torch.randn(n, device="cuda") for n in (100, 300_001, 7)]
+    plan, want = Z.zero_tensor_plan(tensors), make_res()
+    Z.zero_tensor_norm(plan, 1.0, want, workspace(plan))
+    recorded = []
+    plan.table.record_stream = recorded.append
+    res, ws = make_res(), workspace(plan)
+    torch.cuda.synchronize()
+    handles = [ctypes.c_void_p() for _ in range(2)]
+    for handle in handles:
+        assert hip.hipStreamCreateWithFlags(ctypes.byref(handle), 1) == 0    # non-blocking
+    for external, handle in enumerate(handles):
+        res.zero_()
+        torch.cuda.synchronize()
+        if external:
+            with torch.cuda.stream(torch.cuda.ExternalStream(handle.value)):
+                Z.zero_tensor_norm(plan, 1.0, res, ws)
+        else:
+            Z.zero_tensor_norm(plan, 1.0, res, ws, stream=handle.value)
+        torch.cuda.synchronize()
+        assert torch.equal(res, want)
+        assert not recorded                               # before the stream is gone
+        assert hip.hipStreamDestroy(handle) == 0
+    side = torch.cuda.Stream()                            # torch's own is recorded, once
+    for _ in range(2):
+        Z.zero_tensor_norm(plan, 1.0, res, ws, stream=side)
+    side.synchronize()
+    assert recorded == [side] and torch.equal(res, want)
+    del plan
+    assert bool((torch.zeros(4096, dtype=torch.uint8, device="cuda") == 0).all())

@@ -264,6 +264,42 @@ def test_no_plan_inside_a_capture_on_either_device(monkeypatch, capturing):
     assert current == [0]
 
 
+def test_a_callers_streams_are_not_recorded(monkeypatch):
+    """torch's allocator uses the streams recorded for the table when the plan goes, and
+    a stream that the caller made may be gone by then: torch's own are recorded, once
+    each, handles and streams around handles are not."""
+    import torch
+    from types import SimpleNamespace as NS
+
+    dev = torch.device("cuda", 0)
+
+    def stream(handle, stream_id):
+        return NS(device=dev, cuda_stream=handle, stream_id=stream_id)
+
+    default, pool, other = stream(0, 0), stream(0x5000, 35), stream(0x5100, 67)
+    external = stream(0x6000, 0x6000)                     # as torch.cuda.ExternalStream
+    current, seen, ran = [default], [], []
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: current[0].cuda_stream)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: current[0])
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda d=None: default)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda raw, device: stream(raw, raw))
+    plan = object.__new__(Z.zero_tensor_plan)
+    plan.device, plan._index, plan._args, plan._streams = dev, 0, (), {0x4000}
+    plan.table = NS(record_stream=lambda s: seen.append(s.cuda_stream))
+
+    def call(s, now=default):
+        current[0] = now
+        plan._call(lambda raw: ran.append(raw) or 0, (), s)
+
+    for s, now in ((None, default), (pool, default), (0x5000, default), (None, other),
+                   (external, default), (None, external), (0x7000, default), (0x7000, other),
+                   (0, pool), (default, pool), (stream(0x7000, 99), default)):
+        call(s, now)                                      # the last: the handle is torch's now
+    assert ran == [0, 0x5000, 0x5000, 0x5100, 0x6000, 0x6000, 0x7000, 0x7000, 0, 0, 0x7000]
+    assert seen == [0, 0x5000, 0x5100, 0x7000]
+
+
 def test_dense_orders():
     import torch
     x = torch.zeros(4, 6, 5)

@@ -67,10 +67,12 @@ class zero_tensor_plan:
     device    the table's device (by default the tensors'; needed for an empty
               list)
 
-    The plan keeps the tensors (where calls run on another stream than the tensors'
-    own, keep the plan until that is done).  A plan over tensors that overlap can
-    be read only: the calls that write raise ZeroError.  Building one waits for
-    the current stream.
+    The plan keeps the tensors.  A plan over tensors that overlap can be read only:
+    the calls that write raise ZeroError.  Building one waits for the current stream.
+
+    Calls do not tell torch's allocator what they use on which stream: where a call
+    runs on another stream than a tensor's own, keep the plan, and the call's res,
+    norms, workspace and ctl, until that call is done.
     """
 
     def __init__(self, tensors: Sequence, out: Optional[Sequence] = None, device=None):
@@ -152,9 +154,7 @@ class zero_tensor_plan:
                 raise ValueError(f"a stream of {self.device} expected")
             raw = stream.cuda_stream
         if raw not in self._streams:
-            # the table is the plan's own: its memory stays until that stream is done
-            self.table.record_stream(torch.cuda.ExternalStream(raw, device=self.device))
-            self._streams.add(raw)
+            self._keep_table(raw, stream)
         if torch._C._cuda_getDevice() == self._index:
             rc = fn(*self._args, *args, raw)
         else:
@@ -162,6 +162,22 @@ class zero_tensor_plan:
                 rc = fn(*self._args, *args, raw)
         if rc != ZERO_OK:
             _check(rc, fn.__name__)
+
+    def _keep_table(self, raw: int, stream) -> None:
+        """On a call's first use of a stream: the table is the plan's own, so its memory
+        stays until that stream is done.  Only for torch's streams, which live for ever:
+        the record is used when the table is freed, and a stream of the caller's making
+        may have been destroyed by then (and its handle be another stream's)."""
+        import torch
+        if raw == 0:
+            stream = torch.cuda.default_stream(self.device)
+        elif stream is None or isinstance(stream, int):
+            stream = torch.cuda.current_stream(self.device)
+        # a handle that is not the current stream's, or a stream around a handle, whose
+        # id the handle is, is the caller's
+        if stream.cuda_stream == raw and (raw == 0 or stream.stream_id != raw):
+            self.table.record_stream(stream)
+            self._streams.add(raw)
 
     def _buffer(self, t, nbytes: int, name: str) -> int:
         if t.device != self.device:
