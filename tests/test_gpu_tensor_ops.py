@@ -981,3 +981,51 @@ def test_a_stream_destroyed_before_the_plan():
     assert recorded == [side] and torch.equal(res, want)
     del plan
     assert bool((torch.zeros(4096, dtype=torch.uint8, device="cuda") == 0).all())
+
+
+@pytest.mark.parametrize("per_tensor", [False, True])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_clip_of_tables_beyond_the_cache(in_place, per_tensor):
+    """Tables of over 256 MiB have a kernel of their own: every type pair, ragged sizes and
+    starts give the bits of small plans over the same tensors, the guards stay, a
+    skipped step writes nothing, and so does a factor of 1 in place."""
+    large = [5_000_001, 70, 4_500_017, 16385, 3_999_999, 4_194_309, 6_000_007, 4_100_003,
+             4_194_304, 6_500_003, 5_500_012, 5_300_005, 4_096_000, 4_800_008, 4_700_003]
+    sizes = [n for pair in zip(SIZES, large + SIZES) for n in pair] + [0, 5_100_001]
+    count = len(sizes)
+    pick = [F32, HALF, BF]
+    s = Set(sizes, [pick[k % 3] for k in range(count)], [k % 8 for k in range(count)], seed=19)
+    if in_place:
+        o = s
+        plan = Z.zero_tensor_plan(s.t)
+    else:
+        o = Set(sizes, [pick[k // 3 % 3] for k in range(count)], [(5 * k + 1) % 8 for k in range(count)],
+                seed=20)
+        plan = Z.zero_tensor_plan(s.t, out=o.t)
+    assert plan.c.bytes > 256 << 20
+    inv, max_norm = f32(0.7), f32(0.9)
+    norms = torch.rand(count, generator=torch.Generator(device="cuda").manual_seed(21),
+                       device="cuda") * 2.0
+    given = norms if per_tensor else None
+    before = [t.clone() for t in o.t]
+    Z.zero_tensor_clip(plan, max_norm, make_res(1.5625, 1, inv), norms=given)
+    assert all(torch.equal(t, b) for t, b in zip(o.t, before))
+    if in_place:
+        for off in (0.0, 100.0):
+            Z.zero_tensor_clip(plan, off, make_res(1.5625, 0, 1.0), norms=given)
+            assert all(torch.equal(t, b) for t, b in zip(o.t, before))
+    res = make_res(1.5625, 0, inv)                        # norm 1.25
+    want = [torch.zeros_like(t) for t in o.t]
+    for k, (x, w) in enumerate(zip(s.t, want)):
+        small = Z.zero_tensor_plan([x], out=[w])
+        assert small.c.bytes < 256 << 20
+        Z.zero_tensor_clip(small, max_norm, res, norms=norms[k:k + 1] if per_tensor else None)
+    host = [host64(x) if n < 1 << 20 or k == 1 else None for k, (n, x) in enumerate(zip(sizes, s.t))]
+    Z.zero_tensor_clip(plan, max_norm, res, norms=given)
+    for k, (t, w) in enumerate(zip(o.t, want)):
+        assert torch.equal(t.view(torch.uint8), w.view(torch.uint8)), k
+        if host[k] is not None:
+            norm = norms[k].item() if per_tensor else 1.25
+            assert_rounded(t, clip_want(host[k], norm, max_norm, inv), t.dtype, clip_steps(t.dtype))
+    o.assert_guards()
+    s.assert_guards()
