@@ -892,6 +892,22 @@ def test_many_empty_tensors_are_not_one_blocks_work():
     assert bool((tensors[-1] == 2.0).all()) and ms < 2.0
 
 
+def test_overwriting_16_bit_accumulators_runs_as_a_clip_does():
+    """The first micro-batch of 2.2e8 bf16 values into bf16 accumulators, with the norm, and
+    their clip move the same bytes: 142 and 134 us.  With the blocks per CU that adding
+    to fp32 accumulators takes it was 228."""
+    n = 220_000_000
+    x, y = torch.zeros(n, dtype=BF, device="cuda"), torch.zeros(n, dtype=BF, device="cuda")
+    plan = Z.zero_tensor_plan(list(x.split(1_000_000)), out=list(y.split(1_000_000)))
+    res, given, ws = make_res(), make_res(4.0, 0, 0.5), workspace(plan)
+    first, clip = [], []
+    for _ in range(10):                                   # in turn
+        first.append(call_ms(lambda: Z.zero_tensor_accumulate(plan, 0.5, overwrite=True, res=res,
+                                                              workspace=ws), 4))
+        clip.append(call_ms(lambda: Z.zero_tensor_clip(plan, 1.0, given), 4))
+    assert min(first) < 1.35 * min(clip), (min(first), min(clip))
+
+
 @pytest.mark.parametrize("kind", ["l2", "max"])
 @pytest.mark.parametrize("few", [3, 128, 129, 600])
 def test_tensors_of_many_partials(few, kind):

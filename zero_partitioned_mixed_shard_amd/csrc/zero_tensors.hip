@@ -61,9 +61,8 @@ constexpr int kRun = 16384;
 constexpr int kRunGroup = 16, kPieceGroup = 32;
 // Resident blocks per CU (lds_for_blocks).  Clip: 9.4e8 bf16 in place take 564 us
 // at 5, 589 at 4, 585 at 8.  The norm has 5, and 3 for large tables of aligned
-// 16-bit tensors (norm_blocks); accumulation 3, and 2 for large tables with fp32
-// outputs (add_blocks).
-constexpr int kNormBlocksPerCU = 5, kClipBlocksPerCU = 5, kAddBlocksPerCU = 3;
+// 16-bit tensors (norm_blocks); accumulation 2 to 8 (add_blocks).
+constexpr int kNormBlocksPerCU = 5, kClipBlocksPerCU = 5;
 // Loads of 16 bytes that a lane has in flight in the norm of a run, and of a
 // rest (8 for the runs: 1 % slower; 4 for the rests: the same).
 constexpr int kRunLoads = 4, kRestLoads = 8;
@@ -1035,12 +1034,23 @@ int clip_norm_impl(const zero_tensor_plan* plan, const void* table, float max_no
     return clip_impl(plan, table, max_norm, res, per_tensor ? norms : nullptr, stream);
 }
 
-// Resident blocks per CU of an accumulation.  bf16 into fp32, 9.4e8 elements: 1489 us
-// at 3, 1432-1458 at 2, 1517 at 4, 1571 at 8; 5.1e8: 714 at 3, 704 at 2; 1.7e8: 230
-// at both; 4001 ragged tensors of 8.3e7: 134 at 3, 140 at 2.  fp16 into fp16: 12-15
-// % more at 2 than at 3.
-int add_blocks(const zero_tensor_plan* p) {
-    return p->fp32_out && p->bytes > int64_t(2) << 30 ? 2 : kAddBlocksPerCU;
+// Resident blocks per CU of an accumulation (us; 9.4e8 elements unless said).  Added to
+// what is there, two streams in and one out:
+//   bf16 into fp32              1445 at 2, 1486 at 3, 1517 at 4, 1569 at 8
+//   5.1e8, 1.7e8 of them         704 and 230 at 2, 714 and 230 at 3
+//   with the norm               1500 at 2, 1455 at 3 (fp32 into fp32: 1749, 1793)
+//   bf16 into bf16               973 at 2, 838 at 3, 874 at 4, 932 at 8
+// One stream less (overwrite), the norm's squares in 64 bits and the rounding to 16 bits
+// leave a block less time in which its loads are under way, and take more blocks:
+//   bf16 into bf16, the norm     952 at 3, 852 at 4, 859 at 5, 928 at 8 (fp32 into bf16:
+//                               1170, 1154, 1214, 1244)
+//   overwrite                    668 at 3, 573 at 5, 600 at 8
+//   overwrite, the norm          890 at 3, 623 at 5, 595 at 8
+//   bf16 into fp32, both         913 at 3, 898 at 4, 894 at 5, 933 at 8
+int add_blocks(const zero_tensor_plan* p, bool overwrite, bool norm) {
+    if (overwrite && norm) return p->fp32_out ? 4 : 8;
+    if (!p->fp32_out && (overwrite || norm)) return overwrite ? 5 : 4;
+    return p->fp32_out && p->bytes > int64_t(2) << 30 ? 2 : 3;
 }
 
 template <int KIND>
@@ -1048,8 +1058,9 @@ int accumulate_impl(const zero_tensor_plan* plan, const void* table, float weigh
                     int32_t overwrite, double* part, hipStream_t stream) {
     const auto kernel = overwrite ? tensor_accumulate_kernel<KIND, true>
                                   : tensor_accumulate_kernel<KIND, false>;
+    const unsigned lds = lds_for_blocks(add_blocks(plan, overwrite != 0, KIND != 0));
     return in_launches(plan->n_pieces, [&](int64_t b, int64_t grid) {
-        return launch(kernel, grid, lds_for_blocks(add_blocks(plan)), stream, pieces_of(plan, table) + b,
+        return launch(kernel, grid, lds, stream, pieces_of(plan, table) + b,
                       dsts_of(plan, table) + b, weight, KIND ? part + b : part);
     });
 }
