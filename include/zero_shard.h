@@ -73,11 +73,14 @@ enum zero_dtype {
 #define ZERO_MAX_RANKS 16
 
 /* Result of the check phase.  Lives in device memory; written by
- * zero_unscale_check_norm, read by zero_adamw_step on the device, and copied
- * to the host by the caller only for the loss-scale update.  16 bytes. */
+ * zero_unscale_check_norm (and zero_tensor_norm), read by zero_adamw_step on the
+ * device, and copied to the host by the caller only for the loss-scale update.
+ * 16 bytes. */
 typedef struct zero_step_result {
-    double sumsq;        /* sum over the checked elements of (value * inv_scale)^2, fp64;
-                            value * inv_scale is the fp32 product                       */
+    double sumsq;        /* square of the norm: sum over the checked elements of
+                            (value * inv_scale)^2, fp64; value * inv_scale is the fp32
+                            product (zero_tensor_*: in fp64, inv_scale^2 * sum value^2,
+                            or the largest magnitude's (value * inv_scale)^2)           */
     uint32_t overflow;   /* 1 if some checked element is +-inf or NaN, else 0          */
     float inv_scale;     /* the unscale factor the check used                           */
 } zero_step_result;
@@ -548,6 +551,8 @@ int zero_tensor_norm(const zero_tensor_plan* plan, const void* table, int32_t ki
  * norms[k] (inf gives f = 0; an f below fp32's normal range has fewer bits).  The
  * product is fp32, then rounded once (nearest, ties to even) to y's type.  With
  * res->overflow set nothing is written, and in place with f = 1 nothing need be.
+ * y is unscaled: a zero_adamw_step that takes it needs a result with inv_scale 1 and
+ * no clip of its own.
  *   res    device, in: written by zero_tensor_norm or any check of this library
  *   norms  device, in, fp32[n_tensors], or NULL
  * Errors: ZERO_EINVAL for NULL pointers, a plan that is not writable, a NaN

@@ -52,16 +52,18 @@ static_assert(sizeof(Piece) == 16, "one scalar load");
 constexpr int kPiece = 4096;
 // Elements of a run of the norm: 4096-element pieces, a wave each, read 6.7e9 bf16
 // at 6.73 TB/s, runs by whole blocks at 6.97 (and 10,000 ragged tensors at 6.56
-// with rests by waves, 6.37 by blocks).
+// with rests by waves, 6.37 by blocks; all four at 8 blocks per CU and groups of 1).
 constexpr int kRun = 16384;
-// Consecutive units an XCD gets of each.  Norm of 6.7e9 bf16, at 3 blocks per CU:
-// 1800 us at 16, 1828 at 8, 1795 at 32, which costs ragged tables 1 %; at 1 (with
-// 8 blocks per CU) 1937, and 1973 at 2 and 4.  Norm and clip of 9.4e8 fp16: 860 us
-// at 32, 877 at 1, 891-905 at 2 to 8.
+// Consecutive units an XCD gets of each.  Norm of 6.7e9 bf16: 1854 us at 16, 1878 at 8,
+// 1837 at 32, 1935 to 1941 at 1 to 4; 10,000 ragged tensors 304 at 16, 303 at 8, 305 at
+// 32, 311 at 1.  Clip of 9.4e8 bf16 in place: 566 us at 32, 561 at 16, 576 at 8, 583 at
+// 1; accumulation into fp32 1449, 1443, 1449 and 1497.
 constexpr int kRunGroup = 16, kPieceGroup = 32;
-// Resident blocks per CU (lds_for_blocks).  Clip: 9.4e8 bf16 in place take 564 us
-// at 5, 589 at 4, 585 at 8.  The norm has 5, and 3 for large tables of aligned
-// 16-bit tensors (norm_blocks); accumulation 2 to 8 (add_blocks).
+// Resident blocks per CU (lds_for_blocks).  Clip of 9.4e8 elements, at 3, 5 and 8: bf16 in
+// place 686, 566 and 592 us, fp16 592, 562 and 575, fp32 into bf16 864, 885 and 903, fp32
+// 1184, 1210 and 1242; 8.3e7 ragged bf16 72, 54 and 53.  The norm has 5, and 3 for
+// large tables of aligned 16-bit tensors (norm_blocks); accumulation 2 to 8
+// (add_blocks).
 constexpr int kNormBlocksPerCU = 5, kClipBlocksPerCU = 5;
 // Loads of 16 bytes that a lane has in flight in the norm of a run, and of a
 // rest (8 for the runs: 1 % slower; 4 for the rests: the same).
@@ -473,7 +475,7 @@ __device__ __forceinline__ void piece_scale(const void* src, void* dst, int coun
         return y;
     };
     // a skipped step, or in place with a factor of 1 (900 tensors of 16384 fp32: norm
-    // and clip 22.9 us for 31.5): nothing to write
+    // and clip 22.9 us for 31.5): nothing to write, though it has been read
     auto nothing = [&](float f) { return f != f || (SRC == DST && f == 1.0f && src == dst); };
     Raw<SRC, W> r[U];
     if (U * R == kPiece && count == kPiece) {
@@ -969,9 +971,9 @@ int one_block_impl(const zero_tensor_plan* plan, const void* table, float max_no
 }
 
 // Resident blocks per CU of the norm.  16-bit tensors that begin at a dword: 6.7e9
-// elements take 1800 us at 3, 1872 at 5, 1886 at 8; 4.4e8 127 and 131; 1.4e8 the same
-// at 3 and 5, and below 2e8 3 gains nothing.  10,000 packed tensors, half of which
-// begin between dwords: 333 at 3, 314 at 5; fp32 1 % more at 3.
+// elements take 1851 us at 3, 1908 at 5 and at 8; 9.4e8 256 and 272; 4.4e8 127 and 131;
+// 2.2e8 65 and 68; 1.4e8 the same.  10,000 packed tensors, half of which begin between
+// dwords: 325 at 3, 304 at 5; ragged ones of 8.3e7 33 and 31; fp32 the same to 1 %.
 int norm_blocks(const zero_tensor_plan* p) {
     return p->even16 && p->n_runs >= 16384 ? 3 : kNormBlocksPerCU;
 }
@@ -1000,10 +1002,14 @@ int norm_impl(const zero_tensor_plan* plan, const void* table, float inv_scale,
                         inv_scale, ctl, accumulate, res, norms, part, stream);
 }
 
-// Whether a table is larger than the last-level cache (256 MB): the clip then
-// loads its inputs so that they do not stay in it.  Three tables in turn, of 202 MB
-// each: 36.1 us so, 31.5 us with plain loads; of 401 MB: 63.5 and 69.9; one of
-// 3.8 GB: 608 and 697.
+// Whether a clip reads and writes more than the last-level cache holds (256 MB): it
+// then loads its inputs so that they do not stay there.  Three tables in turn: 202 MB
+// read and written 36.1 us so, 31.5 us with plain loads; 401 MB 63.5 and 69.9; 3.8 GB
+// 608 and 697.  In place counts twice too: 130 MB in place 41 us and 46-49, 200 MB 62
+// and 70-72, also where the table has just been written (bf16 59 and 77, fp32 59 and
+// 60).  Plain loads win there only where nothing but the clip touches one table again and
+// again (200 MB: 57 for 61) and in the clip right after the norm of fp32 (100 for 107);
+// non-temporal ones would win from 100 MB in place on already (32 for 34-36).
 bool streams(const zero_tensor_plan* p) { return p->bytes > int64_t(256) << 20; }
 
 int clip_impl(const zero_tensor_plan* plan, const void* table, float max_norm,

@@ -9,6 +9,10 @@ norm, clipping and accumulation.
     bucket = zero_tensor_plan(accumulators, out=pieces_of_a_flat_buffer)
     zero_tensor_clip(bucket, 1.0, res)                  # clipped, unscaled, 16-bit
 
+(zero_adamw_step unscales and clips by its own result: give it one with inv_scale 1 and
+no max_grad_norm after that clip, or leave the clip to it and cast the accumulators with
+a result that has inv_scale 1 and max_norm 0.)
+
 Calls are asynchronous on the current stream of the plan's device (or
 ``stream``), allocate nothing and can be captured in a graph (build the plan
 before the capture and keep it, and the tensors' memory, for as long as the
