@@ -586,6 +586,121 @@ int zero_tensor_accumulate_norm(const zero_tensor_plan* plan, const void* table,
                                 void* workspace, size_t workspace_bytes, int32_t accumulate,
                                 hipStream_t stream);
 
+/* ------------------------------------------------------------ matrices ---- */
+/* Steps that need whole matrices: orthogonalisation of an update, and the owner
+ * step of the Muon optimiser, for owners of whole tensors (ZeRO 优化器, cookllm.com,
+ * "参数分配策略": round-robin ownership; the pages name AdamW alone, the equations
+ * here are the definition).
+ *
+ * orth(G) for a matrix G of any size: X_0 = G / (||G||_F + eps), and `steps` times
+ *   A = X X^T,  X <- a X + (b A + c A A) X
+ * on the wide form (G or its transpose, rows <= columns), transposed back.  A matrix of
+ * zeros gives zeros; one that holds inf or NaN gives NaN.  The products are fp16 with
+ * fp32 sums, the linear term a X has 22 bits; the result is off by 1e-3 to 2e-3 of its
+ * norm (fewer for ill-conditioned matrices), and with `precise`, where every factor has
+ * 22 bits, by about 1e-5. */
+
+/* Coefficients.  They have to keep the singular values within 1.75: the largest value
+ * of |a x + b x^3 + c x^5| for x in [0, 1], then in [0, that value], and so on for all
+ * steps.  3.4445, -4.7750, 2.0315 and 5 steps, the usual choice, stay below 1.21. */
+typedef struct zero_newton_schulz {
+    float a, b, c;
+    float eps;           /* >= 1e-30; 1e-7 */
+    int32_t steps;       /* 1 .. 64        */
+} zero_newton_schulz;
+
+/* A matrix of a list: `rows` rows of `cols` elements, `src_ld` elements apart, and
+ * where its result goes: elsewhere, in another type perhaps, or onto itself (the same
+ * pointer, type and distance).  0 rows or columns are allowed; the pointers are then
+ * not read. */
+typedef struct zero_matrix_entry {
+    const void* src;     /* device, aligned to its element size          */
+    void* dst;           /* device, likewise                             */
+    int64_t rows, cols;  /* the longer at most 4194240, the shorter 65536 */
+    int64_t src_ld, dst_ld;
+    int32_t src_dtype;   /* zero_dtype: FP16, BF16 or FP32               */
+    int32_t dst_dtype;
+} zero_matrix_entry;
+
+/* A matrix of a flat shard: rows * cols elements from `offset` of every buffer, row by
+ * row. */
+typedef struct zero_matrix_range {
+    int64_t offset, rows, cols;
+} zero_matrix_range;
+
+/* What a plan's init finds out about a list (host); passed, unchanged, to the calls
+ * with the table that belongs to it. */
+typedef struct zero_matrix_plan {
+    int64_t n_matrices;      /* of the list                                    */
+    int64_t numel;           /* elements of all                                */
+    int64_t extent;          /* zero_muon_step: elements that the buffers need */
+    int64_t table_bytes;
+    int64_t workspace_bytes; /* device scratch of a call                       */
+    int32_t kind;            /* whose plan: orthogonalize (1) or muon (2)      */
+    int32_t precise;
+} zero_matrix_plan;
+
+/* Plan of a list (host array; n_matrices 0 is allowed).  No result may overlap another
+ * result, nor a matrix other than its own in the same place; blocks of columns of one
+ * buffer (the same distance of rows) do not overlap.
+ * Errors: ZERO_EINVAL for a NULL argument, a negative size, an unknown type, a NULL or
+ * misaligned pointer, rows closer than their elements, results that overlap;
+ * ZERO_ERANGE for sides beyond the limits, addresses that overflow, or a list that host
+ * memory does not hold. */
+int zero_matrix_plan_init(const zero_matrix_entry* entries, int64_t n_matrices, int32_t precise,
+                          zero_matrix_plan* plan);
+int zero_muon_plan_init(const zero_matrix_range* ranges, int64_t n_matrices, int32_t precise,
+                        zero_matrix_plan* plan);
+
+/* Writes the plan's table, plan->table_bytes bytes, to host memory.  The caller copies
+ * it to device memory, 16-byte aligned; the calls are passed both.
+ * Errors: as init, and ZERO_EINVAL if the plan is not that of this list. */
+int zero_matrix_plan_table(const zero_matrix_entry* entries, const zero_matrix_plan* plan, void* table);
+int zero_muon_plan_table(const zero_matrix_range* ranges, const zero_matrix_plan* plan, void* table);
+
+/* Every matrix's result: dst = round(orth(src)), rounded once (nearest, ties to even).
+ *   host_table, table  the plan's table on the host and on the device
+ *   workspace          device scratch of plan->workspace_bytes bytes, 256-byte aligned;
+ *                      needs no initialisation, not shared by calls that may overlap
+ * Errors: ZERO_EINVAL for NULL pointers, a plan or table of another kind, coefficients
+ * out of their limits, a small or misaligned workspace. */
+int zero_orthogonalize(const zero_matrix_plan* plan, const void* host_table, const void* table,
+                       const zero_newton_schulz* ns, void* workspace, size_t workspace_bytes,
+                       hipStream_t stream);
+
+enum zero_muon_scaling {     /* alpha, for a matrix of r rows and c columns */
+    ZERO_MUON_NONE = 0,      /* 1                                           */
+    ZERO_MUON_ASPECT = 1,    /* sqrt(max(1, r / c))                         */
+    ZERO_MUON_RMS = 2        /* 0.2 sqrt(max(r, c)): updates as large as AdamW's */
+};
+
+typedef struct zero_muon_hparams {
+    float lr, momentum, weight_decay;
+    float max_grad_norm;     /* <= 0: no clipping                    */
+    int32_t nesterov;        /* != 0: the update is g + momentum * m */
+    int32_t scaling;         /* zero_muon_scaling                    */
+    zero_newton_schulz ns;
+} zero_muon_hparams;
+
+/* The Muon step of the plan's matrices in an owner's flat buffers, which
+ * zero_adamw_step_ranges steps everywhere else.  With *res as zero_adamw_step takes it
+ * (nothing is written where res->overflow is set), per element in fp32:
+ *   g = grad16 * res->inv_scale * coef     coef = max_grad_norm / (norm + 1e-6) if
+ *                                          that is below 1 (as zero_adamw_step)
+ *   m = momentum * m + g
+ *   u = g + momentum * m, or m
+ *   p = p * (1 - lr * weight_decay) - lr * alpha * orth(u)
+ *   param16 = round(p)
+ *   master, momentum, param16   device, in/out (param16: out), plan->extent elements
+ *   grad16                      device, in; overlaps none of these
+ *   dtype                       of param16 and grad16
+ * Errors: ZERO_EINVAL for NULL or misaligned pointers, an unknown type, parameters that
+ * are not finite, and as zero_orthogonalize. */
+int zero_muon_step(float* master, float* momentum, void* param16, const void* grad16, int32_t dtype,
+                   const zero_matrix_plan* plan, const void* host_table, const void* table,
+                   const zero_muon_hparams* hp, const zero_step_result* res, void* workspace,
+                   size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

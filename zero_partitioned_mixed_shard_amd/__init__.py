@@ -1,8 +1,8 @@
 """Python binding of the ZeRO-1/2 owner-shard step library (libzero_shard.so).
 
 Argument marshalling only: every phase runs in the HIP kernels of
-``csrc/zero_shard.hip``, ``csrc/zero_flat.hip`` and ``csrc/zero_tensors.hip``
-behind the C ABI of ``include/zero_shard.h``.  The functions keep the C names.  Device buffers are
+``csrc/zero_shard.hip``, ``csrc/zero_flat.hip``, ``csrc/zero_tensors.hip`` and
+``csrc/zero_matrix.hip`` behind the C ABI of ``include/zero_shard.h``.  The functions keep the C names.  Device buffers are
 torch tensors (device memory and streams are all torch is used for); 16-bit
 data is passed as torch.float16 / torch.bfloat16 tensors, fp32 state as
 torch.float32.  There is no fallback: if the library is missing, importing
@@ -22,6 +22,7 @@ LIB_PATH = os.path.join(PKG, "libzero_shard.so")
 ZERO_OK, ZERO_EINVAL, ZERO_ERANGE, ZERO_EDEVICE = 0, -1, -2, -3
 ZERO_FP16, ZERO_BF16, ZERO_FP32 = 1, 2, 3
 ZERO_NORM_L2, ZERO_NORM_MAX = 1, 2
+ZERO_MUON_NONE, ZERO_MUON_ASPECT, ZERO_MUON_RMS = 0, 1, 2
 ZERO_MAX_RANKS = 16
 
 
@@ -55,6 +56,16 @@ class zero_step_control(ctypes.Structure):
                 ("bc1", ctypes.c_float), ("bc2", ctypes.c_float)]
 
 
+class zero_newton_schulz(ctypes.Structure):
+    """Coefficients of the orthogonalisation (by default the usual five quintic steps)."""
+    _fields_ = [("a", ctypes.c_float), ("b", ctypes.c_float), ("c", ctypes.c_float),
+                ("eps", ctypes.c_float), ("steps", ctypes.c_int32)]
+
+    def __init__(self, a: float = 3.4445, b: float = -4.7750, c: float = 2.0315,
+                 eps: float = 1e-7, steps: int = 5):
+        super().__init__(a, b, c, eps, steps)
+
+
 RESULT_BYTES = ctypes.sizeof(zero_step_result)   # 16
 CONTROL_BYTES = ctypes.sizeof(zero_step_control)  # 72
 
@@ -71,6 +82,8 @@ EXPORTS = (
     "zero_tensor_workspace_bytes",
     "zero_tensor_norm", "zero_tensor_clip", "zero_tensor_clip_norm", "zero_tensor_accumulate",
     "zero_tensor_accumulate_norm",
+    "zero_matrix_plan_init", "zero_matrix_plan_table", "zero_muon_plan_init",
+    "zero_muon_plan_table", "zero_orthogonalize", "zero_muon_step",
 )
 
 
@@ -139,6 +152,12 @@ def _load():
         "zero_tensor_accumulate": ([P, P, f32, i32, P], ctypes.c_int),
         "zero_tensor_accumulate_norm": ([P, P, f32, i32, i32, f32, P, P, P, P, ctypes.c_size_t,
                                          i32, P], ctypes.c_int),
+        "zero_matrix_plan_init": ([P, i64, i32, P], ctypes.c_int),
+        "zero_matrix_plan_table": ([P, P, P], ctypes.c_int),
+        "zero_muon_plan_init": ([P, i64, i32, P], ctypes.c_int),
+        "zero_muon_plan_table": ([P, P, P], ctypes.c_int),
+        "zero_orthogonalize": ([P, P, P, P, P, ctypes.c_size_t, P], ctypes.c_int),
+        "zero_muon_step": ([P, P, P, P, i32, P, P, P, P, P, P, ctypes.c_size_t, P], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -547,3 +566,7 @@ def zero_reduce_check_owned_noalloc(dst, srcs: Sequence, inv_scale: float, res,
 from .tensors import (zero_tensor_accumulate, zero_tensor_accumulate_norm,  # noqa: E402,F401
                       zero_tensor_clip, zero_tensor_clip_norm, zero_tensor_norm, zero_tensor_plan,
                       zero_tensor_workspace_bytes)
+
+# --------------------------------------------------------------- matrices ---
+from .matrix import (zero_matrix_plan, zero_matrix_workspace_bytes, zero_muon_hparams,  # noqa: E402,F401
+                     zero_muon_plan, zero_muon_step, zero_orthogonalize)

@@ -6,10 +6,10 @@ import subprocess
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-# owner-step kernels + C ABI, the flat copy kernels and the operators over
-# tensor tables; zero_common.h is included by all
+# owner-step kernels + C ABI, the flat copy kernels, the operators over tensor
+# tables and over matrices; zero_common.h is included by all
 SRCS = [os.path.join(PKG, "csrc", f)
-        for f in ("zero_shard.hip", "zero_flat.hip", "zero_tensors.hip")]
+        for f in ("zero_shard.hip", "zero_flat.hip", "zero_tensors.hip", "zero_matrix.hip")]
 LIB = os.path.join(PKG, "libzero_shard.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
