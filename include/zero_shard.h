@@ -701,6 +701,50 @@ int zero_muon_step(float* master, float* momentum, void* param16, const void* gr
                    const zero_muon_hparams* hp, const zero_step_result* res, void* workspace,
                    size_t workspace_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------ embedding rows ---- */
+/* Rows of the vocabulary table W (vocab rows of dim elements, flat, one of the group's
+ * tensors) by tokens: what the forward pass takes of an owner's store (as the per-layer
+ * gathers of ZeRO-3: wmrh.cn ZeRO article, section 2.2.3), and the gradient, which
+ * touches only the rows that tokens have.  A call has a slice of the table, elements
+ * [begin, begin + count): partitions are cut at elements (ZeRO-2 source walkthrough,
+ * section 2.1), so a slice may begin and end inside a row.
+ *   ids       device, n_tokens (at most 2^31 - 1) ids of id_bytes 4 or 8, signed; an id
+ *             outside [0, vocab) is allowed and has no row
+ *   vocab     1 .. 2^31 - 2;  dim  1 .. 2^29 - 1 */
+
+/* y[t] = round(scale * W[ids[t]]): one fp32 product, rounded to y's type once; 0 for
+ * what lies outside the slice.
+ *   out    device, out: row t's dim elements from out + t * out_ld
+ *   table  device, in: the slice, W's elements from `begin`
+ * Errors: ZERO_EINVAL for NULL or misaligned pointers, sizes below 1 (n_tokens: 0), an
+ * unknown type, rows closer than dim, a slice outside the table, a scale that is not
+ * finite; ZERO_ERANGE for sizes beyond the limits. */
+int zero_embedding_lookup(void* out, int64_t out_ld, int32_t out_dtype, const void* ids, int32_t id_bytes,
+                          int64_t n_tokens, const void* table, int32_t table_dtype, int64_t vocab, int64_t dim,
+                          int64_t begin, int64_t count, float scale, hipStream_t stream);
+
+/* Bytes of workspace for zero_embedding_grad (0 for sizes that it refuses).  No fewer
+ * tokens need more: the bytes for the most tokens serve all calls. */
+size_t zero_embedding_workspace_bytes(int64_t n_tokens, int64_t vocab, int64_t dim);
+
+/* dW[v] = round(dW[v] + scale * sum over the tokens t with ids[t] = v of dy[t]), for the
+ * elements of the slice; one fused multiply-add in fp32 after the sum, which is fp32 in
+ * an order that goes by the ids alone (the same call gives the same bits).  With
+ * overwrite != 0 dW[v] = round(scale * sum), and 0 in rows that no token has.  Tokens
+ * with padding_id (< 0: none) give nothing, and their dy is not read.
+ *   grad       device, in/out: the slice, from `begin`
+ *   dy         device, in: row t's dim elements from dy + t * dy_ld
+ *   workspace  device scratch of zero_embedding_workspace_bytes(n_tokens, vocab, dim),
+ *              256-byte aligned; needs no initialisation, not shared by calls that
+ *              may overlap
+ * grad and workspace overlap neither each other nor ids and dy.
+ * Errors: as zero_embedding_lookup, and ZERO_EINVAL for a small or misaligned
+ * workspace. */
+int zero_embedding_grad(void* grad, int32_t grad_dtype, const void* ids, int32_t id_bytes, int64_t n_tokens,
+                        const void* dy, int64_t dy_ld, int32_t dy_dtype, int64_t vocab, int64_t dim,
+                        int64_t begin, int64_t count, int64_t padding_id, float scale, int32_t overwrite,
+                        void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

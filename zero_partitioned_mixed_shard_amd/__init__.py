@@ -1,8 +1,8 @@
 """Python binding of the ZeRO-1/2 owner-shard step library (libzero_shard.so).
 
 Argument marshalling only: every phase runs in the HIP kernels of
-``csrc/zero_shard.hip``, ``csrc/zero_flat.hip``, ``csrc/zero_tensors.hip`` and
-``csrc/zero_matrix.hip`` behind the C ABI of ``include/zero_shard.h``.  The functions keep the C names.  Device buffers are
+``csrc/zero_shard.hip``, ``csrc/zero_flat.hip``, ``csrc/zero_tensors.hip``,
+``csrc/zero_matrix.hip`` and ``csrc/zero_embedding.hip`` behind the C ABI of ``include/zero_shard.h``.  The functions keep the C names.  Device buffers are
 torch tensors (device memory and streams are all torch is used for); 16-bit
 data is passed as torch.float16 / torch.bfloat16 tensors, fp32 state as
 torch.float32.  There is no fallback: if the library is missing, importing
@@ -84,6 +84,7 @@ EXPORTS = (
     "zero_tensor_accumulate_norm",
     "zero_matrix_plan_init", "zero_matrix_plan_table", "zero_muon_plan_init",
     "zero_muon_plan_table", "zero_orthogonalize", "zero_muon_step",
+    "zero_embedding_lookup", "zero_embedding_workspace_bytes", "zero_embedding_grad",
 )
 
 
@@ -158,6 +159,11 @@ def _load():
         "zero_muon_plan_table": ([P, P, P], ctypes.c_int),
         "zero_orthogonalize": ([P, P, P, P, P, ctypes.c_size_t, P], ctypes.c_int),
         "zero_muon_step": ([P, P, P, P, i32, P, P, P, P, P, P, ctypes.c_size_t, P], ctypes.c_int),
+        "zero_embedding_lookup": ([P, i64, i32, P, i32, i64, P, i32, i64, i64, i64, i64, f32, P],
+                                  ctypes.c_int),
+        "zero_embedding_workspace_bytes": ([i64, i64, i64], ctypes.c_size_t),
+        "zero_embedding_grad": ([P, i32, P, i32, i64, P, i64, i32, i64, i64, i64, i64, i64, f32, i32,
+                                 P, ctypes.c_size_t, P], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -570,3 +576,7 @@ from .tensors import (zero_tensor_accumulate, zero_tensor_accumulate_norm,  # no
 # --------------------------------------------------------------- matrices ---
 from .matrix import (zero_matrix_plan, zero_matrix_workspace_bytes, zero_muon_hparams,  # noqa: E402,F401
                      zero_muon_plan, zero_muon_step, zero_orthogonalize)
+
+# ------------------------------------------------------- embedding rows -----
+from .embedding import (zero_embedding_grad, zero_embedding_lookup,  # noqa: E402,F401
+                        zero_embedding_workspace_bytes)

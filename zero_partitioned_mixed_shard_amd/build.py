@@ -7,9 +7,10 @@ import subprocess
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 # owner-step kernels + C ABI, the flat copy kernels, the operators over tensor
-# tables and over matrices; zero_common.h is included by all
+# tables, over matrices and over embedding rows; zero_common.h is included by all
 SRCS = [os.path.join(PKG, "csrc", f)
-        for f in ("zero_shard.hip", "zero_flat.hip", "zero_tensors.hip", "zero_matrix.hip")]
+        for f in ("zero_shard.hip", "zero_flat.hip", "zero_tensors.hip", "zero_matrix.hip",
+                  "zero_embedding.hip")]
 LIB = os.path.join(PKG, "libzero_shard.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -1,0 +1,728 @@
+// zero_embedding.hip -- rows of the vocabulary table by tokens: lookup with scaling
+// (zero_embedding_lookup) and its gradient by sorted tokens (zero_embedding_grad), from
+// and into an owner's slice of the flat table.
+//
+// Gradient.  dW[v] = scale * sum of dy[t] over the tokens t of v.  The tokens are sorted
+// by their id, stably, so equal ones lie next to each other in the order of t.  The
+// sorted list is cut into chunks; a wave adds up the rows of a chunk for 512 columns, in
+// fp32, and writes the sums of the ids that begin and end in its chunk.  What an id
+// has in a chunk beside others goes to the workspace, and a second pass adds these
+// up in order.  No atomics on floats: the same call gives the same bits.
+//
+// Everything here is bound by HBM (dy is read once, rows that tokens have are read and
+// written once) or, for few tokens, by the launches.
+
+#include <math.h>
+
+#include "zero_common.h"
+
+namespace {
+
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+
+constexpr int kCols = 8;                   // columns of a lane
+constexpr int kSlab = 64 * kCols;          // columns of a wave
+constexpr int kSortLanes = 1024, kSortWaves = kSortLanes / 64;
+constexpr int kSmallSort = 8192;           // tokens that one block sorts in LDS
+constexpr int kSortTile = 4096;            // tokens of a block of the larger sort
+constexpr int kDigit = 9, kBins = 1 << kDigit;   // most bits of a pass
+
+template <int DT>
+constexpr int kSize = DT == ZERO_FP32 ? 4 : 2;
+
+template <int DT>
+__device__ __forceinline__ float widen(uint16_t b) {
+    return DT == ZERO_FP16 ? (float)__builtin_bit_cast(_Float16, b) : __uint_as_float((uint32_t)b << 16);
+}
+// Nearest, ties to even; overflow gives inf, NaN stays (quiet) NaN.
+template <int DT>
+__device__ __forceinline__ uint16_t narrow(float f) {
+    if (DT == ZERO_FP16) return __builtin_bit_cast(uint16_t, (_Float16)f);
+    const uint32_t u = __float_as_uint(f);
+    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x0040u);
+    return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
+}
+
+// 8 consecutive elements as they lie in memory, which may begin at any element.
+template <int DT>
+struct Raw8 {
+    static constexpr int kQuads = kSize<DT> / 2;
+    u32x4 q[kQuads];
+    __device__ __forceinline__ float get(int k) const {
+        if constexpr (DT == ZERO_FP32) return __uint_as_float(q[k >> 2][k & 3]);
+        else return widen<DT>(half_of(q[0], k));
+    }
+};
+template <int DT, bool NT>
+__device__ __forceinline__ Raw8<DT> load8(const void* base, int64_t e) {
+    Raw8<DT> r;
+    const char* p = (const char*)base + e * kSize<DT>;
+#pragma unroll
+    for (int k = 0; k < Raw8<DT>::kQuads; ++k) {
+        const u32x4_a2* c = (const u32x4_a2*)p + k;
+        r.q[k] = NT ? __builtin_nontemporal_load(c) : *c;
+    }
+    return r;
+}
+template <int DT, bool NT>
+__device__ __forceinline__ void store8(void* base, int64_t e, const float* v) {
+    char* p = (char*)base + e * kSize<DT>;
+#pragma unroll
+    for (int k = 0; k < Raw8<DT>::kQuads; ++k) {
+        u32x4 w;
+        if constexpr (DT == ZERO_FP32) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(v[4 * k + j]);
+        } else {
+            uint16_t h[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[j] = narrow<DT>(v[j]);
+            w = pack8(h);
+        }
+        u32x4_a2* c = (u32x4_a2*)p + k;
+        if (NT) __builtin_nontemporal_store(w, c);
+        else *c = w;
+    }
+}
+template <int DT>
+__device__ __forceinline__ float load1(const void* base, int64_t e) {
+    if constexpr (DT == ZERO_FP32) return ((const float*)base)[e];
+    else return widen<DT>(((const uint16_t*)base)[e]);
+}
+template <int DT>
+__device__ __forceinline__ void store1(void* base, int64_t e, float v) {
+    if constexpr (DT == ZERO_FP32) ((float*)base)[e] = v;
+    else ((uint16_t*)base)[e] = narrow<DT>(v);
+}
+
+// The table's slice: elements [begin, begin + count) of vocab * dim.
+struct Slice {
+    int64_t vocab, dim, begin, count;
+};
+__device__ __forceinline__ int64_t id_at(const void* ids, int wide, int64_t t) {
+    return wide ? ((const int64_t*)ids)[t] : (int64_t)((const int32_t*)ids)[t];
+}
+
+// ------------------------------------------------------------ lookup -------
+// A wave takes 512 columns of a token.
+template <int SRC, int DST>
+__global__ void __launch_bounds__(kThreads)
+embedding_lookup_kernel(void* __restrict__ out, int64_t out_ld, const void* __restrict__ ids, int wide,
+                        int64_t units, int64_t slabs, const void* __restrict__ table, Slice s, float scale,
+                        int64_t blk0) {
+    const int64_t u = (blk0 + blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6);
+    if (u >= units) return;
+    const int64_t token = u / slabs;
+    const int64_t col = (u - token * slabs) * kSlab + (threadIdx.x & 63) * kCols;
+    if (col >= s.dim) return;
+    const int64_t id = id_at(ids, wide, token);
+    const int n = (int)(s.dim - col < kCols ? s.dim - col : kCols);
+    const bool known = id >= 0 && id < s.vocab;
+    const int64_t at = known ? id * s.dim + col - s.begin : -kCols, to = token * out_ld + col;
+    float v[kCols];
+    if (at >= 0 && at + kCols <= s.count && n == kCols) {
+        const Raw8<SRC> r = load8<SRC, false>(table, at);
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) v[k] = scale * r.get(k);
+    } else {
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) {
+            const int64_t e = at + k;
+            v[k] = known && k < n && e >= 0 && e < s.count ? scale * load1<SRC>(table, e) : 0.0f;
+        }
+    }
+    if (n == kCols) {
+        store8<DST, true>(out, to, v);
+    } else {
+#pragma unroll
+        for (int k = 0; k < kCols; ++k)
+            if (k < n) store1<DST>(out, to + k, v[k]);
+    }
+}
+
+// ------------------------------------------------------------ sort ---------
+// The key of a token: its id, or `vocab`, after all ids, where it gives nothing to the
+// slice (an id that is none, the padding id, a row outside).
+struct Keys {
+    const void* ids;
+    int wide;
+    int64_t n, padding;
+    Slice s;
+    __device__ __forceinline__ uint32_t get(int64_t t) const {
+        const int64_t id = id_at(ids, wide, t);
+        if (id < 0 || id >= s.vocab || id == padding) return (uint32_t)s.vocab;
+        const int64_t a = id * s.dim - s.begin;
+        return a + s.dim <= 0 || a >= s.count ? (uint32_t)s.vocab : (uint32_t)id;
+    }
+};
+
+// Stable ranks of a wave's keys, 64 at a time: how many equal digits are before each
+// in the wave, counted on in count[digit].
+__device__ __forceinline__ int wave_rank(uint32_t digit, bool valid, int bits, uint32_t* count, int lane) {
+    uint64_t peers = __ballot(valid);
+    for (int b = 0; b < bits; ++b) {
+        const uint64_t set = __ballot((digit >> b) & 1);
+        peers &= (digit >> b) & 1 ? set : ~set;
+    }
+    const int below = __popcll(peers & ((uint64_t(1) << lane) - 1));
+    const uint32_t before = valid ? count[digit] : 0;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (valid && below == 0) count[digit] = before + (uint32_t)__popcll(peers);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    return (int)before + below;
+}
+
+// count[wave][bin] into the number of keys before the wave's first of that bin; add[bin]
+// (or the bins' own sums) is where a bin begins.  Lanes 0 to 511 take a bin each.
+__device__ __forceinline__ void bin_starts(uint32_t (*count)[kBins], const uint32_t* start, uint32_t* sums) {
+    const int t = threadIdx.x;
+    uint32_t total = 0;
+    if (t < kBins)
+        for (int w = 0; w < kSortWaves; ++w) {
+            const uint32_t c = count[w][t];
+            count[w][t] = total;
+            total += c;
+        }
+    uint32_t base = 0;
+    if (start == nullptr) {
+        // exclusive sum over the bins: within waves, then over the 8 waves that hold them
+        uint32_t v = total;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const uint32_t o = (uint32_t)__shfl_up((int)v, off, 64);
+            if ((t & 63) >= off) v += o;
+        }
+        if (t < kBins && (t & 63) == 63) sums[t >> 6] = v;
+        __syncthreads();
+        base = v - total;
+        if (t < kBins)
+            for (int w = 0; w < (t >> 6); ++w) base += sums[w];
+    } else if (t < kBins) {
+        base = start[t];
+    }
+    if (t < kBins)
+        for (int w = 0; w < kSortWaves; ++w) count[w][t] += base;
+    __syncthreads();
+}
+
+// Up to kSmallSort tokens by one block in LDS.
+__global__ void __launch_bounds__(kSortLanes)
+embedding_sort_small_kernel(Keys keys, int passes, int bits, uint32_t* __restrict__ out_key,
+                            uint32_t* __restrict__ out_pos) {
+    __shared__ uint32_t count[kSortWaves][kBins];
+    __shared__ uint32_t sums[kSortWaves];
+    __shared__ uint32_t lk[kSmallSort], lp[kSmallSort];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = (int)keys.n;
+    constexpr int kRounds = kSmallSort / kSortLanes;
+    const int rounds = (n + kSortLanes - 1) / kSortLanes;    // of every wave
+    uint32_t k[kRounds], p[kRounds];
+    int rank[kRounds];
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        const int t = (w * rounds + r) * 64 + lane;
+        k[r] = r < rounds && t < n ? keys.get(t) : 0;
+        p[r] = (uint32_t)t;
+    }
+    for (int pass = 0; pass < passes; ++pass) {
+        for (int b = lane; b < kBins; b += 64) count[w][b] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            if (r >= rounds) break;
+            const bool valid = (w * rounds + r) * 64 + lane < n;
+            rank[r] = wave_rank((k[r] >> (pass * bits)) & ((1u << bits) - 1), valid, bits, count[w], lane);
+        }
+        __syncthreads();
+        bin_starts(count, nullptr, sums);
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            if (r >= rounds) break;
+            if ((w * rounds + r) * 64 + lane < n) {
+                const uint32_t at = count[w][(k[r] >> (pass * bits)) & ((1u << bits) - 1)] + (uint32_t)rank[r];
+                lk[at] = k[r];
+                lp[at] = p[r];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const int t = (w * rounds + r) * 64 + lane;
+            if (r < rounds && t < n) {
+                k[r] = lk[t];
+                p[r] = lp[t];
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        const int t = (w * rounds + r) * 64 + lane;
+        if (r < rounds && t < n) {
+            out_key[t] = k[r];
+            out_pos[t] = p[r];
+        }
+    }
+}
+
+// A pass of the larger sort reads (key, position) pairs, or the ids in the first.
+struct Pairs {
+    const uint32_t *key, *pos;
+};
+__device__ __forceinline__ uint32_t key_of(const Keys& keys, const Pairs& in, int64_t t) {
+    return in.key ? in.key[t] : keys.get(t);
+}
+__global__ void __launch_bounds__(kSortLanes)
+embedding_count_kernel(Keys keys, Pairs in, int shift, int bits, int64_t blocks, uint32_t* __restrict__ counts) {
+    __shared__ uint32_t bin[kBins];
+    if (threadIdx.x < kBins) bin[threadIdx.x] = 0;
+    __syncthreads();
+    const int64_t t0 = (int64_t)blockIdx.x * kSortTile;
+#pragma unroll
+    for (int r = 0; r < kSortTile / kSortLanes; ++r) {
+        const int64_t t = t0 + r * kSortLanes + threadIdx.x;
+        if (t < keys.n) atomicAdd(&bin[(key_of(keys, in, t) >> shift) & ((1u << bits) - 1)], 1u);
+    }
+    __syncthreads();
+    if (threadIdx.x < (1u << bits)) counts[(int64_t)threadIdx.x * blocks + blockIdx.x] = bin[threadIdx.x];
+}
+// Exclusive sums of n counts, by one block.
+__global__ void __launch_bounds__(kSortLanes)
+embedding_scan_kernel(uint32_t* __restrict__ counts, int64_t n) {
+    __shared__ uint32_t sums[kSortWaves];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    uint32_t carry = 0;
+    for (int64_t at = 0; at < n; at += kSortLanes * 4) {
+        uint32_t c[4], total = 0;
+        const int64_t e = at + threadIdx.x * 4;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            c[k] = e + k < n ? counts[e + k] : 0;
+            total += c[k];
+        }
+        uint32_t v = total;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const uint32_t o = (uint32_t)__shfl_up((int)v, off, 64);
+            if (lane >= off) v += o;
+        }
+        if (lane == 63) sums[w] = v;
+        __syncthreads();
+        uint32_t base = carry + v - total, all = 0;
+        for (int k = 0; k < kSortWaves; ++k) {
+            if (k < w) base += sums[k];
+            all += sums[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (e + k < n) counts[e + k] = base;
+            base += c[k];
+        }
+        carry += all;
+        __syncthreads();
+    }
+}
+__global__ void __launch_bounds__(kSortLanes)
+embedding_scatter_kernel(Keys keys, Pairs in, int shift, int bits, int64_t blocks,
+                         const uint32_t* __restrict__ counts, uint32_t* __restrict__ out_key,
+                         uint32_t* __restrict__ out_pos) {
+    __shared__ uint32_t count[kSortWaves][kBins];
+    __shared__ uint32_t start[kBins];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    for (int b = lane; b < kBins; b += 64) count[w][b] = 0;
+    if (threadIdx.x < kBins)
+        start[threadIdx.x] = threadIdx.x < (1u << bits) ? counts[(int64_t)threadIdx.x * blocks + blockIdx.x] : 0;
+    __syncthreads();
+    constexpr int kRounds = kSortTile / kSortLanes;
+    const int64_t t0 = (int64_t)blockIdx.x * kSortTile + w * kRounds * 64 + lane;
+    uint32_t k[kRounds], p[kRounds];
+    int rank[kRounds];
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        const int64_t t = t0 + r * 64;
+        k[r] = t < keys.n ? key_of(keys, in, t) : 0;
+        p[r] = t < keys.n && in.key ? in.pos[t] : (uint32_t)t;
+    }
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r)
+        rank[r] = wave_rank((k[r] >> shift) & ((1u << bits) - 1), t0 + r * 64 < keys.n, bits, count[w], lane);
+    __syncthreads();
+    bin_starts(count, start, nullptr);
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        if (t0 + r * 64 >= keys.n) continue;
+        const uint32_t at = count[w][(k[r] >> shift) & ((1u << bits) - 1)] + (uint32_t)rank[r];
+        out_key[at] = k[r];
+        out_pos[at] = p[r];
+    }
+}
+
+// ------------------------------------------------------------ sums ---------
+struct Sorted {
+    const uint32_t *key, *pos;
+    int64_t n, chunk;          // tokens, and of a chunk
+    int64_t slabs;
+    float* part;               // [chunk][0: of an id that began before; 1: that goes on][dim]
+};
+
+// Adds scale * v to row `id`, columns col .. of the slice (or stores it).
+template <int DST>
+__device__ __forceinline__ void emit(void* grad, const Slice& s, int64_t id, int64_t col, const float* v,
+                                     float scale, int overwrite) {
+    const int64_t at = id * s.dim + col - s.begin;
+    const int n = (int)(s.dim - col < kCols ? s.dim - col : kCols);
+    if (n <= 0) return;
+    if (n == kCols && at >= 0 && at + kCols <= s.count) {
+        float y[kCols];
+        if (overwrite) {
+#pragma unroll
+            for (int k = 0; k < kCols; ++k) y[k] = scale * v[k];
+        } else {
+            const Raw8<DST> old = load8<DST, false>(grad, at);
+#pragma unroll
+            for (int k = 0; k < kCols; ++k) y[k] = fmaf(scale, v[k], old.get(k));
+        }
+        store8<DST, false>(grad, at, y);
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) {
+        const int64_t e = at + k;
+        if (k < n && e >= 0 && e < s.count)
+            store1<DST>(grad, e, overwrite ? scale * v[k] : fmaf(scale, v[k], load1<DST>(grad, e)));
+    }
+}
+__device__ __forceinline__ void store_part(float* part, int64_t dim, int64_t col, const float* v) {
+#pragma unroll
+    for (int k = 0; k < kCols; ++k)
+        if (col + k < dim) part[col + k] = v[k];
+}
+
+// Rows of the slice that no token has become zero: the first blocks of the launch, a
+// wave for `rows` rows.
+template <int DST>
+__device__ __forceinline__ void clear_rows(const Sorted& q, void* grad, const Slice& s, int64_t u, int rows) {
+    const int lane = threadIdx.x & 63;
+    const int64_t first = s.begin / s.dim + u * rows;
+    const int64_t last = (s.begin + s.count + s.dim - 1) / s.dim;
+    const int64_t row = first + lane;
+    bool mine = lane < rows && row < last;
+    if (mine) {                              // the first sorted token not before this row
+        int64_t lo = 0, hi = q.n;
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) >> 1;
+            if ((int64_t)q.key[mid] < row) lo = mid + 1;
+            else hi = mid;
+        }
+        mine = !(lo < q.n && (int64_t)q.key[lo] == row);
+    }
+    uint64_t todo = __ballot(mine);
+    const float zero[kCols] = {0, 0, 0, 0, 0, 0, 0, 0};
+    while (todo) {
+        const int r = __ffsll((unsigned long long)todo) - 1;
+        todo &= todo - 1;
+        for (int64_t col = lane * kCols; col < s.dim; col += kSlab) emit<DST>(grad, s, first + r, col, zero, 0.0f, 1);
+    }
+}
+
+template <int SRC, int DST>
+__global__ void __launch_bounds__(kThreads)
+embedding_sum_kernel(Sorted q, const void* __restrict__ dy, int64_t dy_ld, void* __restrict__ grad, Slice s,
+                     float scale, int overwrite, int64_t clear_blocks, int clear_rows_, int64_t blk0) {
+    const int64_t blk = blk0 + blockIdx.x;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (blk < clear_blocks) {
+        clear_rows<DST>(q, grad, s, blk * (kThreads / 64) + w, clear_rows_);
+        return;
+    }
+    const int64_t u = (blk - clear_blocks) * (kThreads / 64) + w;
+    const int64_t c = u / q.slabs;
+    const int64_t a = c * q.chunk, b = a + q.chunk < q.n ? a + q.chunk : q.n;
+    if (a >= b) return;
+    const uint32_t none = (uint32_t)s.vocab;
+    const int64_t col = (u - c * q.slabs) * kSlab + (threadIdx.x & 63) * kCols;
+    const bool active = col < s.dim, whole = col + kCols <= s.dim;
+    float* part = q.part + 2 * c * s.dim;
+    uint32_t id = q.key[a];
+    if (id == none) return;
+    bool began = a > 0 && q.key[a - 1] == id;      // in an earlier chunk
+    float sum[kCols] = {0, 0, 0, 0, 0, 0, 0, 0};
+    constexpr int U = 4;
+    for (int64_t i = a; i < b; i += U) {
+        Raw8<SRC> r[U];
+        uint32_t key[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            key[k] = i + k < b ? q.key[i + k] : none;
+            if (key[k] != none && active) {
+                const int64_t row = (int64_t)q.pos[i + k] * dy_ld + col;
+                if (whole) {
+                    r[k] = load8<SRC, true>(dy, row);
+                } else {
+                    float v[kCols];
+#pragma unroll
+                    for (int e = 0; e < kCols; ++e) v[e] = col + e < s.dim ? load1<SRC>(dy, row + e) : 0.0f;
+                    if constexpr (SRC == ZERO_FP32) {
+#pragma unroll
+                        for (int e = 0; e < kCols; ++e) r[k].q[e >> 2][e & 3] = __float_as_uint(v[e]);
+                    } else {
+                        uint16_t h[8];
+#pragma unroll
+                        for (int e = 0; e < kCols; ++e) h[e] = narrow<SRC>(v[e]);
+                        r[k].q[0] = pack8(h);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (i + k >= b) break;
+            if (key[k] != id) {
+                if (active) {
+                    if (began) store_part(part, s.dim, col, sum);
+                    else emit<DST>(grad, s, id, col, sum, scale, overwrite);
+                }
+                began = false;
+                id = key[k];
+                if (id == none) return;
+#pragma unroll
+                for (int e = 0; e < kCols; ++e) sum[e] = 0.0f;
+            }
+            if (active) {
+#pragma unroll
+                for (int e = 0; e < kCols; ++e) sum[e] += r[k].get(e);
+            }
+        }
+    }
+    if (!active) return;
+    if (began) store_part(part, s.dim, col, sum);
+    else if (b < q.n && q.key[b] == id) store_part(part + s.dim, s.dim, col, sum);
+    else emit<DST>(grad, s, id, col, sum, scale, overwrite);
+}
+
+// The ids that go on past a chunk's end, at the chunk where they begin: a block adds up
+// their parts of the following chunks for 512 columns, its waves a quarter each, in order.
+template <int DST>
+__global__ void __launch_bounds__(kThreads)
+embedding_join_kernel(Sorted q, void* __restrict__ grad, Slice s, float scale, int overwrite, int64_t blk0) {
+    __shared__ float quarter[kThreads / 64][kSlab];
+    const int64_t u = blk0 + blockIdx.x, c = u / q.slabs;
+    const int64_t a = c * q.chunk, b = a + q.chunk;
+    if (b >= q.n) return;
+    const uint32_t id = q.key[b - 1];
+    if (id == (uint32_t)s.vocab || q.key[b] != id) return;
+    // the id begins in this chunk, not before
+    if (q.key[a] == id && a > 0 && q.key[a - 1] == id) return;
+    int64_t lo = b, hi = q.n;                      // first token after the id's
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (q.key[mid] <= id) lo = mid + 1;
+        else hi = mid;
+    }
+    const int64_t more = (lo - 1) / q.chunk - c;   // chunks that it goes on in
+    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t col = (u - c * q.slabs) * kSlab + lane * kCols;
+    const int64_t per = (more + 3) / 4, from = w * per, to = from + per < more ? from + per : more;
+    float sum[kCols] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (col < s.dim) {
+#pragma unroll 4
+        for (int64_t k = from; k < to; ++k) {
+            const float* p = q.part + 2 * (c + 1 + k) * s.dim;
+#pragma unroll
+            for (int e = 0; e < kCols; ++e) sum[e] += col + e < s.dim ? p[col + e] : 0.0f;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < kCols; ++e) quarter[w][lane * kCols + e] = sum[e];
+    __syncthreads();
+    if (w != 0 || col >= s.dim) return;
+    const float* first = q.part + (2 * c + 1) * s.dim;
+#pragma unroll
+    for (int e = 0; e < kCols; ++e) {
+        float v = col + e < s.dim ? first[col + e] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < kThreads / 64; ++k) v += quarter[k][lane * kCols + e];
+        sum[e] = v;
+    }
+    emit<DST>(grad, s, id, col, sum, scale, overwrite);
+}
+
+// ------------------------------------------------------------ host ---------
+bool valid_type(int32_t dt) { return dt == ZERO_FP32 || dt == ZERO_FP16 || dt == ZERO_BF16; }
+int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+bool misaligned(const void* p, int32_t dt) { return (uintptr_t)p % (dt == ZERO_FP32 ? 4 : 2) != 0; }
+
+int check_sizes(int64_t n_tokens, int64_t vocab, int64_t dim) {
+    if (n_tokens < 0 || vocab < 1 || dim < 1) return ZERO_EINVAL;
+    if (n_tokens > INT32_MAX || vocab > INT32_MAX - 1 || dim > INT32_MAX / 4) return ZERO_ERANGE;
+    return ZERO_OK;
+}
+int check_slice(int64_t vocab, int64_t dim, int64_t begin, int64_t count) {
+    if (begin < 0 || count < 0 || begin > vocab * dim || count > vocab * dim - begin) return ZERO_EINVAL;
+    return ZERO_OK;
+}
+
+// Tokens of a chunk: enough chunks to fill the device, few enough that an id that
+// most tokens have is added up in two short passes.
+constexpr int64_t kLeastChunk = 8, kMostChunk = 512, kChunkUnits = 8192;
+int64_t chunk_for(int64_t n, int64_t slabs) {
+    int64_t c = kLeastChunk;
+    while (c < kMostChunk && n * slabs > c * kChunkUnits) c *= 2;
+    return c;
+}
+// A bound of the chunks of up to n tokens, so that a workspace for n serves fewer.
+int64_t most_chunks(int64_t n, int64_t slabs) {
+    const int64_t few = (n + kLeastChunk - 1) / kLeastChunk, full = kChunkUnits / slabs + 1;
+    const int64_t many = (n + kMostChunk - 1) / kMostChunk;
+    return many > full ? many : few < full ? few : full;
+}
+struct Layout {
+    int64_t key[2], pos[2], counts, part, bytes;
+    int64_t chunk, chunks, slabs, blocks;
+};
+Layout layout_for(int64_t n, int64_t dim) {
+    Layout l;
+    l.slabs = (dim + kSlab - 1) / kSlab;
+    l.chunk = chunk_for(n, l.slabs);
+    l.chunks = (n + l.chunk - 1) / l.chunk;
+    l.blocks = (n + kSortTile - 1) / kSortTile;
+    int64_t at = 0;
+    for (int k = 0; k < 2; ++k) {
+        l.key[k] = at, at = up(at + 4 * n, 256);
+        l.pos[k] = at, at = up(at + 4 * n, 256);
+    }
+    l.counts = at, at = up(at + 4 * kBins * l.blocks, 256);
+    l.part = at, at = up(at + 8 * most_chunks(n, l.slabs) * dim, 256);
+    l.bytes = at;
+    return l;
+}
+
+// go(first block, blocks) for pieces of a launch, in order.
+template <typename F>
+int in_pieces(int64_t blocks, F&& go) {
+    for (int64_t b = 0; b < blocks; b += kMaxLaunchBlocks) {
+        const int rc = go(b, blocks - b < kMaxLaunchBlocks ? blocks - b : kMaxLaunchBlocks);
+        if (rc != ZERO_OK) return rc;
+    }
+    return ZERO_OK;
+}
+
+template <int DT>
+struct Type {
+    static constexpr int value = DT;
+};
+template <typename F>
+int by_type(int32_t dt, F&& go) {
+    return dt == ZERO_FP32 ? go(Type<ZERO_FP32>{}) : dt == ZERO_FP16 ? go(Type<ZERO_FP16>{}) : go(Type<ZERO_BF16>{});
+}
+
+}  // namespace
+
+extern "C" {
+
+int zero_embedding_lookup(void* out, int64_t out_ld, int32_t out_dtype, const void* ids, int32_t id_bytes,
+                          int64_t n_tokens, const void* table, int32_t table_dtype, int64_t vocab, int64_t dim,
+                          int64_t begin, int64_t count, float scale, hipStream_t stream) {
+    if (const int rc = check_sizes(n_tokens, vocab, dim)) return rc;
+    if (const int rc = check_slice(vocab, dim, begin, count)) return rc;
+    if (!valid_type(out_dtype) || !valid_type(table_dtype) || (id_bytes != 4 && id_bytes != 8) ||
+        out_ld < dim || !isfinite(scale))
+        return ZERO_EINVAL;
+    if (n_tokens == 0) return ZERO_OK;
+    int64_t extent;
+    if (__builtin_mul_overflow(out_ld, 4 * n_tokens, &extent)) return ZERO_ERANGE;
+    if (!out || !ids || (count > 0 && !table) || (uintptr_t)ids % id_bytes || misaligned(out, out_dtype) ||
+        misaligned(table, table_dtype))
+        return ZERO_EINVAL;
+    const Slice s = {vocab, dim, begin, count};
+    const int64_t slabs = (dim + kSlab - 1) / kSlab, units = n_tokens * slabs;
+    return by_type(table_dtype, [&](auto src) {
+        return by_type(out_dtype, [&](auto dst) {
+            return in_pieces((units + 3) / 4, [&](int64_t b, int64_t grid) {
+                return launch(embedding_lookup_kernel<decltype(src)::value, decltype(dst)::value>, grid, 0, stream,
+                              out, out_ld, ids, id_bytes == 8, units, slabs, table, s, scale, b);
+            });
+        });
+    });
+}
+
+size_t zero_embedding_workspace_bytes(int64_t n_tokens, int64_t vocab, int64_t dim) {
+    if (check_sizes(n_tokens, vocab, dim) != ZERO_OK) return 0;
+    return (size_t)layout_for(n_tokens, dim).bytes;
+}
+
+int zero_embedding_grad(void* grad, int32_t grad_dtype, const void* ids, int32_t id_bytes, int64_t n_tokens,
+                        const void* dy, int64_t dy_ld, int32_t dy_dtype, int64_t vocab, int64_t dim,
+                        int64_t begin, int64_t count, int64_t padding_id, float scale, int32_t overwrite,
+                        void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (const int rc = check_sizes(n_tokens, vocab, dim)) return rc;
+    if (const int rc = check_slice(vocab, dim, begin, count)) return rc;
+    if (!valid_type(grad_dtype) || !valid_type(dy_dtype) || (id_bytes != 4 && id_bytes != 8) || dy_ld < dim ||
+        !isfinite(scale))
+        return ZERO_EINVAL;
+    if (count == 0 || (n_tokens == 0 && !overwrite)) return ZERO_OK;
+    int64_t extent;
+    if (__builtin_mul_overflow(dy_ld, 4 * n_tokens, &extent)) return ZERO_ERANGE;
+    if (!grad || misaligned(grad, grad_dtype)) return ZERO_EINVAL;
+    if (n_tokens > 0 && (!ids || !dy || (uintptr_t)ids % id_bytes || misaligned(dy, dy_dtype))) return ZERO_EINVAL;
+    const Layout l = layout_for(n_tokens, dim);
+    if (n_tokens > 0 && (!workspace || (uintptr_t)workspace % 256 || workspace_bytes < (size_t)l.bytes))
+        return ZERO_EINVAL;
+    char* ws = (char*)workspace;
+    const Slice s = {vocab, dim, begin, count};
+    Keys keys = {ids, id_bytes == 8, n_tokens, padding_id < 0 ? -1 : padding_id, s};
+    // passes of at most kDigit bits over the keys 0 .. vocab
+    int bits = 1;
+    while ((vocab >> bits) != 0) ++bits;
+    const int passes = (bits + kDigit - 1) / kDigit, per = (bits + passes - 1) / passes;
+    int at = 0;                                     // where the sorted tokens are
+    int rc = ZERO_OK;
+    if (n_tokens > 0 && n_tokens <= kSmallSort) {
+        rc = launch_shape(embedding_sort_small_kernel, 1, kSortLanes, 0, stream, keys, passes, per,
+                          (uint32_t*)(ws + l.key[0]), (uint32_t*)(ws + l.pos[0]));
+    } else if (n_tokens > 0) {
+        uint32_t* counts = (uint32_t*)(ws + l.counts);
+        for (int p = 0; p < passes && rc == ZERO_OK; ++p) {
+            const Pairs in = {p == 0 ? nullptr : (const uint32_t*)(ws + l.key[at]),
+                              p == 0 ? nullptr : (const uint32_t*)(ws + l.pos[at])};
+            const int to = p == 0 ? 0 : at ^ 1;
+            rc = launch_shape(embedding_count_kernel, l.blocks, kSortLanes, 0, stream, keys, in, p * per, per,
+                              l.blocks, counts);
+            if (rc == ZERO_OK)
+                rc = launch_shape(embedding_scan_kernel, 1, kSortLanes, 0, stream, counts, l.blocks << per);
+            if (rc == ZERO_OK)
+                rc = launch_shape(embedding_scatter_kernel, l.blocks, kSortLanes, 0, stream, keys, in, p * per, per,
+                                  l.blocks, (const uint32_t*)counts, (uint32_t*)(ws + l.key[to]),
+                                  (uint32_t*)(ws + l.pos[to]));
+            at = to;
+        }
+    }
+    if (rc != ZERO_OK) return rc;
+    const Sorted q = {(const uint32_t*)(ws + l.key[at]), (const uint32_t*)(ws + l.pos[at]), n_tokens, l.chunk,
+                      l.slabs, (float*)(ws + l.part)};
+    const int64_t size = grad_dtype == ZERO_FP32 ? 4 : 2;
+    int rows = 64;                                   // of a wave that clears, about 64 KiB
+    while (rows > 1 && rows * dim * size > 65536) rows /= 2;
+    const int64_t all_rows = (begin + count + dim - 1) / dim - begin / dim;
+    const int64_t clear = overwrite ? ((all_rows + rows - 1) / rows + 3) / 4 : 0;
+    const int64_t blocks = clear + (l.chunks * l.slabs + 3) / 4;
+    rc = by_type(dy_dtype, [&](auto src) {
+        return by_type(grad_dtype, [&](auto dst) {
+            return in_pieces(blocks, [&](int64_t b, int64_t grid) {
+                return launch(embedding_sum_kernel<decltype(src)::value, decltype(dst)::value>, grid, 0, stream, q,
+                              dy, dy_ld, grad, s, scale, overwrite != 0, clear, rows, b);
+            });
+        });
+    });
+    if (rc != ZERO_OK || l.chunks < 2) return rc;
+    return by_type(grad_dtype, [&](auto dst) {
+        return in_pieces((l.chunks - 1) * l.slabs, [&](int64_t b, int64_t grid) {
+            return launch(embedding_join_kernel<decltype(dst)::value>, grid, 0, stream, q, grad, s, scale,
+                          overwrite != 0, b);
+        });
+    });
+}
+
+}  // extern "C"
