@@ -38,6 +38,7 @@ __device__ __forceinline__ float widen(uint16_t b) {
 // Nearest, ties to even; overflow gives inf, NaN stays (quiet) NaN.
 template <int DT>
 __device__ __forceinline__ uint16_t narrow(float f) {
+    asm("" : "+v"(f));      // rounded to fp32 before (the compiler would skip that)
     if (DT == ZERO_FP16) return __builtin_bit_cast(uint16_t, (_Float16)f);
     const uint32_t u = __float_as_uint(f);
     if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x0040u);

@@ -50,8 +50,11 @@ constexpr float kScaleX = 32768.0f, kScaleA = 16384.0f;
 // below fp16's 65504.
 constexpr double kMostSigma = 1.75;
 constexpr int64_t kMostLong = 4194240, kMostShort = 65536;   // sides of a matrix
-constexpr int kBK = 64;                    // depth of a K step: 128 bytes of a row
+constexpr int kBK = 32;                    // depth of a stage: 64 bytes of a row
 constexpr int kUnitM = 64, kUnitN = 128;   // elements of a unit of the streaming passes
+
+// Square planes of a matrix (A, B and a third) and their vectors.
+constexpr int kPlanes = 3;
 
 // A matrix of the plan, as the kernels read it.
 struct Mat {
@@ -59,8 +62,9 @@ struct Mat {
     void* dst;
     int64_t offset;             // muon: its first element in the shard
     int64_t src_ld, dst_ld;     // elements between rows
-    int64_t x[2], a, b;         // byte offsets of its planes in the workspace
-    int64_t plane_x, plane_a;   // bytes of a plane of X, and of A or B
+    int64_t x[2], p[kPlanes];   // byte offsets in the workspace: X, two of it; the planes
+    int64_t r[kPlanes];         // what the planes' diagonals lost in rounding, fp32
+    int64_t plane_x, plane_a;   // bytes of a part of X, and of a plane
     int64_t part0;              // its first partial of the norm
     int32_t rows, cols;
     int32_t m, n, mp, np;       // its wide form, and that padded to whole tiles
@@ -73,17 +77,27 @@ struct Item {
     uint32_t mat;
     uint16_t i, j;
 };
+// Tiles of a product: the last ones, of a round that would leave most of the device
+// idle, are each cut along the depth into `parts`.
+struct Cut {
+    int64_t whole;
+    int32_t parts, pad;
+};
 // Matrices that go through the steps together.
 struct Group {
     int64_t mat0, n_mats, unit0, n_units, tri0, n_tri, full0, n_full;
+    Cut gram, square, apply;
     int64_t inv_off, part_off;  // the norms' factors and partials in the workspace
-    int32_t tile, pad;
+    int64_t sums_off;           // partial sums of cut tiles
+    int32_t tile, pairs;        // pairs: two steps to a pass over X
 };
 struct Head {
     uint64_t magic;
     int64_t n_groups, groups_off, mats_off, items_off, bytes;
 };
 constexpr uint64_t kMagic = 0x7a65726f6d617431ull;
+
+static_assert(kUnitM * kUnitN == 8192, "4 times 8 elements for each of 256 lanes");
 
 // What a call passes to every kernel.
 struct Step {
@@ -92,11 +106,17 @@ struct Step {
     int64_t n_items;
     char* ws;
     const zero_step_result* res;   // NULL: orthogonalize
-    int64_t inv_off, part_off;
+    int64_t inv_off, part_off, sums_off;
 };
-struct NsConsts {
-    float a, b, c, eps;
-    float scale_b;          // B is kept times this
+// One product.  Its planes hold values times a power of two; the factors undo that.
+//   kGram    out = c X X^T
+//   kSquare  out = p P + q Q + c P Q     (P and Q commute: the product is symmetric)
+//   kApply   X' = p X + c P X
+struct Product {
+    int32_t from;           // which X
+    int32_t p, q, out;      // planes
+    float fp, fq, fc;
+    Cut cut;
 };
 struct MuonConsts {
     float momentum, decay, lr, max_norm;
@@ -131,6 +151,7 @@ __device__ __forceinline__ float widen16(int dt, uint16_t b) {
 }
 // Nearest, ties to even; overflow gives inf, NaN stays (quiet) NaN.
 __device__ __forceinline__ uint16_t narrow16(int dt, float f) {
+    asm("" : "+v"(f));      // rounded to fp32 before (the compiler would skip that)
     if (dt == ZERO_FP16) return __builtin_bit_cast(uint16_t, (f16)f);
     const uint32_t u = __float_as_uint(f);
     if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x0040u);
@@ -140,16 +161,45 @@ __device__ __forceinline__ float load_elem(const void* p, int64_t e, int dt) {
     return dt == ZERO_FP32 ? ((const float*)p)[e] : widen16(dt, ((const uint16_t*)p)[e]);
 }
 
+__device__ __forceinline__ void store_elem(void* p, int64_t e, int dt, float v) {
+    if (dt == ZERO_FP32) ((float*)p)[e] = v;
+    else ((uint16_t*)p)[e] = narrow16(dt, v);
+}
+
+// 8 consecutive elements of a buffer, which may begin at any element.
+typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+__device__ __forceinline__ void load8_f32(const float* p, float* v) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const f32x4 q = *(const f32x4_a4*)(p + 4 * k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * k + e] = q[e];
+    }
+}
+__device__ __forceinline__ void load8_16(int dt, const uint16_t* p, float* v) {
+    const u32x4 q = *(const u32x4_a2*)p;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = widen16(dt, half_of(q, e));
+}
+
 // ------------------------------------------------------------ norm, init ----
-// The element of the update at (row, col) of a matrix.  Source of the two
-// streaming passes: orthogonalize reads the matrix, the Muon step makes the update of
-// gradient and momentum (and stores the momentum in the first pass; the second makes
-// the same value again from what was stored).
+// 8 elements of the update from (row, col) of a matrix, of which n exist (the others are
+// 0).  Source of the two streaming passes: orthogonalize reads the matrix, the Muon step
+// makes the update of gradient and momentum (and stores the momentum in the first pass;
+// the second makes the same value again from what was stored).
 struct OrthSource {
     __device__ void begin(const Step&) {}
     template <bool FIRST>
-    __device__ __forceinline__ float get(const Mat& t, int64_t row, int64_t col) const {
-        return load_elem(t.src, row * t.src_ld + col, t.src_dtype);
+    __device__ __forceinline__ void get(const Mat& t, int64_t row, int64_t col, int n, float* v) const {
+        const int64_t at = row * t.src_ld + col;
+        if (n == 8) {
+            if (t.src_dtype == ZERO_FP32) load8_f32((const float*)t.src + at, v);
+            else load8_16(t.src_dtype, (const uint16_t*)t.src + at, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = e < n ? load_elem(t.src, at + e, t.src_dtype) : 0.0f;
+        }
     }
 };
 template <int DT>
@@ -166,17 +216,54 @@ struct MuonSource {
         }
     }
     template <bool FIRST>
-    __device__ __forceinline__ float get(const Mat& t, int64_t row, int64_t col) const {
-        const int64_t e = t.offset + row * t.cols + col;
-        const float g = widen16(DT, p.g16[e]) * inv * coef;
-        float mo = p.momentum[e];
-        if (FIRST) {
-            mo = c.momentum * mo + g;
-            p.momentum[e] = mo;
+    __device__ __forceinline__ void get(const Mat& t, int64_t row, int64_t col, int n, float* v) const {
+        const int64_t at = t.offset + row * t.cols + col;
+        float g[8], mo[8];
+        if (n == 8) {
+            load8_16(DT, p.g16 + at, g);
+            load8_f32(p.momentum + at, mo);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                g[e] = e < n ? widen16(DT, p.g16[at + e]) : 0.0f;
+                mo[e] = e < n ? p.momentum[at + e] : 0.0f;
+            }
         }
-        return c.nesterov ? g + c.momentum * mo : mo;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            g[e] = g[e] * inv * coef;
+            if (FIRST) mo[e] = c.momentum * mo[e] + g[e];
+            v[e] = c.nesterov ? g[e] + c.momentum * mo[e] : mo[e];
+            if (e >= n) v[e] = 0.0f;
+        }
+        if (FIRST) {
+            if (n == 8) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const f32x4 q = {mo[4 * k], mo[4 * k + 1], mo[4 * k + 2], mo[4 * k + 3]};
+                    *(f32x4_a4*)(p.momentum + at + 4 * k) = q;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e < n) p.momentum[at + e] = mo[e];
+            }
+        }
     }
 };
+
+// A unit is 64 x 128 elements of the wide form: 64 rows of 128 columns in memory, or of
+// a tall matrix 128 rows of 64.  A lane has 8 columns of a row, 4 times; lane_at gives
+// its q-th row and first column in memory, and how many of the 8 exist.
+__device__ __forceinline__ int lane_at(const Mat& t, const Item& it, int q, int64_t& row, int64_t& col) {
+    const int lanes = t.tall ? kUnitM / 8 : kUnitN / 8;       // to a row
+    const int r = (int)threadIdx.x / lanes + q * (kThreads / lanes);
+    row = (int64_t)(t.tall ? it.j * kUnitN : it.i * kUnitM) + r;
+    col = (int64_t)(t.tall ? it.i * kUnitM : it.j * kUnitN) + (int)threadIdx.x % lanes * 8;
+    if (row >= t.rows || col >= t.cols) return 0;
+    return t.cols - col < 8 ? (int)(t.cols - col) : 8;
+}
+constexpr int kQuarters = kUnitM * kUnitN / 8 / kThreads;
 
 // First pass: the sum of squares of every unit's elements, in fp64.
 template <typename Source>
@@ -187,17 +274,16 @@ matrix_norm_kernel(Step s, Source src) {
     const int64_t idx = item_of<8>(blockIdx.x, s.n_items);
     const Item it = s.items[idx];
     const Mat t = s.mats[it.mat];
-    // the unit's rows and columns in the matrix as it lies in memory
-    const int64_t r0 = (int64_t)(t.tall ? it.j * kUnitN : it.i * kUnitM);
-    const int64_t c0 = (int64_t)(t.tall ? it.i * kUnitM : it.j * kUnitN);
-    const int nr = t.tall ? kUnitN : kUnitM, lc = t.tall ? 6 : 7;
     double sum = 0.0;
-    for (int e = threadIdx.x; e < (nr << lc); e += kThreads) {
-        const int64_t row = r0 + (e >> lc), col = c0 + (e & ((1 << lc) - 1));
-        if (row < t.rows && col < t.cols) {
-            const double v = (double)src.template get<true>(t, row, col);
-            sum = fma(v, v, sum);
-        }
+#pragma unroll
+    for (int q = 0; q < kQuarters; ++q) {
+        int64_t row, col;
+        const int n = lane_at(t, it, q, row, col);
+        if (n == 0) continue;
+        float v[8];
+        src.template get<true>(t, row, col, n, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum = fma((double)v[e], (double)v[e], sum);
     }
     __shared__ double part[kThreads / 64];
 #pragma unroll
@@ -227,7 +313,10 @@ matrix_factor_kernel(Step s, float eps) {
     }
 }
 
+// v is made a value of its own first: the compiler would otherwise round the product or
+// sum that it is once, straight to fp16, in one of hi's uses and by way of fp32 in another.
 __device__ __forceinline__ void split(float v, f16& hi, f16& lo) {
+    asm("" : "+v"(v));
     hi = (f16)v;
     lo = (f16)(v - (float)hi);
 }
@@ -242,35 +331,51 @@ matrix_init_kernel(Step s, int64_t mat0, Source src) {
     const Item it = s.items[item_of<8>(blockIdx.x, s.n_items)];
     const Mat t = s.mats[it.mat];
     const float inv = ((const float*)(s.ws + s.inv_off))[it.mat - mat0];
-    const int i0 = it.i * kUnitM, j0 = it.j * kUnitN;
-    if (t.tall) {
-        for (int e = threadIdx.x; e < kUnitM * kUnitN; e += kThreads) {
-            const int r = e >> 6, c = e & 63;
-            const int64_t row = j0 + r, col = i0 + c;
-            turn[r * (kUnitM + 1) + c] =
-                row < t.rows && col < t.cols ? src.template get<false>(t, row, col) : 0.0f;
+    f16* x = (f16*)(s.ws + t.x[0]);
+    const int64_t lower = t.plane_x / 2;
+    float v[kQuarters][8];
+#pragma unroll
+    for (int q = 0; q < kQuarters; ++q) {
+        int64_t row, col;
+        const int n = lane_at(t, it, q, row, col);
+        if (n > 0) {
+            src.template get<false>(t, row, col, n, v[q]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[q][e] = 0.0f;
         }
+    }
+    if (t.tall) {
+#pragma unroll
+        for (int q = 0; q < kQuarters; ++q)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                turn[((int)threadIdx.x / 8 + q * 32) * (kUnitM + 1) + (int)threadIdx.x % 8 * 8 + e] = v[q][e];
         __syncthreads();
     }
-    f16* x = (f16*)(s.ws + t.x[0]);
-    f16* y = (f16*)(s.ws + t.x[0] + t.plane_x);
-    for (int e = threadIdx.x; e < kUnitM * kUnitN; e += kThreads) {
-        const int i = e >> 7, j = e & 127;
-        if (i0 + i >= t.mp || j0 + j >= t.np) continue;
-        float v = 0.0f;
-        if (t.tall) v = turn[j * (kUnitM + 1) + i];
-        else if (i0 + i < t.m && j0 + j < t.n) v = src.template get<false>(t, i0 + i, j0 + j);
-        f16 hi, lo;
-        split(v * inv, hi, lo);
-        const int64_t at = (int64_t)(i0 + i) * t.np + j0 + j;
-        x[at] = hi;
-        y[at] = lo;
+    // lane: 8 columns of a row of the wide form
+#pragma unroll
+    for (int q = 0; q < kQuarters; ++q) {
+        const int i = (int)threadIdx.x / 16 + q * 16, j = (int)threadIdx.x % 16 * 8;
+        if (t.tall) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[q][e] = turn[(j + e) * (kUnitM + 1) + i];
+        }
+        f16x8 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            f16 h, l;
+            split(v[q][e] * inv, h, l);
+            hi[e] = h;
+            lo[e] = l;
+        }
+        const int64_t at = ((int64_t)it.i * kUnitM + i) * t.np + (int64_t)it.j * kUnitN + j;
+        *(f16x8*)(x + at) = hi;
+        *(f16x8*)(x + lower + at) = lo;
     }
 }
 
 // ------------------------------------------------------------ products -----
-enum Product { kGram, kSquare, kApply, kLastOrth, kLastMuon };
-
 // 16 bytes per lane from `base` + lane_off + off straight into LDS at lds + 16 lane.  A
 // buffer access: the tile's address and the row's offset stay in scalar registers and
 // all accesses of a side share one vector register (as global accesses they took over
@@ -280,43 +385,39 @@ __device__ __forceinline__ void copy_to_lds(const f16* base, uint32_t lane_off, 
         __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)0xFFFFFFFF, 0x00027000);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, (int)lane_off, (int)off, 0, 0);
 }
-// ROWS rows of 64 fp16 (128 bytes) from global memory into LDS, the NW waves'
-// share by wave w.  The 16-byte chunk c of row r lies at place c ^ (r & 7) of the
-// row, so that 8 lanes that read the same chunk of 8 rows hit 8 different places.
+// ROWS rows of 32 fp16 (64 bytes) from global memory into LDS, the NW waves' share by
+// wave w.  The 16-byte chunk c of row r lies at place c ^ ((r >> 1) & 3) of the row, so
+// that 8 lanes that read the same chunk of 8 rows hit 8 different places of 128 bytes.
 // A tile's rows span at most 256 * 2 * kMostLong bytes, 2.1e9.
 __device__ __forceinline__ uint32_t rows_lane_off(uint32_t ld, int lane) {
-    return (uint32_t)(lane >> 3) * ld * 2 + (uint32_t)(((lane & 7) ^ (lane >> 3)) * 16);
+    return (uint32_t)(lane >> 2) * ld * 2 + (uint32_t)(((lane & 3) ^ ((lane >> 3) & 3)) * 16);
 }
-template <int ROWS, int NW>
-__device__ __forceinline__ void stage_rows(const f16* base, uint32_t ld, uint32_t lane_off, char* lds, int w) {
-#pragma unroll
-    for (int q = 0; q < ROWS / 8 / NW; ++q) {
-        const uint32_t u = (uint32_t)(q * NW + w);
-        copy_to_lds(base, lane_off, u * 16 * ld, lds + u * 1024);
-    }
+// Access q of the wave.
+template <int NW>
+__device__ __forceinline__ void stage_rows(const f16* base, uint32_t ld, uint32_t lane_off, char* lds, int w,
+                                           int q) {
+    const uint32_t u = (uint32_t)(q * NW + w);
+    copy_to_lds(base, lane_off, u * 32 * ld, lds + u * 1024);
 }
-// 64 rows (depth) of COLS fp16, for reads that transpose: the 16-byte chunk c of row r
-// lies at place c ^ ((r & 3) << 1), so that the 4 rows x 32 bytes that 16 lanes read
-// together hit different banks.
+// 32 rows (depth) of COLS fp16, for reads that transpose: the 16-byte chunk c of row r
+// lies at place c ^ 2 key(r), so that the 8 rows x 32 bytes that 32 lanes read together
+// (rows 0 to 3 and 8 to 11, for instance) hit different banks.
+__device__ __forceinline__ int col_key(int row) { return (row & 3) | ((row >> 1) & 4); }
 template <int COLS, int NW>
-__device__ __forceinline__ uint32_t cols_lane_off(uint32_t ld, int lane, int w) {
+__device__ __forceinline__ uint32_t cols_lane_off(uint32_t ld, int lane, int w, int q) {
     constexpr int kPer = COLS / 8, kRows = 64 / kPer;   // chunks of a row; rows of an access
     const int r = lane / kPer, slot = lane % kPer;
-    const int key = ((w * kRows + r) & 3) << 1;         // the same in all accesses of the wave
-    static_assert(NW * kRows % 4 == 0, "whole turns of the key");
-    return (uint32_t)r * ld * 2 + (uint32_t)((slot ^ key) * 16);
+    return (uint32_t)r * ld * 2 + (uint32_t)((slot ^ (col_key((q * NW + w) * kRows + r) << 1)) * 16);
 }
 template <int COLS, int NW>
-__device__ __forceinline__ void stage_cols(const f16* base, uint32_t ld, uint32_t lane_off, char* lds, int w) {
+__device__ __forceinline__ void stage_cols(const f16* base, uint32_t ld, uint32_t lane_off, char* lds, int w,
+                                           int q) {
     constexpr int kRows = 64 / (COLS / 8);
-#pragma unroll
-    for (int q = 0; q < kBK / kRows / NW; ++q) {
-        const uint32_t u = (uint32_t)(q * NW + w);
-        copy_to_lds(base, lane_off, u * kRows * ld * 2, lds + u * 1024);
-    }
+    const uint32_t u = (uint32_t)(q * NW + w);
+    copy_to_lds(base, lane_off, u * kRows * ld * 2, lds + u * 1024);
 }
 __device__ __forceinline__ f16x8 read_row_frag(const char* lds, int row, int chunk) {
-    return *(const f16x8*)(lds + row * 128 + ((chunk ^ (row & 7)) << 4));
+    return *(const f16x8*)(lds + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
 }
 // Fragment of 16 columns from `col`, lane l's column l % 16, depths k0 + (l / 16) * 8
 // + (0..7): two transposing reads, in each of which lane t of 16 brings 4 columns of
@@ -325,7 +426,7 @@ template <int COLS>
 __device__ __forceinline__ f16x8 read_col_frag(const char* lds, int col, int k0, int lane) {
     const int t = lane & 15, row = k0 + ((lane >> 4) << 3) + (t >> 2);
     const int byte = (col + ((t & 3) << 2)) * 2;
-    const char* p = lds + row * (COLS * 2) + (byte ^ ((row & 3) << 5));
+    const char* p = lds + row * (COLS * 2) + (byte ^ (col_key(row) << 5));
     const f16x4 lo = __builtin_bit_cast(f16x4, __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_fp16x4*)p));
     const f16x4 hi = __builtin_bit_cast(f16x4, __builtin_amdgcn_ds_read_tr16_b64_v4f16(
         (lds_fp16x4*)(p + 4 * COLS * 2)));
@@ -347,21 +448,10 @@ __device__ __forceinline__ void turn_over(char* block, float* at, float* v, int 
 #pragma unroll
     for (int e = 0; e < 16; ++e) v[e] = ((const float*)block)[e * kTurn + lane];
 }
-// 16 elements in one plane, or (plane != 0) in two that lie so far apart.
-__device__ __forceinline__ void load_plane(const f16* p, int64_t plane, float* v) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const f16x8 h = *(const f16x8*)(p + 8 * k);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[8 * k + e] = (float)h[e];
-    }
-    if (plane == 0) return;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const f16x8 l = *(const f16x8*)(p + plane + 8 * k);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[8 * k + e] += (float)l[e];
-    }
+// 16 elements of a plane; stored in one, or (plane != 0) in two that lie so far apart.
+__device__ __forceinline__ void load_plane(const f16* p, f16x8* v) {
+    v[0] = *(const f16x8*)p;
+    v[1] = *(const f16x8*)(p + 8);
 }
 __device__ __forceinline__ void store_plane(f16* p, int64_t plane, const float* v) {
 #pragma unroll
@@ -378,90 +468,274 @@ __device__ __forceinline__ void store_plane(f16* p, int64_t plane, const float* 
         if (plane != 0) *(f16x8*)(p + plane + 8 * k) = l;
     }
 }
-// n <= 16 consecutive elements of a caller's buffer, which may begin at any element.
-typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
-typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
-__device__ __forceinline__ void load_f32(const float* p, int n, float* v) {
-    if (n == 16) {
+// 16 consecutive elements of a buffer, which may begin at any element.
+__device__ __forceinline__ void load_f32(const float* p, float* v) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const f32x4 q = *(const f32x4_a4*)(p + 4 * k);
+    for (int k = 0; k < 4; ++k) {
+        const f32x4 q = *(const f32x4_a4*)(p + 4 * k);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[4 * k + e] = q[e];
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = e < n ? p[e] : 0.0f;
+        for (int e = 0; e < 4; ++e) v[4 * k + e] = q[e];
     }
 }
-__device__ __forceinline__ void store_f32(void* to, int n, const float* v) {
+__device__ __forceinline__ void store_f32(void* to, const float* v) {
     float* p = (float*)to;
-    if (n == 16) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const f32x4 q = {v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]};
-            *(f32x4_a4*)(p + 4 * k) = q;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-            if (e < n) p[e] = v[e];
+    for (int k = 0; k < 4; ++k) {
+        const f32x4 q = {v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]};
+        *(f32x4_a4*)(p + 4 * k) = q;
     }
 }
 template <int DT>
-__device__ __forceinline__ void store_16(void* to, int n, const float* v) {
+__device__ __forceinline__ void store_16(void* to, const float* v) {
     uint16_t* p = (uint16_t*)to;
-    if (n == 16) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            uint16_t h[8];
+    for (int k = 0; k < 2; ++k) {
+        uint16_t h[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[e] = narrow16(DT, v[8 * k + e]);
-            *(u32x4_a2*)(p + 8 * k) = pack8(h);
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-            if (e < n) p[e] = narrow16(DT, v[e]);
+        for (int e = 0; e < 8; ++e) h[e] = narrow16(DT, v[8 * k + e]);
+        *(u32x4_a2*)(p + 8 * k) = pack8(h);
     }
 }
 
-// A tile of one product: T x T, by NW = WM x WN waves.
-//   kGram    A = X X^T          rows of X by rows of X
-//   kSquare  B = b A + c A A    rows of A by rows of A
-//   kApply   X' = a X + B X     rows of B by columns of X; kLast*: into the result
-template <int T, int WM, int WN, int OP, int DT>
-__global__ void __launch_bounds__(WM * WN * 64, 2)
-matrix_product_kernel(Step s, NsConsts ns, int from, int precise, MuonBufs mb, MuonConsts mc) {
-    constexpr int NW = WM * WN, FI = T / WM / 16, FJ = T / WN / 16;
-    static_assert(FJ == 4, "64 columns to a wave");
-    constexpr bool kTri = OP == kGram || OP == kSquare;
+// acc += r l, in place: left to itself the compiler moves accumulators between registers
+// in the loop (856 TFLOP/s, where these reach 1200).  It does not know that these are
+// matrix instructions, whose results other instructions must not touch for some cycles:
+// the accumulators are used by nothing else between the loop's first product and the
+// s_nop after its last.
+__device__ __forceinline__ void mul(f32x4& acc, f16x8 r, f16x8 l) {
+    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(acc) : "v"(r), "v"(l));
+}
+
+// At most N of the wave's loads into LDS are still on their way.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void block_sync() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+enum Kind { kGram, kSquare, kApply, kLastOrth, kLastMuon };
+
+// The end of a tile of T x T (4 waves, a quarter each): 16 rows of 64 columns at a time,
+// what the sums become and what is read for it.
+template <int T, int OP, int DT, bool PRECISE>
+struct Finish {
+    static constexpr int FI = T / 32, FJ = T / 32;       // fragments of a wave
+    static constexpr int kBlocks = FI * FJ / 4;          // of a wave
+    static constexpr bool kTri = OP == kGram || OP == kSquare;
+    // What a block reads: 16 elements per lane of P or X (and its lower part), of Q, of
+    // the weights; what the diagonals lost at the lane's row and columns.
+    struct Beside {
+        f16x8 h[2], l[2];
+        float p[16];
+        float lost_p, lost_q[16];
+    };
+    const Step& s;
+    const Product& c;
+    const Mat& t;
+    const MuonBufs& mb;
+    const MuonConsts& mc;
+    Item it;
+    int lane, wi, wj;
+    char* mine;             // 16 x kTurn floats of LDS
+    float step;             // lr * alpha / kScaleX
+
+    __device__ __forceinline__ void begin() {
+        step = 0.0f;
+        if constexpr (OP == kLastMuon) {
+            double alpha = 1.0;
+            if (mc.scaling == ZERO_MUON_ASPECT && t.rows > t.cols)
+                alpha = sqrt((double)t.rows / (double)t.cols);
+            if (mc.scaling == ZERO_MUON_RMS) alpha = 0.2 * sqrt((double)(t.rows > t.cols ? t.rows : t.cols));
+            step = (float)((double)mc.lr * alpha) * (1.0f / kScaleX);
+        }
+    }
+    // the lane's row and first column of block ij: of the tile's matrix, and of the
+    // result in memory (with how many of 16 columns exist)
+    __device__ __forceinline__ void place(int ij, int64_t& row, int64_t& col) const {
+        row = (int64_t)it.i * T + wi + ij / (FJ / 4) * 16 + (lane >> 2);
+        col = (int64_t)it.j * T + wj + ij % (FJ / 4) * 64 + ((lane & 3) << 4);
+    }
+    __device__ __forceinline__ int result_place(int ij, int64_t& r, int64_t& col) const {
+        place(ij, r, col);
+        if (t.tall) {
+            const int64_t top = r - (lane >> 2);
+            r = col - ((lane & 3) << 4) + lane;
+            col = top;
+        }
+        return r < t.rows && col < t.cols ? (int)(t.cols - col < 16 ? t.cols - col : 16) : 0;
+    }
+    __device__ __forceinline__ void fetch(int ij, Beside& d) const {
+        int64_t row, col;
+        place(ij, row, col);
+        if constexpr (OP == kSquare) {
+            const int64_t at = row * t.mp + col;
+            load_plane((const f16*)(s.ws + t.p[c.p]) + at, d.h);
+            if constexpr (PRECISE) {
+                load_plane((const f16*)(s.ws + t.p[c.p] + t.plane_a) + at, d.l);
+            } else {
+                load_plane((const f16*)(s.ws + t.p[c.q]) + at, d.l);
+                d.lost_p = ((const float*)(s.ws + t.r[c.p]))[row];
+                load_f32((const float*)(s.ws + t.r[c.q]) + col, d.lost_q);
+            }
+        } else if constexpr (!kTri) {
+            const int64_t at = row * t.np + col;
+            load_plane((const f16*)(s.ws + t.x[c.from]) + at, d.h);
+            load_plane((const f16*)(s.ws + t.x[c.from] + t.plane_x) + at, d.l);
+            if constexpr (!PRECISE) d.lost_p = ((const float*)(s.ws + t.r[c.p]))[row];
+        }
+        if constexpr (OP == kLastMuon) {
+            const int n = result_place(ij, row, col);
+            if (n == 16) load_f32(mb.master + t.offset + row * t.cols + col, d.p);
+        }
+    }
+    // 16 consecutive elements of the result, of X's values v, and of the weights p
+    __device__ __forceinline__ void result(int64_t r, int64_t k, float* v, const float* p) const {
+        if constexpr (OP == kLastOrth) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] *= 1.0f / kScaleX;
+            char* out = (char*)t.dst + (r * t.dst_ld + k) * (t.dst_dtype == ZERO_FP32 ? 4 : 2);
+            if (t.dst_dtype == ZERO_FP32) store_f32(out, v);
+            else if (t.dst_dtype == ZERO_FP16) store_16<ZERO_FP16>(out, v);
+            else store_16<ZERO_BF16>(out, v);
+        } else if constexpr (OP == kLastMuon) {
+            const int64_t e0 = t.offset + r * t.cols + k;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = p[e] * mc.decay - step * v[e];
+            store_f32(mb.master + e0, v);
+            store_16<DT>(mb.p16 + e0, v);
+        }
+    }
+    __device__ __forceinline__ void result_one(int64_t r, int64_t k, float v) const {
+        if constexpr (OP == kLastOrth) {
+            store_elem(t.dst, r * t.dst_ld + k, t.dst_dtype, v * (1.0f / kScaleX));
+        } else if constexpr (OP == kLastMuon) {
+            const int64_t e0 = t.offset + r * t.cols + k;
+            const float p = mb.master[e0] * mc.decay - step * v;
+            mb.master[e0] = p;
+            mb.p16[e0] = narrow16(DT, p);
+        }
+    }
+    // Lane l brings row l % 16 and 4 columns from (l / 16) * 4 of 4 fragments.
+    __device__ __forceinline__ void block(int ij, const f32x4* sums, const Beside& d) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            *(f32x4*)(mine + ((lane & 15) * kTurn + j * 16 + ((lane >> 4) << 2)) * 4) = sums[j];
+        wave_sync();
+        int64_t row, col;
+        place(ij, row, col);
+        float* at = (float*)mine + (lane >> 2) * kTurn + ((lane & 3) << 4);
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = at[e];
+        if constexpr (kTri) {
+            f16* out = (f16*)(s.ws + t.p[c.out]);
+            const int64_t lower = PRECISE ? t.plane_a / 2 : 0;
+            if constexpr (OP == kGram) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] *= c.fc;
+            } else if constexpr (PRECISE) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    v[e] = c.fp * ((float)d.h[e >> 3][e & 7] + (float)d.l[e >> 3][e & 7]) + c.fc * v[e];
+            } else {
+                // to first order, what the diagonals of P and Q lost
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float p = (float)d.h[e >> 3][e & 7], q = (float)d.l[e >> 3][e & 7];
+                    v[e] += p * d.lost_q[e] + d.lost_p * q;
+                    if (row == col + e) {
+                        p += d.lost_p;
+                        q += d.lost_q[e];
+                    }
+                    v[e] = c.fp * p + c.fq * q + c.fc * v[e];
+                }
+            }
+            store_plane(out + row * t.mp + col, lower, v);
+            if (it.i != it.j) {
+                turn_over(mine, at, v, lane);
+                store_plane(out + (col - ((lane & 3) << 4) + lane) * t.mp + row - (lane >> 2), lower, v);
+            } else if constexpr (!PRECISE) {
+                float* lost = (float*)(s.ws + t.r[c.out]);
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (row == col + e) lost[row] = v[e] - (float)(f16)v[e];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float h = (float)d.h[e >> 3][e & 7];
+                if constexpr (!PRECISE) v[e] += d.lost_p * h;
+                v[e] = c.fp * (h + (float)d.l[e >> 3][e & 7]) + c.fc * v[e];
+            }
+            if constexpr (OP == kApply) {
+                store_plane((f16*)(s.ws + t.x[c.from ^ 1]) + row * t.np + col, t.plane_x / 2, v);
+            } else {
+                // in memory: row r, 16 consecutive columns from k, or what of them exists
+                int64_t r, k;
+                const int n = result_place(ij, r, k);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) at[e] = v[e];
+                wave_sync();
+                const float* from = t.tall ? (const float*)mine + lane : at;
+                const int every = t.tall ? kTurn : 1;
+                if (n == 16) {
+                    if (t.tall) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] = from[e * kTurn];
+                    }
+                    result(r, k, v, d.p);
+                } else {
+                    for (int e = 0; e < n; ++e) result_one(r, k + e, from[e * every]);
+                }
+            }
+        }
+        wave_sync();
+    }
+};
+
+// A tile of one product, or a part of its depth: T x T by 4 waves, a quarter each, with
+// the sums in registers.  Stages of 32 of the depth go from memory into LDS three ahead of
+// their products, and from LDS into registers one ahead.
+template <int T, int OP, int DT, bool PRECISE>
+__global__ void __launch_bounds__(256, T == 256 ? 1 : 2)
+matrix_product_kernel(Step s, Product c, MuonBufs mb, MuonConsts mc) {
+    using End = Finish<T, OP, DT, PRECISE>;
+    constexpr int NW = 4, FI = End::FI, FJ = End::FJ;
+    constexpr bool kTri = End::kTri;
     constexpr int kSide = T * kBK * 2;      // bytes of a side's stage
     if (skipped(s.res)) return;
+    // four arrays, so that the compiler sees that reads of one do not wait for loads
+    // into another
     __shared__ __attribute__((aligned(1024))) char lds0[2 * kSide];
     __shared__ __attribute__((aligned(1024))) char lds1[2 * kSide];
-    const Item it = s.items[item_of<32>(blockIdx.x, s.n_items)];
+    __shared__ __attribute__((aligned(1024))) char lds2[2 * kSide];
+    __shared__ __attribute__((aligned(1024))) char lds3[2 * kSide];
+    const int64_t cut = (int64_t)blockIdx.x - c.cut.whole;
+    const int64_t n_cut = s.n_items - c.cut.whole;
+    const int part = cut < 0 ? 0 : (int)(cut / n_cut), parts = cut < 0 ? 1 : c.cut.parts;
+    const Item it = s.items[cut < 0 ? item_of<32>(blockIdx.x, c.cut.whole) : c.cut.whole + cut % n_cut];
     const Mat& t = s.mats[it.mat];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wi = (w / WN) * (T / WM), wj = (w % WN) * (T / WN);
+    const int wi = (w / 2) * (T / 2), wj = (w % 2) * (T / 2);
     const int64_t i0 = (int64_t)it.i * T, j0 = (int64_t)it.j * T;
     const int64_t np = t.np, mp = t.mp;
-    const int64_t px = t.plane_x / 2, pa = t.plane_a / 2;
-    const f16* x = (const f16*)(s.ws + t.x[from]);
-    const f16* a = (const f16*)(s.ws + t.a);
-    const f16* b = (const f16*)(s.ws + t.b);
     const f16 *left, *right;
     int64_t left_plane, right_plane, left_ld, right_ld;
     int depth;
     if constexpr (OP == kGram) {
+        const f16* x = (const f16*)(s.ws + t.x[c.from]);
         left = x + i0 * np, right = x + j0 * np;
-        left_plane = right_plane = px, left_ld = right_ld = np, depth = (int)np;
+        left_plane = right_plane = t.plane_x / 2, left_ld = right_ld = np, depth = (int)np;
     } else if constexpr (OP == kSquare) {
-        left = a + i0 * mp, right = a + j0 * mp;
-        left_plane = right_plane = pa, left_ld = right_ld = mp, depth = (int)mp;
+        left = (const f16*)(s.ws + t.p[c.p]) + i0 * mp, right = (const f16*)(s.ws + t.p[c.q]) + j0 * mp;
+        left_plane = right_plane = t.plane_a / 2, left_ld = right_ld = mp, depth = (int)mp;
     } else {
-        left = b + i0 * mp, right = x + j0;
-        left_plane = pa, right_plane = px, left_ld = mp, right_ld = np, depth = (int)mp;
+        left = (const f16*)(s.ws + t.p[c.p]) + i0 * mp, right = (const f16*)(s.ws + t.x[c.from]) + j0;
+        left_plane = t.plane_a / 2, right_plane = t.plane_x / 2, left_ld = mp, right_ld = np, depth = (int)mp;
     }
     f32x4 acc[FI][FJ];
 #pragma unroll
@@ -470,151 +744,179 @@ matrix_product_kernel(Step s, NsConsts ns, int from, int precise, MuonBufs mb, M
         for (int j = 0; j < FJ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
     const uint32_t left_off = rows_lane_off((uint32_t)left_ld, lane);
-    const uint32_t right_off = kTri ? rows_lane_off((uint32_t)right_ld, lane)
-                                    : cols_lane_off<T, NW>((uint32_t)right_ld, lane, w);
-    const int per = depth / kBK, total = precise ? 3 * per : per;
-    auto stage = [&](int k, char* lds) {
-        const int seg = k / per, kk = (k - seg * per) * kBK;   // hi hi, hi lo, lo hi
-        const f16* l = left + (seg == 2 ? left_plane : 0);
-        const f16* r = right + (seg == 1 ? right_plane : 0);
-        stage_rows<T, NW>(l + kk, (uint32_t)left_ld, left_off, lds, w);
-        if constexpr (kTri) stage_rows<T, NW>(r + kk, (uint32_t)right_ld, right_off, lds + kSide, w);
-        else stage_cols<T, NW>(r + kk * right_ld, (uint32_t)right_ld, right_off, lds + kSide, w);
+    // of even and odd accesses: the key of the columns' rows has a period of 16 rows
+    uint32_t right_off[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+        right_off[q] = kTri ? rows_lane_off((uint32_t)right_ld, lane)
+                            : cols_lane_off<T, NW>((uint32_t)right_ld, lane, w, q);
+    static_assert(NW * (512 / T) * 2 % 16 == 0, "the key's period");
+    // stages of the precise form: hi hi, hi lo, lo hi.  A part has a share of them, in
+    // fours.
+    const int per = depth / kBK, fours = (PRECISE ? 3 * per : per) / 4;
+    const int first = (int)((int64_t)fours * part / parts) * 4;
+    const int total = (int)((int64_t)fours * (part + 1) / parts) * 4 - first;
+    const int64_t step_r = kTri ? kBK : (int64_t)kBK * right_ld;
+    int seg = PRECISE ? first / per : 0;
+    int left_in_seg = per - (first - seg * per);
+    const f16* next_l = left + (seg == 2 ? left_plane : 0) + (int64_t)(first - seg * per) * kBK;
+    const f16* next_r = right + (seg == 1 ? right_plane : 0) + (int64_t)(first - seg * per) * step_r;
+    constexpr int kSideLoads = kSide / 1024 / NW, kLoads = 2 * kSideLoads;   // of a wave
+    auto load_piece = [&](char* lds, int q) {       // access q of the next stage
+        if (q < kSideLoads) stage_rows<NW>(next_l, (uint32_t)left_ld, left_off, lds, w, q);
+        else if constexpr (kTri)
+            stage_rows<NW>(next_r, (uint32_t)right_ld, right_off[(q - kSideLoads) & 1], lds + kSide, w,
+                           q - kSideLoads);
+        else
+            stage_cols<T, NW>(next_r, (uint32_t)right_ld, right_off[(q - kSideLoads) & 1], lds + kSide, w,
+                              q - kSideLoads);
     };
-    auto compute = [&](const char* lds) {
+    // Past the last stage the same one is loaded again, which nothing reads.
+    int left_in_all = total;
+    auto loaded = [&] {
+        const bool go = --left_in_all > 0;
+        next_l += go ? kBK : 0;
+        next_r += go ? step_r : 0;
+        if constexpr (PRECISE) {
+            const bool last = --left_in_seg == 0 && go;   // selected, not branched to
+            left_in_seg = last ? per : left_in_seg;
+            seg += last;
+            next_l = last ? left + (seg == 2 ? left_plane : 0) : next_l;
+            next_r = last ? right + (seg == 1 ? right_plane : 0) : next_r;
+        }
+    };
+    auto load = [&](char* lds) {
 #pragma unroll
-        for (int ks = 0; ks < kBK / 32; ++ks) {
-            f16x8 l[FI], r[FJ];
+        for (int q = 0; q < kLoads; ++q) load_piece(lds, q);
+        loaded();
+    };
+    struct Frags {
+        f16x8 l[FI], r[FJ];
+    };
+    auto read_piece = [&](Frags& f, const char* lds, int q) {
+        if (q < FI) f.l[q] = read_row_frag(lds, wi + q * 16 + (lane & 15), lane >> 4);
+        else if constexpr (kTri)
+            f.r[q - FI] = read_row_frag(lds + kSide, wj + (q - FI) * 16 + (lane & 15), lane >> 4);
+        else f.r[q - FI] = read_col_frag<T>(lds + kSide, wj + (q - FI) * 16, 0, lane);
+    };
+    // One stage: its products from registers, while the next stage's fragments come from
+    // LDS and the stage after the next two goes into LDS, a few of each in turn.
+    constexpr int kTurns = FI + FJ, kMuls = FI * FJ / kTurns, kEvery = kTurns / kLoads;
+    static_assert(kMuls * kTurns == FI * FJ && kEvery * kLoads == kTurns, "even turns");
+    auto phase = [&](const Frags& now, Frags& next, const char* from_lds, char* to_lds) {
 #pragma unroll
-            for (int i = 0; i < FI; ++i)
-                l[i] = read_row_frag(lds, wi + i * 16 + (lane & 15), ks * 4 + (lane >> 4));
+        for (int q = 0; q < kTurns; ++q) {
+            read_piece(next, from_lds, q);
+            if (q % kEvery == 0) load_piece(to_lds, q / kEvery);
 #pragma unroll
-            for (int j = 0; j < FJ; ++j) {
-                if constexpr (kTri)
-                    r[j] = read_row_frag(lds + kSide, wj + j * 16 + (lane & 15), ks * 4 + (lane >> 4));
-                else r[j] = read_col_frag<T>(lds + kSide, wj + j * 16, ks * 32, lane);
-            }
-#pragma unroll
-            for (int i = 0; i < FI; ++i)
-#pragma unroll
-                for (int j = 0; j < FJ; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(r[j], l[i], acc[i][j], 0, 0, 0);
+            for (int e = q * kMuls; e < (q + 1) * kMuls; ++e) mul(acc[e / FJ][e % FJ], now.r[e % FJ], now.l[e / FJ]);
             __builtin_amdgcn_sched_barrier(0);
         }
+        loaded();
+        // the next stage but one has to be there; what was loaded here may be on its way
+        wait_loads<kLoads>();
+        block_sync();
     };
-    float step = 0.0f;                      // lr * alpha
-    if constexpr (OP == kLastMuon) {
-        double alpha = 1.0;
-        if (mc.scaling == ZERO_MUON_ASPECT && t.rows > t.cols)
-            alpha = sqrt((double)t.rows / (double)t.cols);
-        if (mc.scaling == ZERO_MUON_RMS) alpha = 0.2 * sqrt((double)(t.rows > t.cols ? t.rows : t.cols));
-        step = (float)((double)mc.lr * alpha);
-    }
-    stage(0, lds0);
-    __syncthreads();
-    for (int k = 0; k + 2 <= total; k += 2) {
-        stage(k + 1, lds1);
-        compute(lds0);
-        __syncthreads();
-        if (k + 2 < total) stage(k + 2, lds0);
-        compute(lds1);
-        __syncthreads();
-    }
-    if constexpr (T == kBK) {   // larger tiles have an even number of steps
-        if (total & 1) {
-            compute(lds0);
-            __syncthreads();
-        }
-    }
+    Frags f0, f1;
+    load(lds0);
+    load(lds1);
+    load(lds2);
+    wait_loads<kLoads>();
+    block_sync();
+#pragma unroll
+    for (int q = 0; q < kTurns; ++q) read_piece(f0, lds0, q);
+    int k = 0;
+    do {                        // there are at least 4 stages
+        phase(f0, f1, lds1, lds3);
+        phase(f1, f0, lds2, lds0);
+        phase(f0, f1, lds3, lds1);
+        phase(f1, f0, lds0, lds2);
+        k += 4;
+    } while (k < total);
+    // the last loads, into LDS that is used again below, and the last products' results,
+    // which nothing else waits for
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_nop 15\n\ts_nop 15" ::: "memory");
+    block_sync();
 
-    // 16 rows of the wave's 64 columns at a time go through LDS, so that what is read
-    // and written beside them is 16 consecutive elements per lane
-    char* mine = ((w & 1) ? lds1 : lds0) + (w >> 1) * (16 * kTurn * 4);
-    const int64_t first = j0 + wj;
+    if (parts > 1) {            // its sums as they are: matrix_join_kernel's work is the rest
+        f32x4* sums = (f32x4*)(s.ws + s.sums_off) + (cut % n_cut * parts + part) * (T * T / 4) +
+                      w * (FI * FJ * 64) + lane;
 #pragma unroll
-    for (int i = 0; i < FI; ++i) {
-        const int64_t top = i0 + wi + i * 16;
-        // lane l holds row l % 16 and 4 columns from (l / 16) * 4 of every fragment
+        for (int e = 0; e < FI * FJ; ++e) sums[e * 64] = acc[e / FJ][e % FJ];
+        return;
+    }
+    // What a block reads comes kAhead blocks before it is used.
+    constexpr int kAhead = 4;
+    char* mine = w == 0 ? lds0 : w == 1 ? lds1 : w == 2 ? lds2 : lds3;
+    static_assert(2 * kSide >= 16 * kTurn * 4, "an array for each wave");
+    End end{s, c, t, mb, mc, it, lane, wi, wj, mine, 0.0f};
+    end.begin();
+    typename End::Beside d[kAhead];
 #pragma unroll
-        for (int j = 0; j < FJ; ++j)
-            *(f32x4*)(mine + ((lane & 15) * kTurn + j * 16 + ((lane >> 4) << 2)) * 4) = acc[i][j];
-        wave_sync();
-        const int64_t row = top + (lane >> 2), col = first + ((lane & 3) << 4);
-        float* at = (float*)mine + (lane >> 2) * kTurn + ((lane & 3) << 4);
-        float v[16];
+    for (int ij = 0; ij < kAhead; ++ij) end.fetch(ij, d[ij]);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = at[e];
-        if constexpr (kTri) {
-            f16* out = (f16*)(s.ws + (OP == kGram ? t.a : t.b));
-            if constexpr (OP == kGram) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] *= kScaleA / (kScaleX * kScaleX);
-            } else {
-                float h[16];
-                load_plane(a + row * mp + col, precise ? pa : 0, h);
-                const float p = ns.b * (ns.scale_b / kScaleA);
-                const float q = ns.c * (ns.scale_b / (kScaleA * kScaleA));
-#pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = p * h[e] + q * v[e];
-            }
-            store_plane(out + row * mp + col, precise ? pa : 0, v);
-            if (it.i != it.j) {
-                turn_over(mine, at, v, lane);
-                store_plane(out + (first + lane) * mp + top, precise ? pa : 0, v);
-            }
-        } else {
-            float h[16];
-            load_plane(x + row * np + col, px, h);
-            const float q = 1.0f / ns.scale_b;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = ns.a * h[e] + q * v[e];
-            if constexpr (OP == kApply) {
-                store_plane((f16*)(s.ws + t.x[from ^ 1]) + row * np + col, px, v);
-            } else {
-                // in memory: row r, 16 consecutive columns from c, or what of them exists
-                int64_t r = row, c = col;
-                if (t.tall) {
-                    turn_over(mine, at, v, lane);
-                    r = first + lane, c = top;
-                }
-                if (r < t.rows && c < t.cols) {
-                    const int n = (int)(t.cols - c < 16 ? t.cols - c : 16);
-                    if constexpr (OP == kLastOrth) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] *= 1.0f / kScaleX;
-                        char* out = (char*)t.dst + (r * t.dst_ld + c) * (t.dst_dtype == ZERO_FP32 ? 4 : 2);
-                        if (t.dst_dtype == ZERO_FP32) store_f32(out, n, v);
-                        else if (t.dst_dtype == ZERO_FP16) store_16<ZERO_FP16>(out, n, v);
-                        else store_16<ZERO_BF16>(out, n, v);
-                    } else {
-                        const int64_t e0 = t.offset + r * t.cols + c;
-                        float p[16];
-                        load_f32(mb.master + e0, n, p);
-                        const float f = step * (1.0f / kScaleX);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) p[e] = p[e] * mc.decay - f * v[e];
-                        store_f32(mb.master + e0, n, p);
-                        store_16<DT>(mb.p16 + e0, n, p);
-                    }
-                }
-            }
-        }
-        wave_sync();
+    for (int ij = 0; ij < End::kBlocks; ++ij) {
+        end.block(ij, &acc[ij / (FJ / 4)][ij % (FJ / 4) * 4], d[ij % kAhead]);
+        if (ij + kAhead < End::kBlocks) end.fetch(ij + kAhead, d[ij % kAhead]);
         __builtin_amdgcn_sched_barrier(0);
     }
+}
+
+// The parts of cut tiles added up, in order: a block has one of the kBlocks blocks of 16
+// rows of 64 columns of each of a tile's waves.
+template <int T, int OP, int DT, bool PRECISE>
+__global__ void __launch_bounds__(256)
+matrix_join_kernel(Step s, Product c, MuonBufs mb, MuonConsts mc) {
+    using End = Finish<T, OP, DT, PRECISE>;
+    if (skipped(s.res)) return;
+    __shared__ __attribute__((aligned(16))) float turn[4][16 * kTurn];
+    const int64_t tile = blockIdx.x / End::kBlocks;
+    const int ij = (int)(blockIdx.x % End::kBlocks);
+    const Item it = s.items[c.cut.whole + tile];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    End end{s, c, s.mats[it.mat], mb, mc, it, lane, (w / 2) * (T / 2), (w % 2) * (T / 2), (char*)turn[w], 0.0f};
+    end.begin();
+    typename End::Beside d;
+    end.fetch(ij, d);
+    f32x4 sum[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const f32x4* sums = (const f32x4*)(s.ws + s.sums_off) + tile * c.cut.parts * (T * T / 4) +
+                        w * (End::FI * End::FJ * 64) + ij * 256 + lane;
+    for (int k = 0; k < c.cut.parts; ++k, sums += T * T / 4)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[j] += sums[j * 64];
+    end.block(ij, sum, d);
 }
 
 // ------------------------------------------------------------ host ---------
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
-// The tile of a matrix's products by its shorter side.
-int tile_for(int64_t m, int64_t n) {
-    (void)n;
-    return m <= 64 ? 64 : m <= 1024 ? 128 : 256;
-}
+// The tile of a matrix's products, by its shorter side.
+int tile_for(int64_t m) { return m <= 1024 ? 128 : 256; }
+// Whether two steps go together: with Q = a + B, the second step's A is Q A Q and what
+// both do to X is Q' Q, products of m x m that replace two of m x n and m x n x m.
+bool pairs_for(int64_t m, int64_t n) { return 2 * n >= 3 * m; }
 // Tiles below the diagonal of a group of matrices, and bytes of its planes, after
 // which the next matrix begins another group.
 constexpr int64_t kGroupTiles = 1024, kGroupBytes = int64_t(4) << 30;
+
+// How the tiles of a product are cut: the last n % slots of them are the last round of
+// blocks on the device.  Costs are in stages of a tile.
+Cut cut_for(int64_t n, int tile, int64_t stages) {
+    const int64_t slots = tile == 256 ? 256 : 512, rest = n % slots;
+    Cut best = {n, 1, 0};
+    if (rest == 0) return best;
+    int64_t least = stages;
+    for (int64_t parts = 2; parts <= 16 && parts * rest <= 2 * slots && stages / parts >= 8; ++parts) {
+        const int64_t cost = (parts * rest + slots - 1) / slots * ((stages + parts - 1) / parts) + 24;
+        if (cost < least) {
+            least = cost;
+            best = {n - rest, (int32_t)parts, 0};
+        }
+    }
+    return best;
+}
 
 struct Build {
     std::vector<Group> groups;
@@ -622,13 +924,13 @@ struct Build {
     std::vector<Item> items;
     int64_t ws = 0;
 
-    bool add(const Mat* in, int64_t count, int tile, bool precise) {
+    bool add(const Mat* in, int64_t count, int tile, bool pairs, bool precise) {
         // longest products first: the last round of blocks is then a short one
         std::vector<Mat> v(in, in + count);
         std::stable_sort(v.begin(), v.end(), [](const Mat& x, const Mat& y) { return x.np > y.np; });
         Group g;
         memset(&g, 0, sizeof g);
-        g.tile = tile;
+        g.tile = tile, g.pairs = pairs;
         g.mat0 = (int64_t)mats.size(), g.n_mats = count;
         int64_t at = 0, parts = 0;
         const int planes = precise ? 2 : 1;
@@ -636,8 +938,10 @@ struct Build {
             t.plane_x = (int64_t)t.mp * t.np * 2, t.plane_a = (int64_t)t.mp * t.mp * 2;
             t.x[0] = at, at = up(at + 2 * t.plane_x, 256);
             t.x[1] = at, at = up(at + 2 * t.plane_x, 256);
-            t.a = at, at = up(at + planes * t.plane_a, 256);
-            t.b = at, at = up(at + planes * t.plane_a, 256);
+            for (int k = 0; k < (pairs ? 3 : 2); ++k) {
+                t.p[k] = at, at = up(at + planes * t.plane_a, 256);
+                t.r[k] = at, at = up(at + 4 * t.mp, 256);
+            }
             const int64_t u = up(t.mp, kUnitM) / kUnitM * (up(t.np, kUnitN) / kUnitN);
             if (u > INT32_MAX) return false;
             t.part0 = parts, t.n_parts = (int32_t)u;
@@ -645,25 +949,44 @@ struct Build {
         }
         g.inv_off = at, at = up(at + 4 * count, 256);
         g.part_off = at, at = up(at + 8 * parts, 256);
-        ws = std::max(ws, at);
+        g.sums_off = at;
         g.unit0 = (int64_t)items.size();
         for (int64_t k = 0; k < count; ++k)
             for (int64_t i = 0; i * kUnitM < v[k].mp; ++i)
                 for (int64_t j = 0; j * kUnitN < v[k].np; ++j) item(g.mat0 + k, i, j);
         g.n_units = (int64_t)items.size() - g.unit0;
+        // blocks of 8 x 8 tiles (below the diagonal), and bands of 4 rows in each column
+        // by column: 32 consecutive tiles, an XCD's, share rows and columns
         g.tri0 = (int64_t)items.size();
-        for (int64_t k = 0; k < count; ++k)
-            for (int64_t i = 0; i * tile < v[k].mp; ++i)
-                for (int64_t j = 0; j <= i; ++j) item(g.mat0 + k, i, j);
+        for (int64_t k = 0; k < count; ++k) {
+            const int64_t q = v[k].mp / tile;
+            for (int64_t bi = 0; bi < q; bi += 8)
+                for (int64_t bj = 0; bj <= bi; bj += 8)
+                    for (int64_t i0 = bi; i0 < bi + 8 && i0 < q; i0 += 4)
+                        for (int64_t j = bj; j < bj + 8 && j < q; ++j)
+                            for (int64_t i = std::max(i0, j); i < i0 + 4 && i < q; ++i) item(g.mat0 + k, i, j);
+        }
         g.n_tri = (int64_t)items.size() - g.tri0;
         g.full0 = (int64_t)items.size();
-        // bands of 4 rows of tiles, column by column: the blocks that run together
-        // share rows of B and columns of X
         for (int64_t k = 0; k < count; ++k)
             for (int64_t i = 0; i * tile < v[k].mp; i += 4)
                 for (int64_t j = 0; j * tile < v[k].np; ++j)
                     for (int64_t q = i; q < i + 4 && q * tile < v[k].mp; ++q) item(g.mat0 + k, q, j);
         g.n_full = (int64_t)items.size() - g.full0;
+        int64_t short_n = INT64_MAX, short_m = INT64_MAX;
+        for (const Mat& t : v) {
+            short_n = std::min<int64_t>(short_n, t.np);
+            short_m = std::min<int64_t>(short_m, t.mp);
+        }
+        const int64_t thrice = precise ? 3 : 1;
+        g.gram = cut_for(g.n_tri, tile, thrice * short_n / kBK);
+        g.square = cut_for(g.n_tri, tile, thrice * short_m / kBK);
+        g.apply = cut_for(g.n_full, tile, thrice * short_m / kBK);
+        int64_t sums = 0;
+        for (const auto& c : {std::make_pair(g.gram, g.n_tri), std::make_pair(g.square, g.n_tri),
+                              std::make_pair(g.apply, g.n_full)})
+            if (c.first.parts > 1) sums = std::max(sums, (c.second - c.first.whole) * c.first.parts);
+        ws = std::max(ws, up(at + sums * tile * tile * 4, 256));
         if (g.n_units > kMaxLaunchBlocks || g.n_full > kMaxLaunchBlocks) return false;
         mats.insert(mats.end(), v.begin(), v.end());
         groups.push_back(g);
@@ -677,23 +1000,25 @@ struct Build {
             t.tall = t.rows > t.cols;
             t.m = std::min(t.rows, t.cols), t.n = std::max(t.rows, t.cols);
         }
-        for (const int tile : {64, 128, 256}) {
+        for (const int kind : {0, 1, 2, 3}) {
+            const int tile = kind < 2 ? 128 : 256;
+            const bool pairs = kind & 1;
             std::vector<Mat> v;
             int64_t tiles = 0, bytes = 0;
             for (Mat& t : in) {
-                if (t.m == 0 || tile_for(t.m, t.n) != tile) continue;
+                if (t.m == 0 || tile_for(t.m) != tile || (!precise && pairs_for(t.m, t.n)) != pairs) continue;
                 t.mp = (int32_t)up(t.m, tile), t.np = (int32_t)up(t.n, tile);
                 const int64_t q = t.mp / tile;
                 v.push_back(t);
                 tiles += q * (q + 1) / 2;
                 bytes += 8 * (int64_t)t.mp * t.np + 8 * (int64_t)t.mp * t.mp;
                 if (tiles >= kGroupTiles || bytes >= kGroupBytes) {
-                    if (!add(v.data(), (int64_t)v.size(), tile, precise)) return ZERO_ERANGE;
+                    if (!add(v.data(), (int64_t)v.size(), tile, pairs, precise)) return ZERO_ERANGE;
                     v.clear();
                     tiles = bytes = 0;
                 }
             }
-            if (!v.empty() && !add(v.data(), (int64_t)v.size(), tile, precise)) return ZERO_ERANGE;
+            if (!v.empty() && !add(v.data(), (int64_t)v.size(), tile, pairs, precise)) return ZERO_ERANGE;
         }
         return ZERO_OK;
     }
@@ -851,27 +1176,46 @@ int guarded(F&& f) {
     }
 }
 
+// Coefficients, and the powers of two that B and T (what two steps together do to X, but
+// for a^2) are kept times.
+struct NsConsts {
+    double a, b, c;
+    float eps;
+    double scale_b, scale_t;
+};
+
 // Bounds of the singular values through the steps, from 1: the largest value that the
-// polynomial takes between 0 and the last bound.  Also a bound of B's eigenvalues.
-// Sampled at 4096 points with the second-order error added.
-bool ns_bounds(const zero_newton_schulz& ns, double* most_b) {
+// polynomial takes between 0 and the last bound; of B's eigenvalues; and of T's, what the
+// polynomial applied twice multiplies a value by, less a^2.  Sampled at 4096 points, the
+// first with its second-order error added.
+bool ns_bounds(const zero_newton_schulz& ns, double* most_b, double* most_t) {
     const double a = ns.a, b = ns.b, c = ns.c;
-    double r = 1.0, top_b = 0.0;
+    double r = 1.0, top_b = 0.0, top_t = 0.0;
     for (int k = 0; k < ns.steps; ++k) {
         const int n = 4096;
         double top = 0.0;
         for (int q = 0; q <= n; ++q) {
             const double x = r * q / n, l = x * x;
-            const double e = b * l + c * l * l;
+            const double e = b * l + c * l * l, y = (a + e) * x, ll = y * y;
             top_b = std::max(top_b, fabs(e));
-            top = std::max(top, fabs((a + e) * x));
+            top_t = std::max(top_t, fabs((a + b * ll + c * ll * ll) * (a + e) - a * a));
+            top = std::max(top, fabs(y));
         }
         const double h = r / n;
         top += h * h / 8 * (6 * fabs(b) * r + 20 * fabs(c) * r * r * r);
         if (!(top <= kMostSigma)) return false;
         r = std::max(top, 1e-3);
     }
-    *most_b = top_b * 1.1 + 1e-3;
+    *most_b = top_b, *most_t = top_t;
+    return true;
+}
+
+// The power of two that takes values up to `most` to at most 2^15, with a tenth to spare.
+bool scale_for(double most, double* scale) {
+    int e = 0;
+    frexp(most * 1.1 + 1e-3, &e);
+    if (e > 15) return false;
+    *scale = ldexp(1.0, std::min(15 - e, 14));
     return true;
 }
 
@@ -880,44 +1224,66 @@ int ns_consts(const zero_newton_schulz* ns, NsConsts* out) {
     if (!isfinite(ns->a) || !isfinite(ns->b) || !isfinite(ns->c) || !isfinite(ns->eps) ||
         !(ns->eps >= 1e-30f))
         return ZERO_EINVAL;
-    double most = 0.0;
-    if (!ns_bounds(*ns, &most)) return ZERO_EINVAL;
+    double most_b = 0.0, most_t = 0.0;
+    if (!ns_bounds(*ns, &most_b, &most_t)) return ZERO_EINVAL;
     out->a = ns->a, out->b = ns->b, out->c = ns->c, out->eps = ns->eps;
-    // the power of two that takes the bound to at most 2^15, and B to at least A's scale / 2^14
-    int e = 0;
-    frexp(most, &e);
-    e = 15 - e;
-    if (e < 0) return ZERO_EINVAL;
-    if (e > 14) e = 14;
-    out->scale_b = ldexpf(1.0f, e);
+    return scale_for(most_b, &out->scale_b) && scale_for(most_t, &out->scale_t) ? ZERO_OK : ZERO_EINVAL;
+}
+
+template <int T, int OP, int DT, bool P>
+int run_product(Step s, const Item* items, int64_t n, const Cut& cut, Product c, const MuonBufs& mb,
+                const MuonConsts& mc, hipStream_t stream) {
+    s.items = items, s.n_items = n;
+    c.cut = cut;
+    int rc = launch(matrix_product_kernel<T, OP, DT, P>, cut.whole + (n - cut.whole) * cut.parts, 0, stream, s, c,
+                    mb, mc);
+    if (rc == ZERO_OK && cut.parts > 1)
+        rc = launch(matrix_join_kernel<T, OP, DT, P>, (n - cut.whole) * Finish<T, OP, DT, P>::kBlocks, 0, stream,
+                    s, c, mb, mc);
+    return rc;
+}
+
+template <int T, int DT, bool P>
+int run_steps(const Step& s, const Group& g, const Item* items, const NsConsts& ns, int steps, bool muon,
+              const MuonBufs& mb, const MuonConsts& mc, hipStream_t stream) {
+    const double a = ns.a, b = ns.b, c = ns.c, sx = kScaleX, sa = kScaleA, sb = ns.scale_b, st = ns.scale_t;
+    int from = 0;
+    auto square = [&](int p, int q, int out, double fp, double fq, double fc) {
+        const Product d = {from, p, q, out, (float)fp, (float)fq, (float)fc, {}};
+        return run_product<T, kSquare, 0, P>(s, items + g.tri0, g.n_tri, g.square, d, mb, mc, stream);
+    };
+    for (int k = 0; k < steps;) {
+        const bool two = g.pairs && k + 2 <= steps;
+        const Product gram = {from, 0, 0, 0, 0.0f, 0.0f, (float)(sa / (sx * sx)), {}};
+        int rc = run_product<T, kGram, 0, P>(s, items + g.tri0, g.n_tri, g.gram, gram, mb, mc, stream);
+        // plane 0: A; plane 1: B = b A + c A A
+        if (rc == ZERO_OK) rc = square(0, 0, 1, b * sb / sa, 0.0, c * sb / (sa * sa));
+        Product last = {from, 1, 0, 0, (float)a, 0.0f, (float)(1.0 / sb), {}};
+        if (two) {
+            // plane 2: Y = A Q = a A + A B;  plane 0: A' = Y Q = a Y + Y B
+            if (rc == ZERO_OK) rc = square(0, 1, 2, a, 0.0, 1.0 / sb);
+            if (rc == ZERO_OK) rc = square(2, 1, 0, a, 0.0, 1.0 / sb);
+            // plane 2: B' = b A' + c A' A';  plane 0: T = Q' Q - a^2 = a B + a B' + B B'
+            if (rc == ZERO_OK) rc = square(0, 0, 2, b * sb / sa, 0.0, c * sb / (sa * sa));
+            if (rc == ZERO_OK) rc = square(1, 2, 0, a * st / sb, a * st / sb, st / (sb * sb));
+            last = {from, 0, 0, 0, (float)(a * a), 0.0f, (float)(1.0 / st), {}};
+        }
+        k += two ? 2 : 1;
+        if (rc == ZERO_OK)
+            rc = k < steps ? run_product<T, kApply, 0, P>(s, items + g.full0, g.n_full, g.apply, last, mb, mc, stream)
+               : muon ? run_product<T, kLastMuon, DT, P>(s, items + g.full0, g.n_full, g.apply, last, mb, mc, stream)
+                      : run_product<T, kLastOrth, 0, P>(s, items + g.full0, g.n_full, g.apply, last, mb, mc, stream);
+        if (rc != ZERO_OK) return rc;
+        from ^= 1;
+    }
     return ZERO_OK;
 }
 
-template <int T, int WM, int WN, int DT>
-int run_steps(const Step& base, const Group& g, const Item* items, const NsConsts& ns, int steps,
-              int precise, bool muon, const MuonBufs& mb, const MuonConsts& mc, hipStream_t stream) {
-    Step tri = base, full = base;
-    tri.items = items + g.tri0, tri.n_items = g.n_tri;
-    full.items = items + g.full0, full.n_items = g.n_full;
-    constexpr int kLanes = WM * WN * 64;
-    for (int k = 0; k < steps; ++k) {
-        const int from = k & 1;
-        int rc = launch_shape(matrix_product_kernel<T, WM, WN, kGram, 0>, g.n_tri, kLanes, 0, stream, tri,
-                              ns, from, precise, mb, mc);
-        if (rc == ZERO_OK)
-            rc = launch_shape(matrix_product_kernel<T, WM, WN, kSquare, 0>, g.n_tri, kLanes, 0, stream, tri,
-                              ns, from, precise, mb, mc);
-        if (rc == ZERO_OK)
-            rc = k + 1 < steps
-                ? launch_shape(matrix_product_kernel<T, WM, WN, kApply, 0>, g.n_full, kLanes, 0, stream,
-                               full, ns, from, precise, mb, mc)
-                : muon ? launch_shape(matrix_product_kernel<T, WM, WN, kLastMuon, DT>, g.n_full, kLanes, 0,
-                                      stream, full, ns, from, precise, mb, mc)
-                       : launch_shape(matrix_product_kernel<T, WM, WN, kLastOrth, 0>, g.n_full, kLanes, 0,
-                                      stream, full, ns, from, precise, mb, mc);
-        if (rc != ZERO_OK) return rc;
-    }
-    return ZERO_OK;
+template <int T, int DT>
+int run_tiles(const Step& s, const Group& g, const Item* items, const NsConsts& ns, int steps, int precise,
+              bool muon, const MuonBufs& mb, const MuonConsts& mc, hipStream_t stream) {
+    return precise ? run_steps<T, DT, true>(s, g, items, ns, steps, muon, mb, mc, stream)
+                   : run_steps<T, DT, false>(s, g, items, ns, steps, muon, mb, mc, stream);
 }
 
 // Every group in turn, on one stream: they share the workspace.
@@ -935,7 +1301,7 @@ int run_groups(const char* host, const char* table, const NsConsts& ns, int step
         s.mats = (const Mat*)(table + h.mats_off);
         s.items = items + g.unit0, s.n_items = g.n_units;
         s.ws = ws, s.res = res;
-        s.inv_off = g.inv_off, s.part_off = g.part_off;
+        s.inv_off = g.inv_off, s.part_off = g.part_off, s.sums_off = g.sums_off;
         int rc = launch(matrix_norm_kernel<Source>, g.n_units, 0, stream, s, src);
         if (rc != ZERO_OK) return rc;
         Step f = s;
@@ -944,9 +1310,8 @@ int run_groups(const char* host, const char* table, const NsConsts& ns, int step
         if (rc != ZERO_OK) return rc;
         rc = launch(matrix_init_kernel<Source>, g.n_units, 0, stream, s, g.mat0, src);
         if (rc != ZERO_OK) return rc;
-        rc = g.tile == 64 ? run_steps<64, 4, 1, DT>(s, g, items, ns, steps, precise, muon, mb, mc, stream)
-           : g.tile == 128 ? run_steps<128, 2, 2, DT>(s, g, items, ns, steps, precise, muon, mb, mc, stream)
-                           : run_steps<256, 2, 4, DT>(s, g, items, ns, steps, precise, muon, mb, mc, stream);
+        rc = g.tile == 128 ? run_tiles<128, DT>(s, g, items, ns, steps, precise, muon, mb, mc, stream)
+                           : run_tiles<256, DT>(s, g, items, ns, steps, precise, muon, mb, mc, stream);
         if (rc != ZERO_OK) return rc;
     }
     return ZERO_OK;
