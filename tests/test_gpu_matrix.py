@@ -79,7 +79,7 @@ def check(got, g, out_type, precise, **ns):
     return off / size if size else 0.0
 
 
-SIZES = [(1, 1), (1, 7), (7, 1), (1, 1000), (3, 200), (16, 1025), (1025, 16), (63, 65), (64, 64), (65, 64),
+SIZES = [(64, 40000), (40001, 5), (1, 1), (1, 7), (7, 1), (1, 1000), (3, 200), (16, 1025), (1025, 16), (63, 65), (64, 64), (65, 64),
          (64, 130), (128, 128), (129, 500), (500, 129), (256, 1030), (1025, 1100), (1300, 1025)]
 
 

@@ -32,6 +32,8 @@
 
 #include <algorithm>
 #include <new>
+#include <stdexcept>
+#include <utility>
 #include <vector>
 
 #include "zero_common.h"
@@ -49,6 +51,8 @@ constexpr float kScaleX = 32768.0f, kScaleA = 16384.0f;
 // Bound of the singular values in all steps: kScaleX * 1.75 and kScaleA * 1.75^2 are
 // below fp16's 65504.
 constexpr double kMostSigma = 1.75;
+// What the steps may multiply an error of X by: X is rounded to 22 bits.
+constexpr double kMostGrowth = 1 << 20;
 constexpr int64_t kMostLong = 4194240, kMostShort = 65536;   // sides of a matrix
 constexpr int kBK = 32;                    // depth of a stage: 64 bytes of a row
 constexpr int kUnitM = 64, kUnitN = 128;   // elements of a unit of the streaming passes
@@ -63,7 +67,7 @@ struct Mat {
     int64_t offset;             // muon: its first element in the shard
     int64_t src_ld, dst_ld;     // elements between rows
     int64_t x[2], p[kPlanes];   // byte offsets in the workspace: X, two of it; the planes
-    int64_t r[kPlanes];         // what the planes' diagonals lost in rounding, fp32
+    int64_t r[kPlanes];         // the planes' diagonals, fp32: what they lost in rounding, and whole
     int64_t plane_x, plane_a;   // bytes of a part of X, and of a plane
     int64_t part0;              // its first partial of the norm
     int32_t rows, cols;
@@ -115,6 +119,7 @@ struct Step {
 struct Product {
     int32_t from;           // which X
     int32_t p, q, out;      // planes
+    int32_t lower;          // p's lower part counts in its own term (kGram: is written)
     float fp, fq, fc;
     Cut cut;
 };
@@ -131,6 +136,14 @@ struct MuonBufs {
 
 __device__ __forceinline__ bool skipped(const zero_step_result* res) {
     return res != nullptr && res->overflow != 0;
+}
+
+// lr * alpha of a matrix.
+__device__ __forceinline__ float muon_step(const Mat& t, const MuonConsts& mc) {
+    double alpha = 1.0;
+    if (mc.scaling == ZERO_MUON_ASPECT && t.rows > t.cols) alpha = sqrt((double)t.rows / (double)t.cols);
+    if (mc.scaling == ZERO_MUON_RMS) alpha = 0.2 * sqrt((double)(t.rows > t.cols ? t.rows : t.cols));
+    return (float)((double)mc.lr * alpha);
 }
 
 // Unit of block b of n, so that consecutive units go to one XCD (workgroups are dealt
@@ -468,6 +481,21 @@ __device__ __forceinline__ void store_plane(f16* p, int64_t plane, const float* 
         if (plane != 0) *(f16x8*)(p + plane + 8 * k) = l;
     }
 }
+// Those of the 16 from `from` up to `to` (any numbers).
+__device__ __forceinline__ void store_some(f16* p, int64_t plane, const float* v, int64_t to, int64_t from) {
+    if (from <= 0 && to >= 16) {
+        store_plane(p, plane, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            if (e < from || e >= to) continue;
+            f16 hi, lo;
+            split(v[e], hi, lo);
+            p[e] = hi;
+            if (plane != 0) p[plane + e] = lo;
+        }
+    }
+}
 // 16 consecutive elements of a buffer, which may begin at any element.
 __device__ __forceinline__ void load_f32(const float* p, float* v) {
 #pragma unroll
@@ -519,6 +547,31 @@ __device__ __forceinline__ void block_sync() {
 
 enum Kind { kGram, kSquare, kApply, kLastOrth, kLastMuon };
 
+// What a product's kernel uses of its matrix, read once: through the table every store
+// would have it read again (a tile's end took 40 us of such waits).
+struct View {
+    const f16 *x, *p, *q;           // X; the planes that are read
+    f16 *to_x, *out;
+    const float *lost_p, *lost_q;   // the planes' diagonals
+    float* lost_out;
+    int64_t mp, np, plane_x, plane_a;       // (the last two in elements)
+    void* dst;
+    int64_t offset, dst_ld;
+    int32_t rows, cols, tall, dst_dtype;
+    float step;                     // lr * alpha
+    __device__ __forceinline__ View(const Mat& t, const Step& s, const Product& c, const MuonConsts& mc) {
+        x = (const f16*)(s.ws + t.x[c.from]), to_x = (f16*)(s.ws + t.x[c.from ^ 1]);
+        p = (const f16*)(s.ws + t.p[c.p]), q = (const f16*)(s.ws + t.p[c.q]);
+        out = (f16*)(s.ws + t.p[c.out]);
+        lost_p = (const float*)(s.ws + t.r[c.p]), lost_q = (const float*)(s.ws + t.r[c.q]);
+        lost_out = (float*)(s.ws + t.r[c.out]);
+        mp = t.mp, np = t.np, plane_x = t.plane_x / 2, plane_a = t.plane_a / 2;
+        dst = t.dst, offset = t.offset, dst_ld = t.dst_ld;
+        rows = t.rows, cols = t.cols, tall = t.tall, dst_dtype = t.dst_dtype;
+        step = muon_step(t, mc);
+    }
+};
+
 // The end of a tile of T x T (4 waves, a quarter each): 16 rows of 64 columns at a time,
 // what the sums become and what is read for it.
 template <int T, int OP, int DT, bool PRECISE>
@@ -526,31 +579,33 @@ struct Finish {
     static constexpr int FI = T / 32, FJ = T / 32;       // fragments of a wave
     static constexpr int kBlocks = FI * FJ / 4;          // of a wave
     static constexpr bool kTri = OP == kGram || OP == kSquare;
-    // What a block reads: 16 elements per lane of P or X (and its lower part), of Q, of
-    // the weights; what the diagonals lost at the lane's row and columns.
+    // What a block reads: 16 elements per lane of P or X, of Q or X's lower part, of P's
+    // lower part, of the weights.
     struct Beside {
-        f16x8 h[2], l[2];
+        f16x8 h[2], l[2], g[2];
         float p[16];
-        float lost_p, lost_q[16];
     };
-    const Step& s;
     const Product& c;
-    const Mat& t;
+    const View& t;
     const MuonBufs& mb;
     const MuonConsts& mc;
     Item it;
     int lane, wi, wj;
     char* mine;             // 16 x kTurn floats of LDS
+    float* sides;           // 2 T floats of LDS: what P's diagonal lost in the tile's rows;
+                            // what Q's lost in its columns, or P's diagonal in its rows
     float step;             // lr * alpha / kScaleX
 
     __device__ __forceinline__ void begin() {
-        step = 0.0f;
-        if constexpr (OP == kLastMuon) {
-            double alpha = 1.0;
-            if (mc.scaling == ZERO_MUON_ASPECT && t.rows > t.cols)
-                alpha = sqrt((double)t.rows / (double)t.cols);
-            if (mc.scaling == ZERO_MUON_RMS) alpha = 0.2 * sqrt((double)(t.rows > t.cols ? t.rows : t.cols));
-            step = (float)((double)mc.lr * alpha) * (1.0f / kScaleX);
+        step = OP == kLastMuon ? t.step * (1.0f / kScaleX) : 0.0f;
+        if constexpr (OP != kGram && !PRECISE) {
+            const float* p = t.lost_p + (int64_t)it.i * T;
+            const float* q = OP == kSquare ? t.lost_q + (int64_t)it.j * T : p + t.mp;
+            for (int e = threadIdx.x; e < T; e += 256) {
+                sides[e] = p[e];
+                sides[T + e] = q[e];
+            }
+            __syncthreads();
         }
     }
     // the lane's row and first column of block ij: of the tile's matrix, and of the
@@ -573,19 +628,21 @@ struct Finish {
         place(ij, row, col);
         if constexpr (OP == kSquare) {
             const int64_t at = row * t.mp + col;
-            load_plane((const f16*)(s.ws + t.p[c.p]) + at, d.h);
+            load_plane(t.p + at, d.h);
             if constexpr (PRECISE) {
-                load_plane((const f16*)(s.ws + t.p[c.p] + t.plane_a) + at, d.l);
+                load_plane(t.p + t.plane_a + at, d.l);
             } else {
-                load_plane((const f16*)(s.ws + t.p[c.q]) + at, d.l);
-                d.lost_p = ((const float*)(s.ws + t.r[c.p]))[row];
-                load_f32((const float*)(s.ws + t.r[c.q]) + col, d.lost_q);
+                load_plane(t.q + at, d.l);
+                if (c.lower) {
+                    load_plane(t.p + t.plane_a + at, d.g);
+                } else {
+                    d.g[0] = d.g[1] = f16x8{0, 0, 0, 0, 0, 0, 0, 0};
+                }
             }
         } else if constexpr (!kTri) {
             const int64_t at = row * t.np + col;
-            load_plane((const f16*)(s.ws + t.x[c.from]) + at, d.h);
-            load_plane((const f16*)(s.ws + t.x[c.from] + t.plane_x) + at, d.l);
-            if constexpr (!PRECISE) d.lost_p = ((const float*)(s.ws + t.r[c.p]))[row];
+            load_plane(t.x + at, d.h);
+            load_plane(t.x + t.plane_x + at, d.l);
         }
         if constexpr (OP == kLastMuon) {
             const int n = result_place(ij, row, col);
@@ -632,8 +689,8 @@ struct Finish {
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = at[e];
         if constexpr (kTri) {
-            f16* out = (f16*)(s.ws + t.p[c.out]);
-            const int64_t lower = PRECISE ? t.plane_a / 2 : 0;
+            f16* out = t.out;
+            const int64_t lower = PRECISE || (OP == kGram && c.lower) ? t.plane_a : 0;
             if constexpr (OP == kGram) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) v[e] *= c.fc;
@@ -643,36 +700,59 @@ struct Finish {
                     v[e] = c.fp * ((float)d.h[e >> 3][e & 7] + (float)d.l[e >> 3][e & 7]) + c.fc * v[e];
             } else {
                 // to first order, what the diagonals of P and Q lost
+                const float lost_p = sides[row - (int64_t)it.i * T];
+                const float* lost_q = sides + T + (col - (int64_t)it.j * T);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    float p = (float)d.h[e >> 3][e & 7], q = (float)d.l[e >> 3][e & 7];
-                    v[e] += p * d.lost_q[e] + d.lost_p * q;
-                    if (row == col + e) {
-                        p += d.lost_p;
-                        q += d.lost_q[e];
-                    }
-                    v[e] = c.fp * p + c.fq * q + c.fc * v[e];
+                    const float p = (float)d.h[e >> 3][e & 7], q = (float)d.l[e >> 3][e & 7];
+                    v[e] += p * lost_q[e] + lost_p * q;
+                    v[e] = c.fp * (p + (float)d.g[e >> 3][e & 7]) + c.fq * q + c.fc * v[e];
+                }
+                if (it.i == it.j) {
+                    const float own = c.lower ? 0.0f : c.fp * lost_p;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (row == col + e) v[e] += own + c.fq * lost_q[e];
                 }
             }
-            store_plane(out + row * t.mp + col, lower, v);
+            // Below the diagonal as it is, above it turned over, in the diagonal's tiles too:
+            // a product of planes that are not quite symmetric is not quite either, and the
+            // next one, which reads rows for columns, would not be one of the same polynomial
+            // (96 x 300 was off by 4e-3 in the place of 5e-4).
+            const int64_t turned = col - ((lane & 3) << 4) + lane, top = row - (lane >> 2);
             if (it.i != it.j) {
+                store_plane(out + row * t.mp + col, lower, v);
                 turn_over(mine, at, v, lane);
-                store_plane(out + (col - ((lane & 3) << 4) + lane) * t.mp + row - (lane >> 2), lower, v);
-            } else if constexpr (!PRECISE) {
-                float* lost = (float*)(s.ws + t.r[c.out]);
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (row == col + e) lost[row] = v[e] - (float)(f16)v[e];
+                store_plane(out + turned * t.mp + top, lower, v);
+            } else {
+                store_some(out + row * t.mp + col, lower, v, row - col + 1, 0);
+                turn_over(mine, at, v, lane);
+                store_some(out + turned * t.mp + top, lower, v, 16, turned - top + 1);
+                if constexpr (!PRECISE) {
+                    // back to the lane's row: its element on the diagonal
+                    const int64_t own = row - col;
+                    const float u = own >= 0 && own < 16 ? at[own] : 0.0f;
+                    if (own >= 0 && own < 16) {
+                        t.lost_out[row] = u - (float)(f16)u;
+                        t.lost_out[t.mp + row] = u;
+                    }
+                }
             }
         } else {
+            float lost_p = 0.0f, diag_p = 0.0f;
+            if constexpr (!PRECISE) {
+                lost_p = sides[row - (int64_t)it.i * T];
+                diag_p = sides[T + row - (int64_t)it.i * T];
+            }
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                const float h = (float)d.h[e >> 3][e & 7];
-                if constexpr (!PRECISE) v[e] += d.lost_p * h;
-                v[e] = c.fp * (h + (float)d.l[e >> 3][e & 7]) + c.fc * v[e];
+                const float h = (float)d.h[e >> 3][e & 7], l = (float)d.l[e >> 3][e & 7];
+                // to first order, what P's diagonal lost, and P times X's lower part
+                if constexpr (!PRECISE) v[e] += lost_p * h + diag_p * l;
+                v[e] = c.fp * (h + l) + c.fc * v[e];
             }
             if constexpr (OP == kApply) {
-                store_plane((f16*)(s.ws + t.x[c.from ^ 1]) + row * t.np + col, t.plane_x / 2, v);
+                store_plane(t.to_x + row * t.np + col, t.plane_x, v);
             } else {
                 // in memory: row r, 16 consecutive columns from k, or what of them exists
                 int64_t r, k;
@@ -697,6 +777,11 @@ struct Finish {
     }
 };
 
+template <size_t... I, typename F>
+__device__ __forceinline__ void each_of(std::index_sequence<I...>, F&& f) {
+    (f(std::integral_constant<size_t, I>{}), ...);
+}
+
 // A tile of one product, or a part of its depth: T x T by 4 waves, a quarter each, with
 // the sums in registers.  Stages of 32 of the depth go from memory into LDS three ahead of
 // their products, and from LDS into registers one ahead.
@@ -718,7 +803,7 @@ matrix_product_kernel(Step s, Product c, MuonBufs mb, MuonConsts mc) {
     const int64_t n_cut = s.n_items - c.cut.whole;
     const int part = cut < 0 ? 0 : (int)(cut / n_cut), parts = cut < 0 ? 1 : c.cut.parts;
     const Item it = s.items[cut < 0 ? item_of<32>(blockIdx.x, c.cut.whole) : c.cut.whole + cut % n_cut];
-    const Mat& t = s.mats[it.mat];
+    const View t(s.mats[it.mat], s, c, mc);
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wi = (w / 2) * (T / 2), wj = (w % 2) * (T / 2);
     const int64_t i0 = (int64_t)it.i * T, j0 = (int64_t)it.j * T;
@@ -727,15 +812,14 @@ matrix_product_kernel(Step s, Product c, MuonBufs mb, MuonConsts mc) {
     int64_t left_plane, right_plane, left_ld, right_ld;
     int depth;
     if constexpr (OP == kGram) {
-        const f16* x = (const f16*)(s.ws + t.x[c.from]);
-        left = x + i0 * np, right = x + j0 * np;
-        left_plane = right_plane = t.plane_x / 2, left_ld = right_ld = np, depth = (int)np;
+        left = t.x + i0 * np, right = t.x + j0 * np;
+        left_plane = right_plane = t.plane_x, left_ld = right_ld = np, depth = (int)np;
     } else if constexpr (OP == kSquare) {
-        left = (const f16*)(s.ws + t.p[c.p]) + i0 * mp, right = (const f16*)(s.ws + t.p[c.q]) + j0 * mp;
-        left_plane = right_plane = t.plane_a / 2, left_ld = right_ld = mp, depth = (int)mp;
+        left = t.p + i0 * mp, right = t.q + j0 * mp;
+        left_plane = right_plane = t.plane_a, left_ld = right_ld = mp, depth = (int)mp;
     } else {
-        left = (const f16*)(s.ws + t.p[c.p]) + i0 * mp, right = (const f16*)(s.ws + t.x[c.from]) + j0;
-        left_plane = t.plane_a / 2, right_plane = t.plane_x / 2, left_ld = mp, right_ld = np, depth = (int)mp;
+        left = t.p + i0 * mp, right = t.x + j0;
+        left_plane = t.plane_a, right_plane = t.plane_x, left_ld = mp, right_ld = np, depth = (int)mp;
     }
     f32x4 acc[FI][FJ];
 #pragma unroll
@@ -848,18 +932,20 @@ matrix_product_kernel(Step s, Product c, MuonBufs mb, MuonConsts mc) {
     // What a block reads comes kAhead blocks before it is used.
     constexpr int kAhead = 4;
     char* mine = w == 0 ? lds0 : w == 1 ? lds1 : w == 2 ? lds2 : lds3;
-    static_assert(2 * kSide >= 16 * kTurn * 4, "an array for each wave");
-    End end{s, c, t, mb, mc, it, lane, wi, wj, mine, 0.0f};
+    constexpr int kMine = 16 * kTurn * 4;
+    static_assert(2 * kSide >= kMine + 8 * T, "an array for each wave, and the sides");
+    End end{c, t, mb, mc, it, lane, wi, wj, mine, (float*)(lds0 + kMine), 0.0f};
     end.begin();
     typename End::Beside d[kAhead];
 #pragma unroll
     for (int ij = 0; ij < kAhead; ++ij) end.fetch(ij, d[ij]);
-#pragma unroll
-    for (int ij = 0; ij < End::kBlocks; ++ij) {
+    // (a loop of this size the compiler would leave a loop, and the sums in memory)
+    each_of(std::make_index_sequence<End::kBlocks>(), [&](auto at) {
+        constexpr int ij = (int)decltype(at)::value;
         end.block(ij, &acc[ij / (FJ / 4)][ij % (FJ / 4) * 4], d[ij % kAhead]);
-        if (ij + kAhead < End::kBlocks) end.fetch(ij + kAhead, d[ij % kAhead]);
+        if constexpr (ij + kAhead < End::kBlocks) end.fetch(ij + kAhead, d[ij % kAhead]);
         __builtin_amdgcn_sched_barrier(0);
-    }
+    });
 }
 
 // The parts of cut tiles added up, in order: a block has one of the kBlocks blocks of 16
@@ -869,12 +955,13 @@ __global__ void __launch_bounds__(256)
 matrix_join_kernel(Step s, Product c, MuonBufs mb, MuonConsts mc) {
     using End = Finish<T, OP, DT, PRECISE>;
     if (skipped(s.res)) return;
-    __shared__ __attribute__((aligned(16))) float turn[4][16 * kTurn];
+    __shared__ __attribute__((aligned(16))) float turn[4][16 * kTurn], sides[2 * T];
     const int64_t tile = blockIdx.x / End::kBlocks;
     const int ij = (int)(blockIdx.x % End::kBlocks);
     const Item it = s.items[c.cut.whole + tile];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    End end{s, c, s.mats[it.mat], mb, mc, it, lane, (w / 2) * (T / 2), (w % 2) * (T / 2), (char*)turn[w], 0.0f};
+    const View t(s.mats[it.mat], s, c, mc);
+    End end{c, t, mb, mc, it, lane, (w / 2) * (T / 2), (w % 2) * (T / 2), (char*)turn[w], sides, 0.0f};
     end.begin();
     typename End::Beside d;
     end.fetch(ij, d);
@@ -889,14 +976,249 @@ matrix_join_kernel(Step s, Product c, MuonBufs mb, MuonConsts mc) {
     end.block(ij, sum, d);
 }
 
+// ------------------------------------------------------------ small --------
+// Matrices whose shorter side is at most 64 (a low-rank adapter's factors, vectors) go
+// another way: the Gram matrix A = U U^T of the whole update, all steps on it alone,
+//     Q = a + b A + c A A,   P <- Q P,   A <- Q A Q,
+// and the result P U / (||U|| + eps): two passes over the matrix and three launches, all to
+// 32 bits.  A's rounding grows with the square of what the steps multiply small singular
+// values by, so A, Q and P are fp64.  (The way of the larger ones, three launches for
+// each step, took 250 us for 56 factors of 16 x 2048, this one SMALL_US.)
+constexpr int kSmall = 64;                 // shorter side, at most
+constexpr int kSmallCols = 128;            // columns of the wide form that are in LDS at once
+constexpr int kSmallParts = 256;           // blocks of a matrix, at most
+constexpr int kSmallLd = kSmall + 4, kSmallRow = kSmallCols + 4;
+
+// 8 elements of the update at once: item q of a chunk of kSmallCols columns from c0, as
+// (i, k) of the wide form and their direction.  False past the chunk.
+__device__ __forceinline__ bool small_item(const Mat& t, int q, int64_t c0, int& i, int& k, int& n) {
+    if (t.tall) {
+        const int per = (t.m + 7) / 8;
+        k = q / per, i = q % per * 8;
+        n = c0 + k < t.n ? (t.m - i < 8 ? t.m - i : 8) : 0;
+        return k < kSmallCols;
+    }
+    i = q / (kSmallCols / 8), k = q % (kSmallCols / 8) * 8;
+    const int64_t left = t.n - c0 - k;
+    n = left < 0 ? 0 : left < 8 ? (int)left : 8;
+    return i < t.m;
+}
+// A chunk of the update into LDS: by column (to[k * LD + i]), or by row (to[i * LD + k]),
+// times `by`.
+template <bool FIRST, bool BY_COLUMN, typename Source>
+__device__ __forceinline__ void small_load(const Mat& t, const Source& src, int64_t c0, float by, float* to) {
+    for (int q = threadIdx.x;; q += kThreads) {
+        int i, k, n;
+        if (!small_item(t, q, c0, i, k, n)) break;
+        float v[8];
+        if (n > 0) {
+            src.template get<FIRST>(t, t.tall ? c0 + k : i, t.tall ? i : c0 + k, n, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int ii = t.tall ? i + e : i, kk = t.tall ? k : k + e;
+            if (ii < kSmall) to[BY_COLUMN ? kk * kSmallLd + ii : ii * kSmallRow + kk] = v[e] * by;
+        }
+    }
+}
+
+// First pass: a block's part of U U^T, its columns' sums in fp64.  A thread has 4 x 4
+// elements of A and every S-th column.
+template <typename Source>
+__global__ void __launch_bounds__(kThreads)
+small_gram_kernel(Step s, Source src) {
+    if (skipped(s.res)) return;
+    src.begin(s);
+    __shared__ __attribute__((aligned(16))) float u[kSmallCols * kSmallLd];
+    __shared__ double red[16][kThreads];
+    const Item it = s.items[blockIdx.x];
+    const Mat t = s.mats[it.mat];
+    const int side = (t.m + 3) / 4, blocks = side * side, slices = kThreads / blocks;
+    const int blk = (int)threadIdx.x % blocks, slice = (int)threadIdx.x / blocks;
+    const int bi = blk / side * 4, bj = blk % side * 4;
+    for (int e = threadIdx.x; e < kSmallCols * kSmallLd; e += kThreads) u[e] = 0.0f;
+    __syncthreads();
+    double acc[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[e] = 0.0;
+    const int64_t end = (int64_t)(it.i + 1) * t.np < t.n ? (int64_t)(it.i + 1) * t.np : t.n;
+    for (int64_t c0 = (int64_t)it.i * t.np; c0 < end; c0 += kSmallCols) {
+        small_load<true, true>(t, src, c0, 1.0f, u);
+        __syncthreads();
+        if (slice < slices) {
+            for (int k = slice; k < kSmallCols; k += slices) {
+                const f32x4 x = *(const f32x4*)(u + k * kSmallLd + bi), y = *(const f32x4*)(u + k * kSmallLd + bj);
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) acc[p * 4 + q] = fma((double)x[p], (double)y[q], acc[p * 4 + q]);
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) red[e][threadIdx.x] = acc[e];
+    __syncthreads();
+    double* out = (double*)(s.ws + t.p[0]) + (int64_t)it.i * blocks * 16;
+    for (int e = threadIdx.x; e < blocks * 16; e += kThreads) {
+        double sum = 0.0;
+        for (int k = 0; k < slices; ++k) sum += red[e & 15][k * blocks + (e >> 4)];
+        out[e] = sum;
+    }
+}
+
+// One block per matrix: A from its parts, and the steps.
+struct SmallNs {
+    double a, b, c, eps;
+    int32_t steps, pad;
+};
+__global__ void __launch_bounds__(kThreads)
+small_steps_kernel(Step s, SmallNs ns) {
+    if (skipped(s.res)) return;
+    constexpr int kLd = kSmall + 1;
+    __shared__ double A[kSmall * kLd], Q[kSmall * kLd], P[kSmall * kLd], W[kSmall * kLd];
+    __shared__ double norm;
+    const Mat t = s.mats[blockIdx.x];
+    const int side = (t.m + 3) / 4, blocks = side * side, tid = threadIdx.x;
+    const int bi = tid / side * 4, bj = tid % side * 4;
+    const bool on = tid < blocks;
+    const double* part = (const double*)(s.ws + t.p[0]);
+    for (int e = tid; e < blocks * 16; e += kThreads) {
+        double sum = 0.0;
+        for (int k = 0; k < t.n_parts; ++k) sum += part[(int64_t)k * blocks * 16 + e];
+        const int b = e >> 4, p = (e & 15) >> 2, q = e & 3;
+        A[(b / side * 4 + p) * kLd + b % side * 4 + q] = sum;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        double sum = 0.0;
+        for (int k = 0; k < t.m; ++k) sum += A[k * kLd + k];
+        norm = sqrt(sum) + ns.eps;
+        ((float*)(s.ws + t.r[0]))[0] = (float)(1.0 / norm);
+    }
+    __syncthreads();
+    double c[16];
+    auto product = [&](const double* x, const double* y) {     // the thread's 4 x 4 of x y
+#pragma unroll
+        for (int e = 0; e < 16; ++e) c[e] = 0.0;
+        if (on)
+            for (int k = 0; k < side * 4; ++k) {
+                double u[4], v[4];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) u[p] = x[(bi + p) * kLd + k], v[p] = y[k * kLd + bj + p];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) c[e] = fma(u[e >> 2], v[e & 3], c[e]);
+            }
+        __syncthreads();
+    };
+    auto each = [&](auto&& f) {                                 // f(element, its product)
+        if (on) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) f((bi + (e >> 2)) * kLd + bj + (e & 3), c[e], bi + (e >> 2) == bj + (e & 3));
+        }
+        __syncthreads();
+    };
+    const double inv = 1.0 / (norm * norm);
+    each([&](int at, double, bool) { A[at] *= inv; });
+    for (int k = 0; k < ns.steps; ++k) {
+        product(A, A);
+        each([&](int at, double v, bool diag) {
+            Q[at] = (diag ? ns.a : 0.0) + ns.b * A[at] + ns.c * v;
+            if (k == 0) P[at] = Q[at];
+        });
+        if (k > 0) {
+            product(Q, P);
+            each([&](int at, double v, bool) { P[at] = v; });
+        }
+        if (k + 1 == ns.steps) break;
+        product(Q, A);
+        each([&](int at, double v, bool) { W[at] = v; });
+        product(W, Q);
+        each([&](int at, double v, bool) { A[at] = v; });
+    }
+    float* out = (float*)(s.ws + t.p[1]);
+    for (int e = tid; e < side * 4 * kSmall; e += kThreads) {
+        const int i = e / kSmall, j = e % kSmall;
+        out[e] = j < side * 4 ? (float)P[i * kLd + j] : 0.0f;
+    }
+}
+
+// Second pass: P (U / norm), a block's columns, and what becomes of it.  A thread has 4 rows
+// and 4 columns at a time.
+template <bool MUON, int DT, typename Source>
+__global__ void __launch_bounds__(kThreads)
+small_apply_kernel(Step s, Source src, MuonBufs mb, MuonConsts mc) {
+    if (skipped(s.res)) return;
+    src.begin(s);
+    __shared__ __attribute__((aligned(16))) float u[kSmall * kSmallRow];
+    __shared__ __attribute__((aligned(16))) float P[kSmall * kSmall];
+    const Item it = s.items[blockIdx.x];
+    const Mat t = s.mats[it.mat];
+    const int side = (t.m + 3) / 4;
+    const float inv = ((const float*)(s.ws + t.r[0]))[0];
+    for (int e = threadIdx.x; e < side * 4 * kSmall; e += kThreads) P[e] = ((const float*)(s.ws + t.p[1]))[e];
+    for (int e = threadIdx.x; e < kSmall * kSmallRow; e += kThreads) u[e] = 0.0f;
+    __syncthreads();
+    const float step = MUON ? muon_step(t, mc) : 0.0f;
+    const int64_t end = (int64_t)(it.i + 1) * t.np < t.n ? (int64_t)(it.i + 1) * t.np : t.n;
+    for (int64_t c0 = (int64_t)it.i * t.np; c0 < end; c0 += kSmallCols) {
+        small_load<false, false>(t, src, c0, inv, u);
+        __syncthreads();
+        for (int q = threadIdx.x; q < side * (kSmallCols / 4); q += kThreads) {
+            const int i = q / (kSmallCols / 4) * 4, k = q % (kSmallCols / 4) * 4;
+            float o[4][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}};
+            for (int j = 0; j < t.m; ++j) {
+                const f32x4 x = *(const f32x4*)(P + j * kSmall + i), y = *(const f32x4*)(u + j * kSmallRow + k);
+#pragma unroll
+                for (int a = 0; a < 4; ++a)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) o[a][b] = fmaf(x[a], y[b], o[a][b]);
+            }
+            // four runs of up to 4 elements in memory
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                const int64_t r = t.tall ? c0 + k + a : i + a, c = t.tall ? i : c0 + k;
+                if (r >= t.rows) continue;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    if (c + b >= t.cols) continue;
+                    const float v = t.tall ? o[b][a] : o[a][b];
+                    if constexpr (MUON) {
+                        const int64_t at = t.offset + r * t.cols + c + b;
+                        const float w = mb.master[at] * mc.decay - step * v;
+                        mb.master[at] = w;
+                        mb.p16[at] = narrow16(DT, w);
+                    } else {
+                        store_elem(t.dst, r * t.dst_ld + c + b, t.dst_dtype, v);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
 // ------------------------------------------------------------ host ---------
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
-// The tile of a matrix's products, by its shorter side.
-int tile_for(int64_t m) { return m <= 1024 ? 128 : 256; }
+// Matrices with a shorter side of at most kTogether take their steps in pairs, and are `many`
+// with so many tiles of 256 on and below their diagonals.
+constexpr int64_t kTogether = 1024, kMany = 512;
+// The tile of a matrix's products, by its shorter side; 0: it is a small one.
+// 256 wide ones do up to 1.7 times the work of 128 wide ones in the same time, which need
+// more of LDS than of the matrix cores; these are more, and each shorter.  One owner's 9
+// matrices of 1024 x 1024 to 4096: 880 us with 128, 1075 with 256.
+int tile_for(int64_t m, bool many) {
+    return m <= kSmall ? 0 : 4 * up(m, 256) > 5 * up(m, 128) || (m <= kTogether && !many) ? 128 : 256;
+}
 // Whether two steps go together: with Q = a + B, the second step's A is Q A Q and what
-// both do to X is Q' Q, products of m x m that replace two of m x n and m x n x m.
-bool pairs_for(int64_t m, int64_t n) { return 2 * n >= 3 * m; }
+// both do to X is Q' Q, 5 products of m x m (half computed) in the place of 2 and of one
+// of m x n by its transpose and one of m x m by m x n: fewer operations where n > m.  Of
+// the smaller matrices all go together, since their time is that of the launches.
+bool pairs_for(int64_t m, int64_t n) { return m <= kTogether || 2 * n >= 3 * m; }
 // Tiles below the diagonal of a group of matrices, and bytes of its planes, after
 // which the next matrix begins another group.
 constexpr int64_t kGroupTiles = 1024, kGroupBytes = int64_t(4) << 30;
@@ -939,8 +1261,9 @@ struct Build {
             t.x[0] = at, at = up(at + 2 * t.plane_x, 256);
             t.x[1] = at, at = up(at + 2 * t.plane_x, 256);
             for (int k = 0; k < (pairs ? 3 : 2); ++k) {
-                t.p[k] = at, at = up(at + planes * t.plane_a, 256);
-                t.r[k] = at, at = up(at + 4 * t.mp, 256);
+                // pairs: A has its lower part, in its own terms
+                t.p[k] = at, at = up(at + (pairs && k == 0 ? 2 : planes) * t.plane_a, 256);
+                t.r[k] = at, at = up(at + 8 * t.mp, 256);
             }
             const int64_t u = up(t.mp, kUnitM) / kUnitM * (up(t.np, kUnitN) / kUnitN);
             if (u > INT32_MAX) return false;
@@ -992,6 +1315,30 @@ struct Build {
         groups.push_back(g);
         return true;
     }
+    // Matrices with a shorter side of at most kSmall, all at once.
+    bool add_small(const std::vector<Mat>& in) {
+        Group g;
+        memset(&g, 0, sizeof g);
+        g.mat0 = (int64_t)mats.size(), g.n_mats = (int64_t)in.size();
+        g.unit0 = (int64_t)items.size();
+        int64_t at = 0;
+        for (Mat t : in) {
+            const int64_t chunks = (t.n + kSmallCols - 1) / kSmallCols;
+            const int64_t per = (chunks + kSmallParts - 1) / kSmallParts;     // of a block
+            const int64_t side = (t.m + 3) / 4;
+            t.np = (int32_t)(per * kSmallCols);
+            t.n_parts = (int32_t)((chunks + per - 1) / per);
+            t.p[0] = at, at = up(at + t.n_parts * side * side * 128, 256);
+            t.p[1] = at, at = up(at + side * 4 * kSmall * 4, 256);
+            t.r[0] = at, at = up(at + 4, 256);
+            for (int64_t k = 0; k < t.n_parts; ++k) item((int64_t)mats.size(), k, 0);
+            mats.push_back(t);
+        }
+        g.n_units = (int64_t)items.size() - g.unit0;
+        ws = std::max(ws, at);
+        groups.push_back(g);
+        return g.n_units <= kMaxLaunchBlocks;
+    }
     void item(int64_t mat, int64_t i, int64_t j) {
         items.push_back(Item{(uint32_t)mat, (uint16_t)i, (uint16_t)j});
     }
@@ -1000,13 +1347,23 @@ struct Build {
             t.tall = t.rows > t.cols;
             t.m = std::min(t.rows, t.cols), t.n = std::max(t.rows, t.cols);
         }
+        int64_t tiles = 0;
+        for (const Mat& t : in) {
+            const int64_t q = up(t.m, 256) / 256;
+            if (t.m > kSmall && t.m <= kTogether) tiles += q * (q + 1) / 2;
+        }
+        const bool many = tiles >= kMany;
+        std::vector<Mat> few;
+        for (const Mat& t : in)
+            if (t.m > 0 && tile_for(t.m, many) == 0) few.push_back(t);
+        if (!few.empty() && !add_small(few)) return ZERO_ERANGE;
         for (const int kind : {0, 1, 2, 3}) {
             const int tile = kind < 2 ? 128 : 256;
             const bool pairs = kind & 1;
             std::vector<Mat> v;
             int64_t tiles = 0, bytes = 0;
             for (Mat& t : in) {
-                if (t.m == 0 || tile_for(t.m) != tile || (!precise && pairs_for(t.m, t.n)) != pairs) continue;
+                if (t.m == 0 || tile_for(t.m, many) != tile || (!precise && pairs_for(t.m, t.n)) != pairs) continue;
                 t.mp = (int32_t)up(t.m, tile), t.np = (int32_t)up(t.n, tile);
                 const int64_t q = t.mp / tile;
                 v.push_back(t);
@@ -1190,7 +1547,7 @@ struct NsConsts {
 // first with its second-order error added.
 bool ns_bounds(const zero_newton_schulz& ns, double* most_b, double* most_t) {
     const double a = ns.a, b = ns.b, c = ns.c;
-    double r = 1.0, top_b = 0.0, top_t = 0.0;
+    double r = 1.0, top_b = 0.0, top_t = 0.0, grow = 1.0;
     for (int k = 0; k < ns.steps; ++k) {
         const int n = 4096;
         double top = 0.0;
@@ -1201,13 +1558,19 @@ bool ns_bounds(const zero_newton_schulz& ns, double* most_b, double* most_t) {
             top_t = std::max(top_t, fabs((a + b * ll + c * ll * ll) * (a + e) - a * a));
             top = std::max(top, fabs(y));
         }
+        double slope = 0.0;
+        for (int q = 0; q <= n; ++q) {
+            const double l = (r * q / n) * (r * q / n);
+            slope = std::max(slope, fabs(a + 3 * b * l + 5 * c * l * l));
+        }
+        grow *= slope;
         const double h = r / n;
         top += h * h / 8 * (6 * fabs(b) * r + 20 * fabs(c) * r * r * r);
         if (!(top <= kMostSigma)) return false;
         r = std::max(top, 1e-3);
     }
     *most_b = top_b, *most_t = top_t;
-    return true;
+    return grow <= kMostGrowth;
 }
 
 // The power of two that takes values up to `most` to at most 2^15, with a tenth to spare.
@@ -1220,7 +1583,7 @@ bool scale_for(double most, double* scale) {
 }
 
 int ns_consts(const zero_newton_schulz* ns, NsConsts* out) {
-    if (!ns || ns->steps < 1 || ns->steps > 64) return ZERO_EINVAL;
+    if (!ns || ns->steps < 1 || ns->steps > 32) return ZERO_EINVAL;
     if (!isfinite(ns->a) || !isfinite(ns->b) || !isfinite(ns->c) || !isfinite(ns->eps) ||
         !(ns->eps >= 1e-30f))
         return ZERO_EINVAL;
@@ -1248,25 +1611,25 @@ int run_steps(const Step& s, const Group& g, const Item* items, const NsConsts& 
               const MuonBufs& mb, const MuonConsts& mc, hipStream_t stream) {
     const double a = ns.a, b = ns.b, c = ns.c, sx = kScaleX, sa = kScaleA, sb = ns.scale_b, st = ns.scale_t;
     int from = 0;
-    auto square = [&](int p, int q, int out, double fp, double fq, double fc) {
-        const Product d = {from, p, q, out, (float)fp, (float)fq, (float)fc, {}};
+    auto square = [&](int p, int q, int out, int lower, double fp, double fq, double fc) {
+        const Product d = {from, p, q, out, lower, (float)fp, (float)fq, (float)fc, {}};
         return run_product<T, kSquare, 0, P>(s, items + g.tri0, g.n_tri, g.square, d, mb, mc, stream);
     };
     for (int k = 0; k < steps;) {
         const bool two = g.pairs && k + 2 <= steps;
-        const Product gram = {from, 0, 0, 0, 0.0f, 0.0f, (float)(sa / (sx * sx)), {}};
+        const Product gram = {from, 0, 0, 0, two, 0.0f, 0.0f, (float)(sa / (sx * sx)), {}};
         int rc = run_product<T, kGram, 0, P>(s, items + g.tri0, g.n_tri, g.gram, gram, mb, mc, stream);
         // plane 0: A; plane 1: B = b A + c A A
-        if (rc == ZERO_OK) rc = square(0, 0, 1, b * sb / sa, 0.0, c * sb / (sa * sa));
-        Product last = {from, 1, 0, 0, (float)a, 0.0f, (float)(1.0 / sb), {}};
+        if (rc == ZERO_OK) rc = square(0, 0, 1, two, b * sb / sa, 0.0, c * sb / (sa * sa));
+        Product last = {from, 1, 0, 0, 0, (float)a, 0.0f, (float)(1.0 / sb), {}};
         if (two) {
             // plane 2: Y = A Q = a A + A B;  plane 0: A' = Y Q = a Y + Y B
-            if (rc == ZERO_OK) rc = square(0, 1, 2, a, 0.0, 1.0 / sb);
-            if (rc == ZERO_OK) rc = square(2, 1, 0, a, 0.0, 1.0 / sb);
+            if (rc == ZERO_OK) rc = square(0, 1, 2, 1, a, 0.0, 1.0 / sb);
+            if (rc == ZERO_OK) rc = square(2, 1, 0, 0, a, 0.0, 1.0 / sb);
             // plane 2: B' = b A' + c A' A';  plane 0: T = Q' Q - a^2 = a B + a B' + B B'
-            if (rc == ZERO_OK) rc = square(0, 0, 2, b * sb / sa, 0.0, c * sb / (sa * sa));
-            if (rc == ZERO_OK) rc = square(1, 2, 0, a * st / sb, a * st / sb, st / (sb * sb));
-            last = {from, 0, 0, 0, (float)(a * a), 0.0f, (float)(1.0 / st), {}};
+            if (rc == ZERO_OK) rc = square(0, 0, 2, 0, b * sb / sa, 0.0, c * sb / (sa * sa));
+            if (rc == ZERO_OK) rc = square(1, 2, 0, 0, a * st / sb, a * st / sb, st / (sb * sb));
+            last = {from, 0, 0, 0, 0, (float)(a * a), 0.0f, (float)(1.0 / st), {}};
         }
         k += two ? 2 : 1;
         if (rc == ZERO_OK)
@@ -1302,6 +1665,18 @@ int run_groups(const char* host, const char* table, const NsConsts& ns, int step
         s.items = items + g.unit0, s.n_items = g.n_units;
         s.ws = ws, s.res = res;
         s.inv_off = g.inv_off, s.part_off = g.part_off, s.sums_off = g.sums_off;
+        if (g.tile == 0) {
+            const SmallNs small = {ns.a, ns.b, ns.c, ns.eps, steps, 0};
+            Step one = s;
+            one.mats = s.mats + g.mat0;
+            int rc = launch(small_gram_kernel<Source>, g.n_units, 0, stream, s, src);
+            if (rc == ZERO_OK) rc = launch(small_steps_kernel, g.n_mats, 0, stream, one, small);
+            if (rc == ZERO_OK)
+                rc = muon ? launch(small_apply_kernel<true, DT, Source>, g.n_units, 0, stream, s, src, mb, mc)
+                          : launch(small_apply_kernel<false, DT, Source>, g.n_units, 0, stream, s, src, mb, mc);
+            if (rc != ZERO_OK) return rc;
+            continue;
+        }
         int rc = launch(matrix_norm_kernel<Source>, g.n_units, 0, stream, s, src);
         if (rc != ZERO_OK) return rc;
         Step f = s;
