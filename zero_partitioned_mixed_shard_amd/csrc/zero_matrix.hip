@@ -481,21 +481,6 @@ __device__ __forceinline__ void store_plane(f16* p, int64_t plane, const float* 
         if (plane != 0) *(f16x8*)(p + plane + 8 * k) = l;
     }
 }
-// Those of the 16 from `from` up to `to` (any numbers).
-__device__ __forceinline__ void store_some(f16* p, int64_t plane, const float* v, int64_t to, int64_t from) {
-    if (from <= 0 && to >= 16) {
-        store_plane(p, plane, v);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            if (e < from || e >= to) continue;
-            f16 hi, lo;
-            split(v[e], hi, lo);
-            p[e] = hi;
-            if (plane != 0) p[plane + e] = lo;
-        }
-    }
-}
 // 16 consecutive elements of a buffer, which may begin at any element.
 __device__ __forceinline__ void load_f32(const float* p, float* v) {
 #pragma unroll
@@ -725,14 +710,23 @@ struct Finish {
                 turn_over(mine, at, v, lane);
                 store_plane(out + turned * t.mp + top, lower, v);
             } else {
-                store_some(out + row * t.mp + col, lower, v, row - col + 1, 0);
-                turn_over(mine, at, v, lane);
-                store_some(out + turned * t.mp + top, lower, v, 16, turned - top + 1);
+                float turned_v[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) turned_v[e] = v[e];
+                turn_over(mine, at, turned_v, lane);
+                // the 16 x 16 on the diagonal: above it, the element across
+                const int r = lane >> 2;
+                const float* across = (const float*)mine + ((lane & 3) << 4) + r;
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (col == top && e > r) v[e] = across[e * kTurn];
+                if (col <= top) store_plane(out + row * t.mp + col, lower, v);
+                if ((turned & ~int64_t(15)) < top) store_plane(out + turned * t.mp + top, lower, turned_v);
                 if constexpr (!PRECISE) {
-                    // back to the lane's row: its element on the diagonal
-                    const int64_t own = row - col;
-                    const float u = own >= 0 && own < 16 ? at[own] : 0.0f;
-                    if (own >= 0 && own < 16) {
+                    float u = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) u = e == r ? v[e] : u;
+                    if (col == top) {
                         t.lost_out[row] = u - (float)(f16)u;
                         t.lost_out[t.mp + row] = u;
                     }
