@@ -26,6 +26,10 @@ constexpr int kSlab = 64 * kCols;          // columns of a wave
 constexpr int kSortLanes = 1024, kSortWaves = kSortLanes / 64;
 constexpr int kSmallSort = 8192;           // tokens that one block sorts in LDS
 constexpr int kSortTile = 4096;            // tokens of a block of the larger sort
+// Tokens of a chunk, and (chunk, 512 columns) units that are enough for the device.
+constexpr int64_t kLeastChunk = 8, kMostChunk = 512, kChunkUnits = 8192;
+// Blocks whose counts each block of the larger sort adds up by itself; more take a launch.
+constexpr int64_t kFewBlocks = 64;
 constexpr int kDigit = 9, kBins = 1 << kDigit;   // most bits of a pass
 
 template <int DT>
@@ -106,39 +110,55 @@ __device__ __forceinline__ int64_t id_at(const void* ids, int wide, int64_t t) {
 }
 
 // ------------------------------------------------------------ lookup -------
-// A wave takes 512 columns of a token.
+// A wave takes 1024 columns of a token, 16 of each lane in two runs of 8: with 512 (half as
+// many bytes on their way, and twice the units to be told apart) 16384 tokens of 4096
+// bf16 into fp32 took 94 us, so LOOKUP_US.
+constexpr int kLookupRuns = 2, kLookupCols = kSlab * kLookupRuns;
+
 template <int SRC, int DST>
 __global__ void __launch_bounds__(kThreads)
 embedding_lookup_kernel(void* __restrict__ out, int64_t out_ld, const void* __restrict__ ids, int wide,
-                        int64_t units, int64_t slabs, const void* __restrict__ table, Slice s, float scale,
+                        int64_t n_tokens, uint32_t parts, const void* __restrict__ table, Slice s, float scale,
                         int64_t blk0) {
-    const int64_t u = (blk0 + blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6);
-    if (u >= units) return;
-    const int64_t token = u / slabs;
-    const int64_t col = (u - token * slabs) * kSlab + (threadIdx.x & 63) * kCols;
-    if (col >= s.dim) return;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t u = (blk0 + blockIdx.x) * (kThreads / 64) + w;
+    const int64_t token = u >> 32 ? u / parts : (int64_t)((uint32_t)u / parts);
+    if (token >= n_tokens) return;
     const int64_t id = id_at(ids, wide, token);
-    const int n = (int)(s.dim - col < kCols ? s.dim - col : kCols);
     const bool known = id >= 0 && id < s.vocab;
-    const int64_t at = known ? id * s.dim + col - s.begin : -kCols, to = token * out_ld + col;
-    float v[kCols];
-    if (at >= 0 && at + kCols <= s.count && n == kCols) {
-        const Raw8<SRC> r = load8<SRC, false>(table, at);
+    const int64_t first = (u - token * parts) * kLookupCols + (threadIdx.x & 63) * kCols;
+    const int64_t row = known ? id * s.dim - s.begin : 0;
+    Raw8<SRC> r[kLookupRuns];
+    bool whole[kLookupRuns];
 #pragma unroll
-        for (int k = 0; k < kCols; ++k) v[k] = scale * r.get(k);
-    } else {
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) {
-            const int64_t e = at + k;
-            v[k] = known && k < n && e >= 0 && e < s.count ? scale * load1<SRC>(table, e) : 0.0f;
-        }
+    for (int q = 0; q < kLookupRuns; ++q) {
+        const int64_t col = first + q * kSlab, at = row + col;
+        whole[q] = known && col + kCols <= s.dim && at >= 0 && at + kCols <= s.count;
+        if (whole[q]) r[q] = load8<SRC, false>(table, at);
     }
-    if (n == kCols) {
-        store8<DST, true>(out, to, v);
-    } else {
 #pragma unroll
-        for (int k = 0; k < kCols; ++k)
-            if (k < n) store1<DST>(out, to + k, v[k]);
+    for (int q = 0; q < kLookupRuns; ++q) {
+        const int64_t col = first + q * kSlab, at = row + col, to = token * out_ld + col;
+        if (col >= s.dim) continue;
+        const int n = (int)(s.dim - col < kCols ? s.dim - col : kCols);
+        float v[kCols];
+        if (whole[q]) {
+#pragma unroll
+            for (int k = 0; k < kCols; ++k) v[k] = scale * r[q].get(k);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kCols; ++k) {
+                const int64_t e = at + k;
+                v[k] = known && k < n && e >= 0 && e < s.count ? scale * load1<SRC>(table, e) : 0.0f;
+            }
+        }
+        if (n == kCols) {
+            store8<DST, true>(out, to, v);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kCols; ++k)
+                if (k < n) store1<DST>(out, to + k, v[k]);
+        }
     }
 }
 
@@ -212,7 +232,7 @@ __device__ __forceinline__ void bin_starts(uint32_t (*count)[kBins], const uint3
 // Up to kSmallSort tokens by one block in LDS.
 __global__ void __launch_bounds__(kSortLanes)
 embedding_sort_small_kernel(Keys keys, int passes, int bits, uint32_t* __restrict__ out_key,
-                            uint32_t* __restrict__ out_pos) {
+                            uint32_t* __restrict__ out_pos, uint32_t* __restrict__ n_valid) {
     __shared__ uint32_t count[kSortWaves][kBins];
     __shared__ uint32_t sums[kSortWaves];
     __shared__ uint32_t lk[kSmallSort], lp[kSmallSort];
@@ -264,6 +284,9 @@ embedding_sort_small_kernel(Keys keys, int passes, int bits, uint32_t* __restric
         if (r < rounds && t < n) {
             out_key[t] = k[r];
             out_pos[t] = p[r];
+            // the first of no row, or the end
+            if (k[r] == (uint32_t)keys.s.vocab && (t == 0 || lk[t - 1] != k[r])) *n_valid = (uint32_t)t;
+            if (t + 1 == n && k[r] != (uint32_t)keys.s.vocab) *n_valid = (uint32_t)n;
         }
     }
 }
@@ -327,14 +350,38 @@ embedding_scan_kernel(uint32_t* __restrict__ counts, int64_t n) {
 }
 __global__ void __launch_bounds__(kSortLanes)
 embedding_scatter_kernel(Keys keys, Pairs in, int shift, int bits, int64_t blocks,
-                         const uint32_t* __restrict__ counts, uint32_t* __restrict__ out_key,
+                         const uint32_t* __restrict__ counts, int scanned, uint32_t* __restrict__ out_key,
                          uint32_t* __restrict__ out_pos) {
     __shared__ uint32_t count[kSortWaves][kBins];
-    __shared__ uint32_t start[kBins];
+    __shared__ uint32_t start[kBins], sums[kSortWaves];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     for (int b = lane; b < kBins; b += 64) count[w][b] = 0;
-    if (threadIdx.x < kBins)
+    if (!scanned) {
+        // the counts as they are: those of the bins before, and of the blocks before in the bin
+        const uint32_t* c = counts + (int64_t)threadIdx.x * blocks;
+        uint32_t all = 0, before = 0;
+        if (threadIdx.x < (1u << bits)) {
+#pragma unroll 8
+            for (int b = 0; b < (int)blocks; ++b) {
+                const uint32_t v = c[b];
+                all += v;
+                before += b < (int)blockIdx.x ? v : 0;
+            }
+        }
+        uint32_t v = all;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const uint32_t o = (uint32_t)__shfl_up((int)v, off, 64);
+            if (lane >= off) v += o;
+        }
+        if (lane == 63) sums[w] = v;
+        __syncthreads();
+        uint32_t base = v - all;
+        for (int k = 0; k < w; ++k) base += sums[k];
+        if (threadIdx.x < kBins) start[threadIdx.x] = base + before;
+    } else if (threadIdx.x < kBins) {
         start[threadIdx.x] = threadIdx.x < (1u << bits) ? counts[(int64_t)threadIdx.x * blocks + blockIdx.x] : 0;
+    }
     __syncthreads();
     constexpr int kRounds = kSortTile / kSortLanes;
     const int64_t t0 = (int64_t)blockIdx.x * kSortTile + w * kRounds * 64 + lane;
@@ -360,12 +407,39 @@ embedding_scatter_kernel(Keys keys, Pairs in, int shift, int bits, int64_t block
     }
 }
 
+// How many of the sorted tokens have a row: one wave.
+__global__ void __launch_bounds__(64)
+embedding_valid_kernel(const uint32_t* __restrict__ key, int64_t n, uint32_t none, uint32_t* __restrict__ n_valid) {
+    // 64 tokens are looked at in a round
+    int64_t lo = 0, hi = n;
+    while (lo < hi) {
+        const int64_t step = (hi - lo + 63) / 64, at = lo + (int64_t)threadIdx.x * step;
+        const uint64_t below = __ballot(at < hi && key[at] < none);
+        const int c = __popcll(below);              // the first c are below
+        if (c == 0) {
+            hi = lo;
+        } else {
+            const int64_t next = lo + (int64_t)c * step;
+            lo += (int64_t)(c - 1) * step + 1;
+            hi = next < hi ? next : hi;
+        }
+    }
+    if (threadIdx.x == 0) *n_valid = (uint32_t)lo;
+}
+
 // ------------------------------------------------------------ sums ---------
 struct Sorted {
-    const uint32_t *key, *pos;
-    int64_t n, chunk;          // tokens, and of a chunk
-    int64_t slabs;
+    const uint32_t *key, *pos, *n_valid;
+    int64_t most;              // chunks there is room for
+    uint32_t slabs;
     float* part;               // [chunk][0: of an id that began before; 1: that goes on][dim]
+    int64_t n, chunk;          // tokens with a row, and of a chunk
+    // Chunks go by the tokens that have a row: an owner of a few rows has few.
+    __device__ __forceinline__ void begin() {
+        n = n_valid ? (int64_t)*n_valid : 0;
+        chunk = kLeastChunk;
+        while ((n + chunk - 1) / chunk > most) chunk *= 2;
+    }
 };
 
 // Adds scale * v to row `id`, columns col .. of the slice (or stores it).
@@ -396,9 +470,24 @@ __device__ __forceinline__ void emit(void* grad, const Slice& s, int64_t id, int
     }
 }
 __device__ __forceinline__ void store_part(float* part, int64_t dim, int64_t col, const float* v) {
+    if (col + kCols <= dim) {
+        store8<ZERO_FP32, false>(part, col, v);
+    } else {
 #pragma unroll
-    for (int k = 0; k < kCols; ++k)
-        if (col + k < dim) part[col + k] = v[k];
+        for (int k = 0; k < kCols; ++k)
+            if (col + k < dim) part[col + k] = v[k];
+    }
+}
+__device__ __forceinline__ void add_part(const float* part, int64_t dim, int64_t col, float* v) {
+    if (col + kCols <= dim) {
+        const Raw8<ZERO_FP32> r = load8<ZERO_FP32, false>(part, col);
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) v[k] += r.get(k);
+    } else {
+#pragma unroll
+        for (int k = 0; k < kCols; ++k)
+            if (col + k < dim) v[k] += part[col + k];
+    }
 }
 
 // Rows of the slice that no token has become zero: the first blocks of the launch, a
@@ -428,79 +517,93 @@ __device__ __forceinline__ void clear_rows(const Sorted& q, void* grad, const Sl
     }
 }
 
+// A wave: a chunk's rows of dy for 512 columns, kRowsAhead at a time, with the old values of
+// the rows that end among them.
+constexpr int kRowsAhead = 4;
+
 template <int SRC, int DST>
 __global__ void __launch_bounds__(kThreads)
 embedding_sum_kernel(Sorted q, const void* __restrict__ dy, int64_t dy_ld, void* __restrict__ grad, Slice s,
-                     float scale, int overwrite, int64_t clear_blocks, int clear_rows_, int64_t blk0) {
+                     float scale, int overwrite, int64_t clear_blocks, int rows, int64_t blk0) {
     const int64_t blk = blk0 + blockIdx.x;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    q.begin();
     if (blk < clear_blocks) {
-        clear_rows<DST>(q, grad, s, blk * (kThreads / 64) + w, clear_rows_);
+        clear_rows<DST>(q, grad, s, blk * (kThreads / 64) + w, rows);
         return;
     }
     const int64_t u = (blk - clear_blocks) * (kThreads / 64) + w;
-    const int64_t c = u / q.slabs;
+    const int64_t c = u >> 32 ? u / q.slabs : (int64_t)((uint32_t)u / q.slabs);
     const int64_t a = c * q.chunk, b = a + q.chunk < q.n ? a + q.chunk : q.n;
     if (a >= b) return;
-    const uint32_t none = (uint32_t)s.vocab;
     const int64_t col = (u - c * q.slabs) * kSlab + (threadIdx.x & 63) * kCols;
     const bool active = col < s.dim, whole = col + kCols <= s.dim;
     float* part = q.part + 2 * c * s.dim;
+    const uint32_t before = a > 0 ? q.key[a - 1] : ~0u, after = b < q.n ? q.key[b] : ~0u;
     uint32_t id = q.key[a];
-    if (id == none) return;
-    bool began = a > 0 && q.key[a - 1] == id;      // in an earlier chunk
+    bool began = before == id;                     // in an earlier chunk
     float sum[kCols] = {0, 0, 0, 0, 0, 0, 0, 0};
-    constexpr int U = 4;
+    constexpr int U = kRowsAhead;
     for (int64_t i = a; i < b; i += U) {
         Raw8<SRC> r[U];
-        uint32_t key[U];
+        Raw8<DST> old[U];
+        uint32_t key[U + 1];
+        bool has[U];
+#pragma unroll
+        for (int k = 0; k <= U; ++k) key[k] = i + k < b ? q.key[i + k] : after;
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            key[k] = i + k < b ? q.key[i + k] : none;
-            if (key[k] != none && active) {
-                const int64_t row = (int64_t)q.pos[i + k] * dy_ld + col;
-                if (whole) {
-                    r[k] = load8<SRC, true>(dy, row);
+            has[k] = false;
+            if (i + k >= b || !active) continue;
+            const int64_t row = (int64_t)q.pos[i + k] * dy_ld + col;
+            if (whole) {
+                r[k] = load8<SRC, true>(dy, row);
+            } else {
+                float v[kCols];
+#pragma unroll
+                for (int e = 0; e < kCols; ++e) v[e] = col + e < s.dim ? load1<SRC>(dy, row + e) : 0.0f;
+                if constexpr (SRC == ZERO_FP32) {
+#pragma unroll
+                    for (int e = 0; e < kCols; ++e) r[k].q[e >> 2][e & 3] = __float_as_uint(v[e]);
                 } else {
-                    float v[kCols];
+                    uint16_t h[8];
 #pragma unroll
-                    for (int e = 0; e < kCols; ++e) v[e] = col + e < s.dim ? load1<SRC>(dy, row + e) : 0.0f;
-                    if constexpr (SRC == ZERO_FP32) {
-#pragma unroll
-                        for (int e = 0; e < kCols; ++e) r[k].q[e >> 2][e & 3] = __float_as_uint(v[e]);
-                    } else {
-                        uint16_t h[8];
-#pragma unroll
-                        for (int e = 0; e < kCols; ++e) h[e] = narrow<SRC>(v[e]);
-                        r[k].q[0] = pack8(h);
-                    }
+                    for (int e = 0; e < kCols; ++e) h[e] = narrow<SRC>(v[e]);
+                    r[k].q[0] = pack8(h);
                 }
             }
+            const int64_t at = (int64_t)key[k] * s.dim + col - s.begin;
+            has[k] = !overwrite && key[k + 1] != key[k] && whole && at >= 0 && at + kCols <= s.count;
+            if (has[k]) old[k] = load8<DST, false>(grad, at);
         }
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             if (i + k >= b) break;
-            if (key[k] != id) {
-                if (active) {
-                    if (began) store_part(part, s.dim, col, sum);
-                    else emit<DST>(grad, s, id, col, sum, scale, overwrite);
-                }
-                began = false;
-                id = key[k];
-                if (id == none) return;
-#pragma unroll
-                for (int e = 0; e < kCols; ++e) sum[e] = 0.0f;
-            }
             if (active) {
 #pragma unroll
                 for (int e = 0; e < kCols; ++e) sum[e] += r[k].get(e);
             }
+            if (key[k + 1] == key[k] && i + k + 1 < b) continue;
+            // the id's last token, or the chunk's
+            if (active) {
+                if (began) {
+                    store_part(part, s.dim, col, sum);
+                } else if (key[k + 1] == key[k]) {
+                    store_part(part + s.dim, s.dim, col, sum);
+                } else if (has[k]) {
+                    float y[kCols];
+#pragma unroll
+                    for (int e = 0; e < kCols; ++e) y[e] = fmaf(scale, sum[e], old[k].get(e));
+                    store8<DST, false>(grad, (int64_t)key[k] * s.dim + col - s.begin, y);
+                } else {
+                    emit<DST>(grad, s, key[k], col, sum, scale, overwrite);
+                }
+            }
+            began = false;
+#pragma unroll
+            for (int e = 0; e < kCols; ++e) sum[e] = 0.0f;
         }
     }
-    if (!active) return;
-    if (began) store_part(part, s.dim, col, sum);
-    else if (b < q.n && q.key[b] == id) store_part(part + s.dim, s.dim, col, sum);
-    else emit<DST>(grad, s, id, col, sum, scale, overwrite);
 }
 
 // The ids that go on past a chunk's end, at the chunk where they begin: a block adds up
@@ -509,11 +612,12 @@ template <int DST>
 __global__ void __launch_bounds__(kThreads)
 embedding_join_kernel(Sorted q, void* __restrict__ grad, Slice s, float scale, int overwrite, int64_t blk0) {
     __shared__ float quarter[kThreads / 64][kSlab];
-    const int64_t u = blk0 + blockIdx.x, c = u / q.slabs;
+    q.begin();
+    const int64_t u = blk0 + blockIdx.x, c = u >> 32 ? u / q.slabs : (int64_t)((uint32_t)u / q.slabs);
     const int64_t a = c * q.chunk, b = a + q.chunk;
     if (b >= q.n) return;
     const uint32_t id = q.key[b - 1];
-    if (id == (uint32_t)s.vocab || q.key[b] != id) return;
+    if (q.key[b] != id) return;
     // the id begins in this chunk, not before
     if (q.key[a] == id && a > 0 && q.key[a - 1] == id) return;
     int64_t lo = b, hi = q.n;                      // first token after the id's
@@ -528,25 +632,20 @@ embedding_join_kernel(Sorted q, void* __restrict__ grad, Slice s, float scale, i
     const int64_t per = (more + 3) / 4, from = w * per, to = from + per < more ? from + per : more;
     float sum[kCols] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (col < s.dim) {
-#pragma unroll 4
-        for (int64_t k = from; k < to; ++k) {
-            const float* p = q.part + 2 * (c + 1 + k) * s.dim;
-#pragma unroll
-            for (int e = 0; e < kCols; ++e) sum[e] += col + e < s.dim ? p[col + e] : 0.0f;
-        }
+#pragma unroll 8
+        for (int64_t k = from; k < to; ++k) add_part(q.part + 2 * (c + 1 + k) * s.dim, s.dim, col, sum);
     }
 #pragma unroll
     for (int e = 0; e < kCols; ++e) quarter[w][lane * kCols + e] = sum[e];
     __syncthreads();
     if (w != 0 || col >= s.dim) return;
-    const float* first = q.part + (2 * c + 1) * s.dim;
 #pragma unroll
-    for (int e = 0; e < kCols; ++e) {
-        float v = col + e < s.dim ? first[col + e] : 0.0f;
+    for (int e = 0; e < kCols; ++e) sum[e] = 0.0f;
+    add_part(q.part + (2 * c + 1) * s.dim, s.dim, col, sum);
 #pragma unroll
-        for (int k = 0; k < kThreads / 64; ++k) v += quarter[k][lane * kCols + e];
-        sum[e] = v;
-    }
+    for (int e = 0; e < kCols; ++e)
+#pragma unroll
+        for (int k = 0; k < kThreads / 64; ++k) sum[e] += quarter[k][lane * kCols + e];
     emit<DST>(grad, s, id, col, sum, scale, overwrite);
 }
 
@@ -567,7 +666,6 @@ int check_slice(int64_t vocab, int64_t dim, int64_t begin, int64_t count) {
 
 // Tokens of a chunk: enough chunks to fill the device, few enough that an id that
 // most tokens have is added up in two short passes.
-constexpr int64_t kLeastChunk = 8, kMostChunk = 512, kChunkUnits = 8192;
 int64_t chunk_for(int64_t n, int64_t slabs) {
     int64_t c = kLeastChunk;
     while (c < kMostChunk && n * slabs > c * kChunkUnits) c *= 2;
@@ -580,7 +678,7 @@ int64_t most_chunks(int64_t n, int64_t slabs) {
     return many > full ? many : few < full ? few : full;
 }
 struct Layout {
-    int64_t key[2], pos[2], counts, part, bytes;
+    int64_t key[2], pos[2], counts, n_valid, part, bytes;
     int64_t chunk, chunks, slabs, blocks;
 };
 Layout layout_for(int64_t n, int64_t dim) {
@@ -595,6 +693,7 @@ Layout layout_for(int64_t n, int64_t dim) {
         l.pos[k] = at, at = up(at + 4 * n, 256);
     }
     l.counts = at, at = up(at + 4 * kBins * l.blocks, 256);
+    l.n_valid = at, at = up(at + 4, 256);
     l.part = at, at = up(at + 8 * most_chunks(n, l.slabs) * dim, 256);
     l.bytes = at;
     return l;
@@ -638,12 +737,12 @@ int zero_embedding_lookup(void* out, int64_t out_ld, int32_t out_dtype, const vo
         misaligned(table, table_dtype))
         return ZERO_EINVAL;
     const Slice s = {vocab, dim, begin, count};
-    const int64_t slabs = (dim + kSlab - 1) / kSlab, units = n_tokens * slabs;
+    const int64_t parts = (dim + kLookupCols - 1) / kLookupCols;
     return by_type(table_dtype, [&](auto src) {
         return by_type(out_dtype, [&](auto dst) {
-            return in_pieces((units + 3) / 4, [&](int64_t b, int64_t grid) {
+            return in_pieces((n_tokens * parts + 3) / 4, [&](int64_t b, int64_t grid) {
                 return launch(embedding_lookup_kernel<decltype(src)::value, decltype(dst)::value>, grid, 0, stream,
-                              out, out_ld, ids, id_bytes == 8, units, slabs, table, s, scale, b);
+                              out, out_ld, ids, id_bytes == 8, n_tokens, (uint32_t)parts, table, s, scale, b);
             });
         });
     });
@@ -672,6 +771,7 @@ int zero_embedding_grad(void* grad, int32_t grad_dtype, const void* ids, int32_t
     if (n_tokens > 0 && (!workspace || (uintptr_t)workspace % 256 || workspace_bytes < (size_t)l.bytes))
         return ZERO_EINVAL;
     char* ws = (char*)workspace;
+    uint32_t* n_valid = n_tokens > 0 ? (uint32_t*)(ws + l.n_valid) : nullptr;
     const Slice s = {vocab, dim, begin, count};
     Keys keys = {ids, id_bytes == 8, n_tokens, padding_id < 0 ? -1 : padding_id, s};
     // passes of at most kDigit bits over the keys 0 .. vocab
@@ -682,7 +782,7 @@ int zero_embedding_grad(void* grad, int32_t grad_dtype, const void* ids, int32_t
     int rc = ZERO_OK;
     if (n_tokens > 0 && n_tokens <= kSmallSort) {
         rc = launch_shape(embedding_sort_small_kernel, 1, kSortLanes, 0, stream, keys, passes, per,
-                          (uint32_t*)(ws + l.key[0]), (uint32_t*)(ws + l.pos[0]));
+                          (uint32_t*)(ws + l.key[0]), (uint32_t*)(ws + l.pos[0]), n_valid);
     } else if (n_tokens > 0) {
         uint32_t* counts = (uint32_t*)(ws + l.counts);
         for (int p = 0; p < passes && rc == ZERO_OK; ++p) {
@@ -691,18 +791,22 @@ int zero_embedding_grad(void* grad, int32_t grad_dtype, const void* ids, int32_t
             const int to = p == 0 ? 0 : at ^ 1;
             rc = launch_shape(embedding_count_kernel, l.blocks, kSortLanes, 0, stream, keys, in, p * per, per,
                               l.blocks, counts);
-            if (rc == ZERO_OK)
+            const bool scan = l.blocks > kFewBlocks;
+            if (rc == ZERO_OK && scan)
                 rc = launch_shape(embedding_scan_kernel, 1, kSortLanes, 0, stream, counts, l.blocks << per);
             if (rc == ZERO_OK)
                 rc = launch_shape(embedding_scatter_kernel, l.blocks, kSortLanes, 0, stream, keys, in, p * per, per,
-                                  l.blocks, (const uint32_t*)counts, (uint32_t*)(ws + l.key[to]),
+                                  l.blocks, (const uint32_t*)counts, (int)scan, (uint32_t*)(ws + l.key[to]),
                                   (uint32_t*)(ws + l.pos[to]));
             at = to;
         }
+        if (rc == ZERO_OK)
+            rc = launch_shape(embedding_valid_kernel, 1, 64, 0, stream, (const uint32_t*)(ws + l.key[at]), n_tokens,
+                              (uint32_t)vocab, n_valid);
     }
     if (rc != ZERO_OK) return rc;
-    const Sorted q = {(const uint32_t*)(ws + l.key[at]), (const uint32_t*)(ws + l.pos[at]), n_tokens, l.chunk,
-                      l.slabs, (float*)(ws + l.part)};
+    const Sorted q = {(const uint32_t*)(ws + l.key[at]), (const uint32_t*)(ws + l.pos[at]), n_valid, l.chunks,
+                      (uint32_t)l.slabs, (float*)(ws + l.part), 0, 0};
     const int64_t size = grad_dtype == ZERO_FP32 ? 4 : 2;
     int rows = 64;                                   // of a wave that clears, about 64 KiB
     while (rows > 1 && rows * dim * size > 65536) rows /= 2;
