@@ -25,9 +25,12 @@ constexpr int kCols = 8;                   // columns of a lane
 constexpr int kSlab = 64 * kCols;          // columns of a wave
 constexpr int kSortLanes = 1024, kSortWaves = kSortLanes / 64;
 constexpr int kSmallSort = 8192;           // tokens that one block sorts in LDS
-constexpr int kSortTile = 4096;            // tokens of a block of the larger sort
+constexpr int kBigLanes = 512, kBigWaves = kBigLanes / 64;
+constexpr int kSortTile = 2048;            // tokens of a block of the larger sort
 // Tokens of a chunk, and (chunk, 512 columns) units that are enough for the device.
-constexpr int64_t kLeastChunk = 8, kMostChunk = 512, kChunkUnits = 8192;
+constexpr int64_t kLeastChunk = 8, kMostChunk = 512, kChunkUnits = 4096;
+// Bytes that a wave clears, about.
+constexpr int64_t kClearBytes = 32768;
 // Blocks whose counts each block of the larger sort adds up by itself; more take a launch.
 constexpr int64_t kFewBlocks = 64;
 constexpr int kDigit = 9, kBins = 1 << kDigit;   // most bits of a pass
@@ -110,9 +113,12 @@ __device__ __forceinline__ int64_t id_at(const void* ids, int wide, int64_t t) {
 }
 
 // ------------------------------------------------------------ lookup -------
-// A wave takes 1024 columns of a token, 16 of each lane in two runs of 8: with 512 (half as
-// many bytes on their way, and twice the units to be told apart) 16384 tokens of 4096
-// bf16 into fp32 took 94 us, so LOOKUP_US.
+// A wave takes 1024 columns of a token, 16 of each lane in two runs of 8.  16384 tokens of
+// 4096 bf16 into fp32 took 68 us (512 columns the same, 2048 79), 4.6 TB/s; stored
+// non-temporally 106, since a lane's 32 bytes go in two stores that each fill half of
+// every line.  16-bit results, whose stores fill lines, gain 10-15 % by it.
+template <int DT>
+constexpr bool kNtOut = DT != ZERO_FP32;
 constexpr int kLookupRuns = 2, kLookupCols = kSlab * kLookupRuns;
 
 template <int SRC, int DST>
@@ -153,7 +159,7 @@ embedding_lookup_kernel(void* __restrict__ out, int64_t out_ld, const void* __re
             }
         }
         if (n == kCols) {
-            store8<DST, true>(out, to, v);
+            store8<DST, kNtOut<DST>>(out, to, v);
         } else {
 #pragma unroll
             for (int k = 0; k < kCols; ++k)
@@ -198,11 +204,12 @@ __device__ __forceinline__ int wave_rank(uint32_t digit, bool valid, int bits, u
 
 // count[wave][bin] into the number of keys before the wave's first of that bin; add[bin]
 // (or the bins' own sums) is where a bin begins.  Lanes 0 to 511 take a bin each.
+template <int WAVES>
 __device__ __forceinline__ void bin_starts(uint32_t (*count)[kBins], const uint32_t* start, uint32_t* sums) {
     const int t = threadIdx.x;
     uint32_t total = 0;
     if (t < kBins)
-        for (int w = 0; w < kSortWaves; ++w) {
+        for (int w = 0; w < WAVES; ++w) {
             const uint32_t c = count[w][t];
             count[w][t] = total;
             total += c;
@@ -225,7 +232,7 @@ __device__ __forceinline__ void bin_starts(uint32_t (*count)[kBins], const uint3
         base = start[t];
     }
     if (t < kBins)
-        for (int w = 0; w < kSortWaves; ++w) count[w][t] += base;
+        for (int w = 0; w < WAVES; ++w) count[w][t] += base;
     __syncthreads();
 }
 
@@ -257,7 +264,7 @@ embedding_sort_small_kernel(Keys keys, int passes, int bits, uint32_t* __restric
             rank[r] = wave_rank((k[r] >> (pass * bits)) & ((1u << bits) - 1), valid, bits, count[w], lane);
         }
         __syncthreads();
-        bin_starts(count, nullptr, sums);
+        bin_starts<kSortWaves>(count, nullptr, sums);
 #pragma unroll
         for (int r = 0; r < kRounds; ++r) {
             if (r >= rounds) break;
@@ -298,15 +305,15 @@ struct Pairs {
 __device__ __forceinline__ uint32_t key_of(const Keys& keys, const Pairs& in, int64_t t) {
     return in.key ? in.key[t] : keys.get(t);
 }
-__global__ void __launch_bounds__(kSortLanes)
+__global__ void __launch_bounds__(kBigLanes)
 embedding_count_kernel(Keys keys, Pairs in, int shift, int bits, int64_t blocks, uint32_t* __restrict__ counts) {
     __shared__ uint32_t bin[kBins];
     if (threadIdx.x < kBins) bin[threadIdx.x] = 0;
     __syncthreads();
     const int64_t t0 = (int64_t)blockIdx.x * kSortTile;
 #pragma unroll
-    for (int r = 0; r < kSortTile / kSortLanes; ++r) {
-        const int64_t t = t0 + r * kSortLanes + threadIdx.x;
+    for (int r = 0; r < kSortTile / kBigLanes; ++r) {
+        const int64_t t = t0 + r * kBigLanes + threadIdx.x;
         if (t < keys.n) atomicAdd(&bin[(key_of(keys, in, t) >> shift) & ((1u << bits) - 1)], 1u);
     }
     __syncthreads();
@@ -348,12 +355,12 @@ embedding_scan_kernel(uint32_t* __restrict__ counts, int64_t n) {
         __syncthreads();
     }
 }
-__global__ void __launch_bounds__(kSortLanes)
+__global__ void __launch_bounds__(kBigLanes)
 embedding_scatter_kernel(Keys keys, Pairs in, int shift, int bits, int64_t blocks,
                          const uint32_t* __restrict__ counts, int scanned, uint32_t* __restrict__ out_key,
                          uint32_t* __restrict__ out_pos) {
-    __shared__ uint32_t count[kSortWaves][kBins];
-    __shared__ uint32_t start[kBins], sums[kSortWaves];
+    __shared__ uint32_t count[kBigWaves][kBins];
+    __shared__ uint32_t start[kBins], sums[kBigWaves];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     for (int b = lane; b < kBins; b += 64) count[w][b] = 0;
     if (!scanned) {
@@ -383,7 +390,7 @@ embedding_scatter_kernel(Keys keys, Pairs in, int shift, int bits, int64_t block
         start[threadIdx.x] = threadIdx.x < (1u << bits) ? counts[(int64_t)threadIdx.x * blocks + blockIdx.x] : 0;
     }
     __syncthreads();
-    constexpr int kRounds = kSortTile / kSortLanes;
+    constexpr int kRounds = kSortTile / kBigLanes;
     const int64_t t0 = (int64_t)blockIdx.x * kSortTile + w * kRounds * 64 + lane;
     uint32_t k[kRounds], p[kRounds];
     int rank[kRounds];
@@ -397,7 +404,7 @@ embedding_scatter_kernel(Keys keys, Pairs in, int shift, int bits, int64_t block
     for (int r = 0; r < kRounds; ++r)
         rank[r] = wave_rank((k[r] >> shift) & ((1u << bits) - 1), t0 + r * 64 < keys.n, bits, count[w], lane);
     __syncthreads();
-    bin_starts(count, start, nullptr);
+    bin_starts<kBigWaves>(count, start, nullptr);
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
         if (t0 + r * 64 >= keys.n) continue;
@@ -405,26 +412,6 @@ embedding_scatter_kernel(Keys keys, Pairs in, int shift, int bits, int64_t block
         out_key[at] = k[r];
         out_pos[at] = p[r];
     }
-}
-
-// How many of the sorted tokens have a row: one wave.
-__global__ void __launch_bounds__(64)
-embedding_valid_kernel(const uint32_t* __restrict__ key, int64_t n, uint32_t none, uint32_t* __restrict__ n_valid) {
-    // 64 tokens are looked at in a round
-    int64_t lo = 0, hi = n;
-    while (lo < hi) {
-        const int64_t step = (hi - lo + 63) / 64, at = lo + (int64_t)threadIdx.x * step;
-        const uint64_t below = __ballot(at < hi && key[at] < none);
-        const int c = __popcll(below);              // the first c are below
-        if (c == 0) {
-            hi = lo;
-        } else {
-            const int64_t next = lo + (int64_t)c * step;
-            lo += (int64_t)(c - 1) * step + 1;
-            hi = next < hi ? next : hi;
-        }
-    }
-    if (threadIdx.x == 0) *n_valid = (uint32_t)lo;
 }
 
 // ------------------------------------------------------------ sums ---------
@@ -490,31 +477,70 @@ __device__ __forceinline__ void add_part(const float* part, int64_t dim, int64_t
     }
 }
 
+// The first of the sorted tokens [0, n) whose key is not below `key`: 64 are looked at in a
+// round, 3 rounds for 2^18 tokens.  The wave's lanes together.
+__device__ __forceinline__ int64_t wave_lower_bound(const uint32_t* keys, int64_t n, int64_t key) {
+    int64_t lo = 0, hi = n;
+    while (lo < hi) {
+        const int64_t step = (hi - lo + 63) / 64, at = lo + (int64_t)(threadIdx.x & 63) * step;
+        const int c = __popcll(__ballot(at < hi && (int64_t)keys[at] < key));   // the first c are below
+        if (c == 0) return lo;
+        const int64_t next = lo + (int64_t)c * step;
+        lo += (int64_t)(c - 1) * step + 1;
+        hi = next < hi ? next : hi;
+    }
+    return lo;
+}
+
 // Rows of the slice that no token has become zero: the first blocks of the launch, a
-// wave for `rows` rows.
+// wave for `rows` rows.  Rows without tokens between two that have some are one run.
 template <int DST>
 __device__ __forceinline__ void clear_rows(const Sorted& q, void* grad, const Slice& s, int64_t u, int rows) {
     const int lane = threadIdx.x & 63;
     const int64_t first = s.begin / s.dim + u * rows;
     const int64_t last = (s.begin + s.count + s.dim - 1) / s.dim;
-    const int64_t row = first + lane;
-    bool mine = lane < rows && row < last;
-    if (mine) {                              // the first sorted token not before this row
-        int64_t lo = 0, hi = q.n;
+    if (first >= last) return;
+    const int n = (int)(last - first < rows ? last - first : rows);
+    int64_t lo = wave_lower_bound(q.key, q.n, first);
+    const int64_t end = wave_lower_bound(q.key, q.n, first + n);
+    bool mine = lane < n;
+    if (mine) {                              // the first sorted token not before the lane's row
+        const int64_t row = first + lane;
+        int64_t hi = end;
         while (lo < hi) {
             const int64_t mid = (lo + hi) >> 1;
             if ((int64_t)q.key[mid] < row) lo = mid + 1;
             else hi = mid;
         }
-        mine = !(lo < q.n && (int64_t)q.key[lo] == row);
+        mine = !(lo < end && (int64_t)q.key[lo] == row);
     }
+    constexpr int64_t W = 16 / kSize<DST>;
     uint64_t todo = __ballot(mine);
-    const float zero[kCols] = {0, 0, 0, 0, 0, 0, 0, 0};
     while (todo) {
         const int r = __ffsll((unsigned long long)todo) - 1;
-        todo &= todo - 1;
-        for (int64_t col = lane * kCols; col < s.dim; col += kSlab) emit<DST>(grad, s, first + r, col, zero, 0.0f, 1);
+        const uint64_t rest = ~(todo >> r);
+        const int run = rest ? __ffsll((unsigned long long)rest) - 1 : 64;
+        todo &= r + run >= 64 ? 0 : ~uint64_t(0) << (r + run);
+        int64_t a = (first + r) * s.dim - s.begin, b = a + run * s.dim;
+        if (a < 0) a = 0;
+        if (b > s.count) b = s.count;
+        // up to 16-byte alignment, whole 16 bytes, the rest
+        const int64_t skew = (int64_t)(((uintptr_t)grad / kSize<DST> + (uintptr_t)a) % W);
+        int64_t head = skew ? W - skew : 0;
+        if (head > b - a) head = b - a;
+        const int64_t whole = (b - a - head) / W, tail = a + head + whole * W;
+        if (lane < head) store1<DST>(grad, a + lane, 0.0f);
+        u32x4* p = (u32x4*)((char*)grad + (a + head) * kSize<DST>);
+        for (int64_t k = lane; k < whole; k += 64) __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, p + k);
+        if (lane < b - tail) store1<DST>(grad, tail + lane, 0.0f);
     }
+}
+
+// How many of the sorted tokens have a row: one wave.
+__global__ void __launch_bounds__(64)
+embedding_valid_kernel(const uint32_t* __restrict__ key, int64_t n, uint32_t none, uint32_t* __restrict__ n_valid) {
+    const int64_t lo = wave_lower_bound(key, n, none);
+    if (threadIdx.x == 0) *n_valid = (uint32_t)lo;
 }
 
 // A wave: a chunk's rows of dy for 512 columns, kRowsAhead at a time, with the old values of
@@ -789,13 +815,13 @@ int zero_embedding_grad(void* grad, int32_t grad_dtype, const void* ids, int32_t
             const Pairs in = {p == 0 ? nullptr : (const uint32_t*)(ws + l.key[at]),
                               p == 0 ? nullptr : (const uint32_t*)(ws + l.pos[at])};
             const int to = p == 0 ? 0 : at ^ 1;
-            rc = launch_shape(embedding_count_kernel, l.blocks, kSortLanes, 0, stream, keys, in, p * per, per,
+            rc = launch_shape(embedding_count_kernel, l.blocks, kBigLanes, 0, stream, keys, in, p * per, per,
                               l.blocks, counts);
             const bool scan = l.blocks > kFewBlocks;
             if (rc == ZERO_OK && scan)
                 rc = launch_shape(embedding_scan_kernel, 1, kSortLanes, 0, stream, counts, l.blocks << per);
             if (rc == ZERO_OK)
-                rc = launch_shape(embedding_scatter_kernel, l.blocks, kSortLanes, 0, stream, keys, in, p * per, per,
+                rc = launch_shape(embedding_scatter_kernel, l.blocks, kBigLanes, 0, stream, keys, in, p * per, per,
                                   l.blocks, (const uint32_t*)counts, (int)scan, (uint32_t*)(ws + l.key[to]),
                                   (uint32_t*)(ws + l.pos[to]));
             at = to;
@@ -808,8 +834,8 @@ int zero_embedding_grad(void* grad, int32_t grad_dtype, const void* ids, int32_t
     const Sorted q = {(const uint32_t*)(ws + l.key[at]), (const uint32_t*)(ws + l.pos[at]), n_valid, l.chunks,
                       (uint32_t)l.slabs, (float*)(ws + l.part), 0, 0};
     const int64_t size = grad_dtype == ZERO_FP32 ? 4 : 2;
-    int rows = 64;                                   // of a wave that clears, about 64 KiB
-    while (rows > 1 && rows * dim * size > 65536) rows /= 2;
+    int rows = 64;                                   // of a wave that clears
+    while (rows > 1 && rows * dim * size > kClearBytes) rows /= 2;
     const int64_t all_rows = (begin + count + dim - 1) / dim - begin / dim;
     const int64_t clear = overwrite ? ((all_rows + rows - 1) / rows + 3) / 4 : 0;
     const int64_t blocks = clear + (l.chunks * l.slabs + 3) / 4;
