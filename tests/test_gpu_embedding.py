@@ -161,10 +161,162 @@ def test_grad_types_and_slices(src, dst, overwrite):
         check_grad(grad, dst, want, bound)
 
 
-def test_workspace_grows_with_the_tokens():
-    for dim in (1, 100, 512, 513, 4096, 30000):
-        last = 0
-        for n in sorted({int(1.3 ** k) for k in range(70)} | {8 * 8192 // (-(-dim // 512)) + k for k in (-1, 0, 1, 2)}):
-            now = Z.zero_embedding_workspace_bytes(n, 1000, dim)
-            assert now >= last, (n, dim)
-            last = now
+
+
+def test_special_values_stay_in_their_rows():
+    vocab, dim, n = 20, 70, 64
+    ids = torch.arange(n, device="cuda") % 10
+    dy = torch.ones(n, dim, device="cuda")
+    dy[3, 5], dy[14, 6], dy[24, 6] = float("nan"), float("inf"), float("-inf")
+    grad = torch.zeros(vocab, dim, device="cuda")
+    Z.zero_embedding_grad(grad, ids, dy, vocab, dim, workspace(n, vocab, dim))
+    got = grad.cpu()
+    assert bool(got[3, 5].isnan()) and bool(got[4, 6].isnan())
+    got[3, 5] = got[4, 6] = 0.0
+    assert bool(torch.isfinite(got).all()) and not bool(got[10:].any())
+    w = torch.full((vocab, dim), 60000.0, device="cuda")
+    out = torch.empty(n, dim, dtype=torch.float16, device="cuda")
+    Z.zero_embedding_lookup(out, ids, w, vocab, dim, scale=2.0)
+    assert bool(out.isinf().all())                           # past fp16's range
+
+
+def test_nothing_else_is_written():
+    vocab, dim, n, pad = 61, 77, 500, 512
+    for kind in TYPES:
+        for begin, count in ((0, vocab * dim), (dim * 3 + 5, dim * 20 + 9), (7, 3)):
+            buf = torch.full((count + 2 * pad + 1,), 3.0, dtype=TYPES[kind], device="cuda")
+            grad = buf[pad + 1:pad + 1 + count]
+            ids, dy = inputs(n, vocab, dim, "bf16", 3, "any")
+            size = Z.zero_embedding_workspace_bytes(n, vocab, dim)
+            ws = torch.full((size + 8192,), 0x55, dtype=torch.uint8, device="cuda")
+            keep = dy.clone()
+            for overwrite in (True, False):
+                Z.zero_embedding_grad(grad, ids, dy, vocab, dim, ws[4096:4096 + size], begin=begin,
+                                      overwrite=overwrite)
+            assert bool((buf[:pad + 1] == 3.0).all()) and bool((buf[pad + 1 + count:] == 3.0).all())
+            assert bool((ws[:4096] == 0x55).all()) and bool((ws[4096 + size:] == 0x55).all())
+            assert torch.equal(dy, keep)
+            # lookup into rows of a wider buffer
+            wide = torch.full((n, dim + 9), 3.0, dtype=TYPES[kind], device="cuda")
+            Z.zero_embedding_lookup(wide[:, 4:4 + dim], ids, grad, vocab, dim, begin=begin)
+            assert bool((wide[:, :4] == 3.0).all()) and bool((wide[:, 4 + dim:] == 3.0).all())
+
+
+def test_slices_lie_side_by_side():
+    """Owners' lookups add up to the whole one, their gradients are its pieces."""
+    vocab, dim, n = 101, 37, 333
+    ids, dy = inputs(n, vocab, dim, "fp32", 9)
+    w = torch.randn(vocab * dim, generator=torch.Generator().manual_seed(5)).cuda()
+    whole, total = torch.empty(n, dim, device="cuda"), torch.zeros(n, dim, device="cuda")
+    Z.zero_embedding_lookup(whole, ids, w, vocab, dim, scale=0.5)
+    grad = torch.zeros(vocab * dim, device="cuda")
+    ws = workspace(n, vocab, dim)
+    Z.zero_embedding_grad(grad, ids, dy, vocab, dim, ws, overwrite=True)
+    size = -(-vocab * dim // 8)
+    for k in range(8):
+        a, b = k * size, min((k + 1) * size, vocab * dim)
+        part = torch.empty(n, dim, device="cuda")
+        Z.zero_embedding_lookup(part, ids, w[a:b], vocab, dim, begin=a, scale=0.5)
+        total += part
+        piece = torch.full((b - a,), 9.0, device="cuda")
+        Z.zero_embedding_grad(piece, ids, dy, vocab, dim, ws, begin=a, overwrite=True)
+        want, bound = grad_ref(ids, dy, vocab, dim, a, piece, 1.0, True, None)
+        check_grad(piece, "fp32", want, bound)
+    assert torch.equal(whole, total)
+
+
+def test_no_tokens():
+    vocab, dim = 30, 20
+    ids = torch.empty(0, dtype=torch.int64, device="cuda")
+    dy = torch.empty(0, dim, device="cuda")
+    none = torch.empty(0, dtype=torch.uint8, device="cuda")
+    grad = torch.ones(vocab, dim, device="cuda")
+    Z.zero_embedding_grad(grad, ids, dy, vocab, dim, none)
+    assert bool((grad == 1).all())
+    Z.zero_embedding_grad(grad, ids, dy, vocab, dim, none, overwrite=True)
+    assert not bool(grad.any())
+    Z.zero_embedding_lookup(torch.empty(0, dim, device="cuda"), ids, grad, vocab, dim)
+    # all of them of no row
+    ids = torch.full((9000,), -100, device="cuda")
+    grad.fill_(2.0)
+    Z.zero_embedding_grad(grad, ids, torch.ones(9000, dim, device="cuda"), vocab, dim, workspace(9000, vocab, dim))
+    assert bool((grad == 2).all())
+
+
+def test_graph_and_streams():
+    vocab, dim = 300, 100
+    for n in (500, 20000):
+        ids, dy = inputs(n, vocab, dim, "bf16", 1)
+        w = torch.randn(vocab, dim, generator=torch.Generator().manual_seed(5)).cuda()
+        out, grad = torch.empty(n, dim, device="cuda"), torch.zeros(vocab, dim, device="cuda")
+        ws = workspace(n, vocab, dim)
+
+        def run():
+            Z.zero_embedding_lookup(out, ids, w, vocab, dim)
+            Z.zero_embedding_grad(grad, ids, dy, vocab, dim, ws)
+
+        run()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        side = torch.cuda.Stream()
+        for k in range(4):
+            new_ids, new_dy = inputs(n, vocab, dim, "bf16", 2 + k, "any")
+            ids.copy_(new_ids)
+            dy.copy_(new_dy)
+            grad.zero_()
+            graph.replay()
+            got = (out.clone(), grad.clone())
+            torch.cuda.synchronize()
+            with torch.cuda.stream(side):
+                grad.zero_()
+                run()
+            side.synchronize()
+            assert torch.equal(got[0], out) and torch.equal(got[1], grad), (n, k)
+
+
+def test_offsets_past_32_bits():
+    """A table and rows of dy beyond 2^31 elements."""
+    vocab, dim, n = 70000, 32768, 9
+    w = torch.zeros(vocab * dim, dtype=torch.bfloat16, device="cuda")
+    ids = torch.tensor([0, vocab - 1, 65536, vocab - 1, 65535, -1, vocab, 3, 69999], device="cuda")
+    for r in (0, 3, 65535, 65536, vocab - 1):
+        w[r * dim:(r + 1) * dim] = float(r % 251 + 1)
+    out = torch.empty(n, dim, device="cuda")
+    Z.zero_embedding_lookup(out, ids, w, vocab, dim)
+    want = torch.tensor([r % 251 + 1 if 0 <= r < vocab else 0 for r in ids.tolist()], dtype=torch.float32)
+    assert torch.equal(out.cpu(), want[:, None].expand(n, dim))
+    dy = torch.ones(n, dim, dtype=torch.bfloat16, device="cuda")
+    Z.zero_embedding_grad(w, ids, dy, vocab, dim, workspace(n, vocab, dim), overwrite=True)
+    sums = w.view(vocab, dim).float()[[0, 3, 65535, 65536, vocab - 1, 1, 69998]]
+    assert torch.equal(sums[:, 0].cpu(), torch.tensor([1.0, 1, 1, 1, 3, 0, 0]))
+    assert bool((sums == sums[:, :1]).all())
+    assert int((w != 0).sum()) == 5 * dim
+
+
+def test_python_refusals():
+    vocab, dim, n = 10, 16, 6
+    ids = torch.zeros(n, dtype=torch.int64, device="cuda")
+    out, w = torch.zeros(n, dim, device="cuda"), torch.zeros(vocab, dim, device="cuda")
+    ws = workspace(n, vocab, dim)
+    ok = (out, ids, w, vocab, dim)
+    Z.zero_embedding_lookup(*ok)
+    for k, bad in ((0, out[:5]), (0, out.t()), (0, out.cpu()), (1, ids.cpu()), (1, ids[::2].repeat(1)[::2]),
+                   (2, w.t()), (2, w.cpu())):
+        args = list(ok)
+        args[k] = bad
+        with pytest.raises(ValueError):
+            Z.zero_embedding_lookup(*args)
+    for k, bad in ((0, out.double()), (1, ids.float()), (2, w.double())):
+        args = list(ok)
+        args[k] = bad
+        with pytest.raises(TypeError):
+            Z.zero_embedding_lookup(*args)
+    with pytest.raises(Z.ZeroError):
+        Z.zero_embedding_lookup(*ok, begin=1)
+    with pytest.raises(Z.ZeroError):
+        Z.zero_embedding_grad(w, ids, out, vocab, dim, ws[:256])
+    with pytest.raises(ValueError):
+        Z.zero_embedding_grad(w, ids, out, vocab, dim, ws.cpu())
+    with pytest.raises(ValueError):
+        Z.zero_embedding_grad(w, ids, out[:, :8], vocab, dim, ws)

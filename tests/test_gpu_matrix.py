@@ -176,3 +176,259 @@ def test_muon_step(dtype, nesterov, scaling, clip, precise):
     for x, y in ((p, before[0]), (m, before[1])):
         assert torch.equal(x.cpu()[~inside], y.cpu()[~inside])
     assert torch.equal(g, before[3])
+
+
+# Five steps' roundings taken as independent: each is u / sqrt(3) (rms, u = 2^-11) of a term
+# that the polynomial weighs by at most |b| + 2 |c|, and later slopes are below 2 where the
+# singular values are by then; added in squares.
+TYPICAL = 2.0 ** -11 / math.sqrt(3) * (abs(B) + 2 * abs(C)) * math.sqrt(5)
+
+
+@pytest.mark.parametrize("rows,cols", [(65, 66), (96, 300), (512, 512), (1376, 512), (1024, 4096), (1300, 1300),
+                                       (1040, 2800)])
+@pytest.mark.parametrize("kind", ["normal", "low"])
+def test_error_is_that_of_the_roundings(rows, cols, kind):
+    g = update(rows, cols, 3, kind).float().cuda()
+    out = torch.empty_like(g)
+    plan = Z.zero_matrix_plan([g], out=[out], precise=False)
+    Z.zero_orthogonalize(plan, workspace(plan))
+    want, _ = polynomial(g)
+    assert float((out.double().cpu() - want).norm()) <= TYPICAL * float(want.norm())
+    # and to 32 bits, where a product's fp32 sums of K terms weigh most: rms sqrt(K) 2^-24
+    plan = Z.zero_matrix_plan([g], out=[out], precise=True)
+    Z.zero_orthogonalize(plan, workspace(plan))
+    k = max(rows, cols)
+    limit = (2.0 ** -21 + math.sqrt(k) * 2.0 ** -24) * (abs(B) + 2 * abs(C)) * math.sqrt(5) * 4
+    assert float((out.double().cpu() - want).norm()) <= limit * float(want.norm())
+
+
+@pytest.mark.parametrize("steps,a,b,c", [(1, A, B, C), (2, A, B, C), (3, 1.5, -0.5, 0.0), (6, A, B, C),
+                                         (4, 1.875, -1.25, 0.375)])
+@pytest.mark.parametrize("rows,cols", [(20, 90), (130, 500), (300, 140), (1030, 1040)])
+def test_coefficients_and_steps(steps, a, b, c, rows, cols):
+    g = update(rows, cols, 8).float().cuda()
+    out = torch.empty_like(g)
+    for precise in (False, True):
+        plan = Z.zero_matrix_plan([g], out=[out], precise=precise)
+        Z.zero_orthogonalize(plan, workspace(plan), ns=Z.zero_newton_schulz(a, b, c, 1e-7, steps))
+        check(out, g, torch.float32, precise, steps=steps, a=a, b=b, c=c)
+
+
+def test_strides_transposes_and_in_place():
+    gen = torch.Generator().manual_seed(6)
+    wide = (torch.randn(300, 3 * 200 + 7, generator=gen) * 0.01).cuda()
+    q, k, v = (wide[:, 7 + 200 * i:7 + 200 * (i + 1)] for i in range(3))
+    tall = (torch.randn(150, 410, generator=gen) * 0.01).bfloat16().cuda()
+    t = tall.t()                                             # columns of consecutive elements
+    rows = (torch.randn(500, 90, generator=gen) * 0.01).half().cuda()[3:400:2]
+    every = [q, k, v, t, rows]
+    want = [polynomial(x, True) for x in every]
+    outs = [torch.zeros(300, 200, device="cuda"), torch.zeros(300, 200, device="cuda", dtype=torch.bfloat16), v,
+            torch.zeros(150, 410, device="cuda").t(), rows]
+    keep = wide.clone()
+    plan = Z.zero_matrix_plan(every, out=outs)
+    Z.zero_orthogonalize(plan, workspace(plan))
+    for y, (w, bound) in zip(outs, want):
+        limit = bound + half_step(y.dtype) * float(w.norm()) * 1.01 + 1e-6
+        assert float((y.double().cpu() - w).norm()) <= limit
+    assert torch.equal(wide[:, :407], keep[:, :407])         # all but v, which is in place
+    one = q.clone()
+    plan = Z.zero_matrix_plan([one])
+    Z.zero_orthogonalize(plan, workspace(plan))
+    # another plan may cut its sums elsewhere: both are within the bound of the same matrix
+    assert float((one.double() - outs[0].double()).norm()) <= 2 * want[0][1]
+    again = q.clone()
+    Z.zero_orthogonalize(Z.zero_matrix_plan([again]), workspace(plan))
+    assert torch.equal(one, again)
+
+
+def test_special_matrices():
+    shapes = [(70, 90), (20, 300), (200, 200), (40, 8), (300, 70)]
+    g = [update(r, c, k).float() for k, (r, c) in enumerate(shapes)]
+    g[1].zero_()                                             # of zeros
+    g[2][3, 7] = float("inf")
+    g[3][1, 1] = float("nan")
+    dev = [x.cuda() for x in g]
+    out = [torch.full_like(x, 7.0) for x in dev]
+    plan = Z.zero_matrix_plan(dev, out=out)
+    Z.zero_orthogonalize(plan, workspace(plan))
+    assert not bool(out[1].any())
+    assert bool(out[2].isnan().all()) and bool(out[3].isnan().all())
+    check(out[0], g[0], torch.float32, True)
+    check(out[4], g[4], torch.float32, True)
+    # a matrix of zeros among the larger ones
+    z = torch.zeros(100, 130, device="cuda")
+    plan = Z.zero_matrix_plan([z], out=[torch.ones_like(z)])
+    Z.zero_orthogonalize(plan, workspace(plan))
+    assert not bool(plan.out[0].any())
+
+
+@pytest.mark.parametrize("scale", [1e-18, 1e18])
+@pytest.mark.parametrize("shape", [(30, 200), (129, 300)])
+def test_any_magnitude(scale, shape):
+    # the norm is far above eps, or eps is given as small
+    g = (update(*shape, 2) * scale).float().cuda()
+    out = torch.empty_like(g)
+    plan = Z.zero_matrix_plan([g], out=[out])
+    Z.zero_orthogonalize(plan, workspace(plan), ns=Z.zero_newton_schulz(eps=1e-28))
+    check(out, g, torch.float32, True, eps=1e-28)
+
+
+def test_many_matrices_and_whole_tiles():
+    # more 256-wide tiles than a round of blocks, a cut rest, several groups, small ones between
+    shapes = ([(1024, 1030)] * 30 + [(16, 700), (700, 16)] * 20 + [(513, 512)] * 150 + [(1500, 1200)])
+    g = [update(r, c, k % 7, "low").bfloat16().cuda() for k, (r, c) in enumerate(shapes)]
+    out = [torch.empty_like(x) for x in g]
+    plan = Z.zero_matrix_plan(g, out=out)
+    ws = workspace(plan)
+    Z.zero_orthogonalize(plan, ws)
+    for k in (0, 29, 30, 31, 69, 70, 100, 219, 220):
+        want, _ = polynomial(g[k])
+        off = float((out[k].double().cpu() - want).norm())
+        assert off <= (TYPICAL + half_step(torch.bfloat16)) * float(want.norm()), k
+    # the same matrices agree wherever they are in the list (whole or cut tiles)
+    seen = {}
+    for k, (x, y) in enumerate(zip(g, out)):
+        other = seen.setdefault((tuple(x.shape), k % 7), y)
+        off = float((y.double() - other.double()).norm())
+        assert off <= 2 * (TYPICAL + half_step(torch.bfloat16)) * float(y.double().norm()), k
+    again = [y.clone() for y in out]
+    ws.fill_(0x3C)
+    Z.zero_orthogonalize(plan, ws)
+    assert all(torch.equal(x, y) for x, y in zip(out, again))
+
+
+def test_nothing_else_is_written():
+    shapes = [(65, 129), (300, 70), (5, 33), (1300, 257)]
+    pad = 256
+    total = sum(r * c + pad for r, c in shapes) + pad
+    for dtype in (torch.float32, torch.bfloat16, torch.float16):
+        src = torch.randn(total, generator=torch.Generator().manual_seed(1)).to(dtype).cuda()
+        dst = torch.full((total,), 3.0, dtype=dtype, device="cuda")
+        g, out, at, inside = [], [], pad + 1, torch.zeros(total, dtype=torch.bool)
+        for r, c in shapes:
+            g.append(src[at:at + r * c].view(r, c))
+            out.append(dst[at:at + r * c].view(r, c))
+            inside[at:at + r * c] = True
+            at += r * c + pad - 1
+        keep = src.clone()
+        plan = Z.zero_matrix_plan(g, out=out)
+        size = Z.zero_matrix_workspace_bytes(plan)
+        ws = torch.full((size + 8192,), 0x55, dtype=torch.uint8, device="cuda")
+        Z.zero_orthogonalize(plan, ws[4096:4096 + size])
+        assert torch.equal(src, keep)
+        assert bool((dst.cpu()[~inside] == 3.0).all())
+        assert bool((ws[:4096] == 0x55).all()) and bool((ws[4096 + size:] == 0x55).all())
+
+
+def test_muon_skips_on_overflow():
+    matrices = [(0, 30, 50), (1500, 200, 130)]
+    p, m, p16, g = muon_state(matrices, 27500, "fp16", 3)
+    before = [x.clone() for x in (p, m, p16)]
+    plan = Z.zero_muon_plan(matrices)
+    ws = workspace(plan)
+    Z.zero_muon_step(p, m, p16, g, plan, Z.zero_muon_hparams(lr=1.0), result(1.0, 1, 1.0), ws)
+    for x, y in zip((p, m, p16), before):
+        assert torch.equal(x, y)
+
+
+def test_graph_streams_and_two_graphs_of_one_workspace():
+    matrices = [(1, 40, 70), (3000, 260, 300), (90000, 140, 129)]
+    hp = Z.zero_muon_hparams(lr=0.01, max_grad_norm=0.5)
+    plan = Z.zero_muon_plan(matrices)
+    ws = workspace(plan)
+    states = [muon_state(matrices, 110000, "bf16", 7 + k) for k in range(2)]
+    eager = [[x.clone() for x in st] for st in states]
+    res = [result(2.0), result(3.0)]
+    skip = result(1.0, 1)
+
+    def step(st, k, use=None):
+        Z.zero_muon_step(*st, plan, hp, res[k] if use is None else use, ws)
+
+    side = torch.cuda.Stream()
+    graphs = []
+    for k in range(2):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            warm = [x.clone() for x in states[k]]
+            step(warm, k)
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step(states[k], k)
+        graphs.append(graph)
+    for n in range(4):
+        for k in range(2):
+            if n == 2 and k == 1:                            # a skipped step among the replays
+                saved = res[1].clone()
+                res[1].copy_(skip)
+                graphs[1].replay()
+                torch.cuda.synchronize()
+                res[1].copy_(saved)
+                continue
+            graphs[k].replay()
+            torch.cuda.synchronize()
+            with torch.cuda.stream(side):                    # eager work between, on another stream
+                side.wait_stream(torch.cuda.current_stream())
+                step(eager[k], k)
+            side.synchronize()
+            for x, y in zip(states[k], eager[k]):
+                assert torch.equal(x, y), (n, k)
+
+
+def test_python_refusals():
+    g = torch.zeros(8, 9, device="cuda")
+    with pytest.raises(ValueError):
+        Z.zero_matrix_plan([g.view(-1)])
+    with pytest.raises(ValueError):
+        Z.zero_matrix_plan([torch.zeros(8, 9)])
+    with pytest.raises(ValueError):
+        Z.zero_matrix_plan([g], out=[])
+    with pytest.raises(ValueError):
+        Z.zero_matrix_plan([g], out=[torch.zeros(9, 8, device="cuda")])
+    with pytest.raises(ValueError):
+        Z.zero_matrix_plan([g], out=[torch.zeros(9, 8, device="cuda").t()])     # rows here, columns there
+    with pytest.raises(ValueError):
+        Z.zero_matrix_plan([torch.zeros(8, 18, device="cuda")[:, ::2]])
+    with pytest.raises(ValueError):
+        Z.zero_matrix_plan([torch.zeros(1, 9, device="cuda").expand(8, 9)])
+    with pytest.raises(TypeError):
+        Z.zero_matrix_plan([g.double()])
+    with pytest.raises(TypeError):
+        Z.zero_matrix_plan([None])
+    with pytest.raises(Z.ZeroError):
+        Z.zero_matrix_plan([g, g], out=[torch.zeros_like(g)] * 2)
+    plan, ranges = Z.zero_matrix_plan([g]), Z.zero_muon_plan([(0, 8, 9)])
+    ws = workspace(ranges)
+    with pytest.raises(ValueError):
+        Z.zero_orthogonalize(plan, torch.empty(0, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        Z.zero_orthogonalize(plan, torch.empty(1 << 20, dtype=torch.uint8))
+    with pytest.raises(TypeError):
+        Z.zero_orthogonalize(ranges, ws)
+    p, h, r = torch.zeros(72, device="cuda"), torch.zeros(72, device="cuda", dtype=torch.half), result()
+    hp = Z.zero_muon_hparams()
+    with pytest.raises(TypeError):
+        Z.zero_muon_step(p, p.clone(), h, h.clone(), plan, hp, r, ws)
+    with pytest.raises(TypeError):
+        Z.zero_muon_step(p, p.clone(), h, h.bfloat16(), ranges, hp, r, ws)
+    for bad in (p[:71], p.double(), torch.zeros(144, device="cuda")[::2], p.cpu()):
+        with pytest.raises(ValueError):
+            Z.zero_muon_step(bad, p.clone(), h, h.clone(), ranges, hp, r, ws)
+    with pytest.raises(ValueError):
+        Z.zero_muon_step(p, p.clone(), h, h.clone(), ranges, hp, r[:3], ws)
+    with pytest.raises(ValueError):
+        Z.zero_muon_step(p, p.clone(), h, h.clone(), ranges, hp, r, ws[:-1][:16])
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="before the capture"):
+        with torch.cuda.graph(graph, stream=side):
+            Z.zero_muon_plan([(0, 8, 9)])
+
+
+def test_empty_lists():
+    for plan in (Z.zero_matrix_plan([], device="cuda"), Z.zero_matrix_plan([torch.zeros(0, 5, device="cuda")])):
+        Z.zero_orthogonalize(plan, workspace(plan))
+    plan = Z.zero_muon_plan([(0, 0, 9)])
+    p, h = torch.zeros(1, device="cuda"), torch.zeros(1, device="cuda", dtype=torch.half)
+    Z.zero_muon_step(p, p, h, h, plan, Z.zero_muon_hparams(), result(), workspace(plan))

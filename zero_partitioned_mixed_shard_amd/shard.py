@@ -19,6 +19,11 @@ and one for all owners (zero_adamw_step_ranges); the library merges ranges
 that touch into one launch and folds the norm once.  batched=False keeps one
 call per window and per owner.
 
+With `matrices` (whole tensors of two dimensions, as round-robin ownership gives them) the
+step is Muon's there and AdamW's in the rest of every owner's range: one
+zero_adamw_step_ranges call, then one zero_muon_step call, both with the same
+result.  The momentum is exp_avg; exp_avg_sq is not used there.
+
 With fused=False the reduce and the check are separate calls
 (zero_reduce_owned per window, then zero_unscale_check_norm per owner).
 
@@ -88,7 +93,8 @@ from . import (RESULT_BYTES, ZERO_BF16, ZERO_FP16, control_to_device, read_contr
                zero_loss_scaler_update, zero_reduce_check_owned, zero_reduce_check_owned_ctl,
                zero_reduce_owned, zero_step_control_init, zero_step_control_update,
                zero_unscale_check_norm, zero_unscale_check_norm_ctl, zero_adamw_step_ranges,
-               zero_range_workspace_bytes, zero_reduce_check_buckets, zero_reduce_check_ranges)
+               zero_range_workspace_bytes, zero_reduce_check_buckets, zero_reduce_check_ranges,
+               zero_matrix_workspace_bytes, zero_muon_hparams, zero_muon_plan, zero_muon_step)
 
 
 def _interleaved(names, streams, in_place):
@@ -182,7 +188,11 @@ class ShardStep:
                  own_ranks: bool = False, world: int = 0, arena: bool = False,
                  min_gap: int = 0, device_control: bool = False, placement: str = "interleaved",
                  arena_slack: int = 0, batched: bool = True, rank_layout: str = "flat",
-                 device="cuda"):
+                 matrices: Sequence[Tuple[int, int, int]] = (),
+                 muon: Optional[zero_muon_hparams] = None, device="cuda"):
+        """matrices: (flat offset, rows, cols) of the tensors that take Muon steps, each inside
+        one owner's range; muon: their hyper-parameters (by default lr, weight_decay and
+        max_grad_norm as given here)."""
         self.begin, self.end = begin, end
         self.count = end - begin
         self.owners = [(a - begin, b - begin) for a, b in owners]
@@ -229,6 +239,7 @@ class ShardStep:
         if batched and (len(self._reduce_list) > 1 or rank_layout == "bucket"):
             ws = max(ws, zero_range_workspace_bytes(self._reduce_list))
         self.workspace = torch.empty((ws + 7) // 8, dtype=torch.float64, device=device)
+        self._matrices(matrices, muon, lr, weight_decay, max_grad_norm, device)
         self.placement = placement if arena else "separate"
         self.placement_ms = {}                  # first stage: one timed step per candidate
         self.placement_finalists_ms = {}        # second stage: median of three, six fastest
@@ -241,6 +252,32 @@ class ShardStep:
         if device_control:
             self.ctl = control_to_device(zero_step_control_init(
                 scale0, min_scale, window, float(divisor), beta1, beta2), device=device)
+
+    def _matrices(self, matrices, muon, lr, weight_decay, max_grad_norm, device) -> None:
+        """The plan of the Muon steps, and AdamW's ranges without them."""
+        self.muon_plan = None
+        self._adamw_list = self._owner_list
+        if not matrices:
+            return
+        at = sorted((int(o) - self.begin, int(r), int(c)) for o, r, c in matrices)
+        rest = []
+        for a, b in self.owners:
+            for o, r, c in at:
+                if r * c and a <= o < b:
+                    if o + r * c > b:
+                        raise ValueError("a matrix reaches past its owner's range: Muon steps need "
+                                         "whole tensors")
+                    rest.append((a, o - a))
+                    a = max(a, o + r * c)
+            rest.append((a, b - a))
+        if sum(r * c for _, r, c in at) + sum(n for _, n in rest) != sum(b - a for a, b in self.owners):
+            raise ValueError("matrices overlap, or lie outside the owners' ranges")
+        self._adamw_list = [(a, n) for a, n in rest if n > 0]
+        self.muon_plan = zero_muon_plan(at, device=device)
+        self.muon_hp = zero_muon_hparams(lr=lr, weight_decay=weight_decay, max_grad_norm=max_grad_norm) \
+            if muon is None else muon
+        self.muon_workspace = torch.empty(max(1, zero_matrix_workspace_bytes(self.muon_plan)),
+                                          dtype=torch.uint8, device=device)
 
     # ----------------------------------------------------------- placement
     def _allocate(self, n, n_ranks, separate_red, arena, min_gap, placement, slack, device):
@@ -487,7 +524,13 @@ class ShardStep:
                                                 accumulate=k > 0)
         mark(2)
         self.hp.step = self.t + 1
-        if self.batched and len(self._owner_list) > 1:
+        if self.muon_plan is not None:
+            if self._adamw_list:
+                zero_adamw_step_ranges(self.master, self.exp_avg, self.exp_avg_sq, self.param16, red,
+                                       self._adamw_list, self.hp, self.res, ctl_dev=ctl)
+            zero_muon_step(self.master, self.exp_avg, self.param16, red, self.muon_plan, self.muon_hp,
+                           self.res, self.muon_workspace)
+        elif self.batched and len(self._owner_list) > 1:
             zero_adamw_step_ranges(self.master, self.exp_avg, self.exp_avg_sq, self.param16, red,
                                    self._owner_list, self.hp, self.res, ctl_dev=ctl)
         else:
