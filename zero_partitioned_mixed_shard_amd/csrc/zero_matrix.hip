@@ -977,7 +977,7 @@ matrix_join_kernel(Step s, Product c, MuonBufs mb, MuonConsts mc) {
 // and the result P U / (||U|| + eps): two passes over the matrix and three launches, all to
 // 32 bits.  A's rounding grows with the square of what the steps multiply small singular
 // values by, so A, Q and P are fp64.  (The way of the larger ones, three launches for
-// each step, took 250 us for 56 factors of 16 x 2048, this one SMALL_US.)
+// each step, took 250 us for 56 factors of 16 x 2048, this one 73.)
 constexpr int kSmall = 64;                 // shorter side, at most
 constexpr int kSmallCols = 128;            // columns of the wide form that are in LDS at once
 constexpr int kSmallParts = 256;           // blocks of a matrix, at most
@@ -1200,32 +1200,44 @@ int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
 // Matrices with a shorter side of at most kTogether take their steps in pairs, and are `many`
 // with so many tiles of 256 on and below their diagonals.
-constexpr int64_t kTogether = 1024, kMany = 512;
-// The tile of a matrix's products, by its shorter side; 0: it is a small one.
+constexpr int64_t kTogether = 1024, kMany = 480, kManyPrecise = 240;
+// The tile of a matrix's products, by its shorter side.
 // 256 wide ones do up to 1.7 times the work of 128 wide ones in the same time, which need
-// more of LDS than of the matrix cores; these are more, and each shorter.  One owner's 9
-// matrices of 1024 x 1024 to 4096: 880 us with 128, 1075 with 256.
+// more of LDS than of the matrix cores; these are more, and each shorter.  9 matrices of
+// 1024 x 1024 to 4096 (90 tiles of 256): 690 us with 128, 920 with 256; 24 of 1024 x 1024
+// (240) 1177 and 1226, 48 of them 2379 and 2261.  In 32 bits 1611, 1624; 2489, 2302; 5150, 4095.
 int tile_for(int64_t m, bool many) {
-    return m <= kSmall ? 0 : 4 * up(m, 256) > 5 * up(m, 128) || (m <= kTogether && !many) ? 128 : 256;
+    return 4 * up(m, 256) > 5 * up(m, 128) || (m <= kTogether && !many) ? 128 : 256;
 }
 // Whether two steps go together: with Q = a + B, the second step's A is Q A Q and what
 // both do to X is Q' Q, 5 products of m x m (half computed) in the place of 2 and of one
 // of m x n by its transpose and one of m x m by m x n: fewer operations where n > m.  Of
 // the smaller matrices all go together, since their time is that of the launches.
 bool pairs_for(int64_t m, int64_t n) { return m <= kTogether || 2 * n >= 3 * m; }
+// A list of so few 128 wide tiles below the diagonals goes through the steps together, with
+// 128 wide tiles and in pairs: one matrix of 2048 x 2048 in 473 us and not 535, of 2048 x
+// 8192 in 781 and not 830, but two of 2048 x 2048 (272 tiles) in 819 and not 745.  In 32 bits
+// one of 1500 x 1500 (78 tiles) takes 568 us and not 591, one of 2048 x 5504 1840 and not
+// 1511.  Where the list would be several groups, one after the other, and is one round of
+// blocks together, too: 3 of 1500 x 1700 and 9 of 800 x 900 in 804 us and not 1121.
+constexpr int64_t kFew = 160, kFewPrecise = 80, kRound = 512;
 // Tiles below the diagonal of a group of matrices, and bytes of its planes, after
 // which the next matrix begins another group.
 constexpr int64_t kGroupTiles = 1024, kGroupBytes = int64_t(4) << 30;
 
 // How the tiles of a product are cut: the last n % slots of them are the last round of
-// blocks on the device.  Costs are in stages of a tile.
+// blocks on the device.  Costs are in stages of a tile: a block's begin and end, and what
+// the parts' sums (64 kB or 256 kB each) and the second launch take.  Without these, two of
+// 2048 x 2048 took 1084 us in the place of 745, one 666 in the place of 535.
 Cut cut_for(int64_t n, int tile, int64_t stages) {
     const int64_t slots = tile == 256 ? 256 : 512, rest = n % slots;
     Cut best = {n, 1, 0};
     if (rest == 0) return best;
-    int64_t least = stages;
+    const int64_t ends = 2048 / tile;
+    int64_t least = stages + ends;
     for (int64_t parts = 2; parts <= 16 && parts * rest <= 2 * slots && stages / parts >= 8; ++parts) {
-        const int64_t cost = (parts * rest + slots - 1) / slots * ((stages + parts - 1) / parts) + 24;
+        const int64_t rounds = (parts * rest + slots - 1) / slots;
+        const int64_t cost = rounds * ((stages + parts - 1) / parts + ends) + parts * rest / ends + 3 * ends / 2;
         if (cost < least) {
             least = cost;
             best = {n - rest, (int32_t)parts, 0};
@@ -1346,10 +1358,24 @@ struct Build {
             const int64_t q = up(t.m, 256) / 256;
             if (t.m > kSmall && t.m <= kTogether) tiles += q * (q + 1) / 2;
         }
-        const bool many = tiles >= kMany;
+        const bool many = tiles >= (precise ? kManyPrecise : kMany);
+        // whether all of them go together
+        int64_t tiles128 = 0;
+        bool kinds[4] = {false, false, false, false};
+        for (const Mat& t : in) {
+            if (t.m <= kSmall) continue;
+            const int64_t q = up(t.m, 128) / 128;
+            tiles128 += q * (q + 1) / 2;
+            kinds[2 * (tile_for(t.m, many) == 256) + (!precise && pairs_for(t.m, t.n))] = true;
+        }
+        const bool one = tiles128 <= (precise ? kFewPrecise : kFew) ||
+                         (tiles128 <= kRound && kinds[0] + kinds[1] + kinds[2] + kinds[3] > 1);
+        auto kind_of = [&](const Mat& t) {
+            return one ? (precise ? 0 : 1) : 2 * (tile_for(t.m, many) == 256) + (!precise && pairs_for(t.m, t.n));
+        };
         std::vector<Mat> few;
         for (const Mat& t : in)
-            if (t.m > 0 && tile_for(t.m, many) == 0) few.push_back(t);
+            if (t.m > 0 && t.m <= kSmall) few.push_back(t);
         if (!few.empty() && !add_small(few)) return ZERO_ERANGE;
         for (const int kind : {0, 1, 2, 3}) {
             const int tile = kind < 2 ? 128 : 256;
@@ -1357,7 +1383,7 @@ struct Build {
             std::vector<Mat> v;
             int64_t tiles = 0, bytes = 0;
             for (Mat& t : in) {
-                if (t.m == 0 || tile_for(t.m, many) != tile || (!precise && pairs_for(t.m, t.n)) != pairs) continue;
+                if (t.m <= kSmall || kind_of(t) != kind) continue;
                 t.mp = (int32_t)up(t.m, tile), t.np = (int32_t)up(t.n, tile);
                 const int64_t q = t.mp / tile;
                 v.push_back(t);
