@@ -67,7 +67,8 @@ enum zero_status {
 enum zero_dtype {
     ZERO_FP16 = 1,     /* IEEE 754 binary16 */
     ZERO_BF16 = 2,     /* bfloat16          */
-    ZERO_FP32 = 3      /* IEEE 754 binary32; in the zero_tensor_* calls' tables only */
+    ZERO_FP32 = 3      /* IEEE 754 binary32; in the tables of the zero_tensor_* and
+                        * zero_matrix_* calls and in the zero_embedding_* calls */
 };
 
 #define ZERO_MAX_RANKS 16
@@ -596,19 +597,21 @@ int zero_tensor_accumulate_norm(const zero_tensor_plan* plan, const void* table,
  *   A = X X^T,  X <- a X + (b A + c A A) X
  * on the wide form (G or its transpose, rows <= columns), transposed back.  A matrix of
  * zeros gives zeros; one that holds inf or NaN gives NaN.  The products are fp16 with
- * fp32 sums, the linear term a X has 22 bits; the result is off by 1e-3 to 2e-3 of its
- * norm (fewer for ill-conditioned matrices), and with `precise`, where every factor has
- * 22 bits, by about 1e-5. */
+ * fp32 sums, the linear term a X has 22 bits; the result is off by up to 1.4e-3 of its
+ * norm (3.4e-3 for a matrix of almost rank 1), and with `precise`, where every factor has
+ * 22 bits, by 1e-6 to 1e-5 (3e-4).  With a shorter side of at most 64 all is in 32 bits or
+ * more.  The same call gives the same bits; in another list a matrix's sums may be cut
+ * elsewhere, which changes the result within these errors. */
 
 /* Coefficients.  They have to keep the singular values within 1.75: the largest value
  * of |a x + b x^3 + c x^5| for x in [0, 1], then in [0, that value], and so on for all
  * steps; and the product of the largest slopes there, by which an error grows, within
  * 2^20.  3.4445, -4.7750, 2.0315 and 5 steps, the usual choice, stay below 1.21 and at
- * 485 (11 steps are the most). */
+ * 851 (10 steps are the most). */
 typedef struct zero_newton_schulz {
     float a, b, c;
     float eps;           /* >= 1e-30; 1e-7 */
-    int32_t steps;       /* >= 1           */
+    int32_t steps;       /* 1 .. 32        */
 } zero_newton_schulz;
 
 /* A matrix of a list: `rows` rows of `cols` elements, `src_ld` elements apart, and

@@ -2,7 +2,8 @@
 
 Argument marshalling only: every phase runs in the HIP kernels of
 ``csrc/zero_shard.hip``, ``csrc/zero_flat.hip``, ``csrc/zero_tensors.hip``,
-``csrc/zero_matrix.hip`` and ``csrc/zero_embedding.hip`` behind the C ABI of ``include/zero_shard.h``.  The functions keep the C names.  Device buffers are
+``csrc/zero_matrix.hip`` and ``csrc/zero_embedding.hip`` behind the C ABI of
+``include/zero_shard.h``.  The functions keep the C names.  Device buffers are
 torch tensors (device memory and streams are all torch is used for); 16-bit
 data is passed as torch.float16 / torch.bfloat16 tensors, fp32 state as
 torch.float32.  There is no fallback: if the library is missing, importing

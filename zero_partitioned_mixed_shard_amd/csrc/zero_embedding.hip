@@ -27,10 +27,14 @@ constexpr int kSortLanes = 1024, kSortWaves = kSortLanes / 64;
 constexpr int kSmallSort = 8192;           // tokens that one block sorts in LDS
 constexpr int kBigLanes = 512, kBigWaves = kBigLanes / 64;
 constexpr int kSortTile = 2048;            // tokens of a block of the larger sort
-// Tokens of a chunk, and (chunk, 512 columns) units that are enough for the device.
+// Tokens of a chunk, and (chunk, 512 columns) units that are enough for the device: the
+// gradient of 16384 tokens of 4096 takes 115 us with 4096 units and 119 with 8192 (more
+// parts to join).
 constexpr int64_t kLeastChunk = 8, kMostChunk = 512, kChunkUnits = 4096;
 // Bytes that a wave clears, about.
 constexpr int64_t kClearBytes = 32768;
+// (A pass over 16384 to 65537 tokens takes 4 to 5 us for the counts and 7 to 8 for the
+// scatter, two passes up to 2^18 ids: launches and chains of dependent accesses, not bytes.)
 // Blocks whose counts each block of the larger sort adds up by itself; more take a launch.
 constexpr int64_t kFewBlocks = 64;
 constexpr int kDigit = 9, kBins = 1 << kDigit;   // most bits of a pass
@@ -544,7 +548,9 @@ embedding_valid_kernel(const uint32_t* __restrict__ key, int64_t n, uint32_t non
 }
 
 // A wave: a chunk's rows of dy for 512 columns, kRowsAhead at a time, with the old values of
-// the rows that end among them.
+// the rows that end among them.  16384 rows of 4096 bf16 into fp32 sums take 75 us, 4.2 TB/s,
+// in the order of their ids, which is none of memory's; with 8 rows ahead the whole gradient
+// takes 133 us in the place of 115.
 constexpr int kRowsAhead = 4;
 
 template <int SRC, int DST>
@@ -634,6 +640,7 @@ embedding_sum_kernel(Sorted q, const void* __restrict__ dy, int64_t dy_ld, void*
 
 // The ids that go on past a chunk's end, at the chunk where they begin: a block adds up
 // their parts of the following chunks for 512 columns, its waves a quarter each, in order.
+// 11 us for 16384 tokens of 4096.
 template <int DST>
 __global__ void __launch_bounds__(kThreads)
 embedding_join_kernel(Sorted q, void* __restrict__ grad, Slice s, float scale, int overwrite, int64_t blk0) {

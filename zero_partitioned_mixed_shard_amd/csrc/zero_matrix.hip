@@ -7,25 +7,31 @@
 // times
 //     A = X X^T,   B = b A + c A A,   X <- a X + B X,
 // which applies the polynomial a x + b x^3 + c x^5 to the singular values and
-// leaves the singular vectors.  A and A A are symmetric: only the tiles on and
-// below the diagonal are computed, and written twice.  Per step that is
-// 3 m^2 n + m^3 operations where products that know nothing of the symmetry take
-// 4 m^2 n + 2 m^3.
+// leaves the singular vectors.  A and what is made of it are polynomials of one symmetric
+// matrix, so they commute and are symmetric: only the tiles on and below the diagonal are
+// computed, and written twice.  A step is 3 m^2 n + m^3 operations (4 m^2 n + 2 m^3 without
+// the symmetry); two steps to a pass over X (pairs_for) are 3 m^2 n + 5 m^3.
+//
+// Bounds.  Large matrices are bound by the matrix cores, at the clock that their power
+// leaves: a product with X of 8192 x 28672 runs at 1235 TFLOP/s (1324 in its loop), where the
+// library's of 8192^3 reaches 1517.  Of matrices of 1024 to 2048 the tiles' ends weigh (a
+// quarter of the time at a depth of 2048: X's two parts and the planes through HBM), of
+// smaller ones the launches.
 //
 // Numerics.  The products run on the matrix cores in fp16 with fp32 sums.  fp16 has
 // three bits more than bf16 at the same rate, and its range is enough here: a
 // matrix's entries are bounded by its largest singular value, which the host bounds
 // for the given coefficients (at most 1.75), so X is kept times 2^15 and A times
 // 2^14 and nothing overflows, while entries down to 2^-29 stay normal.  X is kept in
-// two parts, hi = fp16(x) and lo = fp16(x - hi).  The products read hi alone; the
-// linear term a X takes both.  A direction of small singular values is multiplied by
-// a in every step (485 times in 5 steps), and so would be the rounding of X; the two
-// parts keep that term to 22 bits.  Relative error of the result (2-norm), against 64
-// bits, of 512 x 1376: a normal matrix 1.4e-3 without lo and 1.6e-3 with it (the
-// rounding of B, the same either way), one of rank 32 with 5 % of noise 6e-3 and
-// 2e-4, one of rank 1 with 0.1 % of noise 0.12 and 2e-4; in bf16 0.011, 0.05 and 1.
-// With `precise` A and B have two parts too and every product is hi hi + hi lo +
-// lo hi, three times the matrix work, for results in 32 bits.
+// two parts, hi = fp16(x) and lo = fp16(x - hi).  A direction of small singular values is
+// multiplied by a in every step (485 times in 5 steps), and so would be the rounding of X:
+// the linear term a X takes both parts, the products hi alone, but for what is large on the
+// planes' diagonals: what these lose in rounding, and their product with lo, are added in
+// the tiles' ends to first order.  Relative error of the result (2-norm) against 64 bits:
+// 3e-4 to 1.4e-3 for normal matrices and for ones of low rank with 5 % of noise, up to
+// 3.4e-3 for ones of almost rank 1 (0.1 % of noise; without lo 0.12, in bf16 1).
+// With `precise` A, B and X have two parts and every product is hi hi + hi lo + lo hi, three
+// times the matrix work: 1e-6 to 1e-5, and up to 3e-4 for large ones of almost rank 1.
 
 #include <math.h>
 #include <string.h>
@@ -778,7 +784,10 @@ __device__ __forceinline__ void each_of(std::index_sequence<I...>, F&& f) {
 
 // A tile of one product, or a part of its depth: T x T by 4 waves, a quarter each, with
 // the sums in registers.  Stages of 32 of the depth go from memory into LDS three ahead of
-// their products, and from LDS into registers one ahead.
+// their products, and from LDS into registers one ahead: 75 to 77 % of the matrix cores'
+// cycles in the loop (1324 TFLOP/s).
+// Ends whose reads begin before the loop, and ends in loops (26 kB of code, not 58), take the
+// same time: what a tile's end costs are its planes' bytes, at once from all blocks.
 template <int T, int OP, int DT, bool PRECISE>
 __global__ void __launch_bounds__(256, T == 256 ? 1 : 2)
 matrix_product_kernel(Step s, Product c, MuonBufs mb, MuonConsts mc) {
@@ -977,7 +986,7 @@ matrix_join_kernel(Step s, Product c, MuonBufs mb, MuonConsts mc) {
 // and the result P U / (||U|| + eps): two passes over the matrix and three launches, all to
 // 32 bits.  A's rounding grows with the square of what the steps multiply small singular
 // values by, so A, Q and P are fp64.  (The way of the larger ones, three launches for
-// each step, took 250 us for 56 factors of 16 x 2048, this one 73.)
+// each step, took 250 us for 56 factors of 16 x 2048, this one 53.)
 constexpr int kSmall = 64;                 // shorter side, at most
 constexpr int kSmallCols = 128;            // columns of the wide form that are in LDS at once
 constexpr int kSmallParts = 256;           // blocks of a matrix, at most
@@ -1069,19 +1078,21 @@ struct SmallNs {
     double a, b, c, eps;
     int32_t steps, pad;
 };
-__global__ void __launch_bounds__(kThreads)
-small_steps_kernel(Step s, SmallNs ns) {
-    if (skipped(s.res)) return;
-    constexpr int kLd = kSmall + 1;
-    __shared__ double A[kSmall * kLd], Q[kSmall * kLd], P[kSmall * kLd], W[kSmall * kLd];
-    __shared__ double norm;
-    const Mat t = s.mats[blockIdx.x];
+// A thread has R x R elements of all products: of 16 x 2048 matrices (R = 1) the launch took
+// 31 us where 16 threads had 4 x 4 each, and 9.7 with an element for each of 256.
+constexpr int kStepsLd = kSmall + 1;
+template <int R>
+__device__ __forceinline__ void small_steps(const Step& s, const SmallNs& ns, const Mat& t, double* A, double* Q,
+                                            double* P, double* W, double* norm) {
+    constexpr int kSide = 16 * R, kLd = kStepsLd;
     const int side = (t.m + 3) / 4, blocks = side * side, tid = threadIdx.x;
-    const int bi = tid / side * 4, bj = tid % side * 4;
-    const bool on = tid < blocks;
+    const int bi = tid / 16 * R, bj = tid % 16 * R;
     const double* part = (const double*)(s.ws + t.p[0]);
+    for (int e = tid; e < kSide * kLd; e += kThreads) A[e] = 0.0;
+    __syncthreads();
     for (int e = tid; e < blocks * 16; e += kThreads) {
         double sum = 0.0;
+#pragma unroll 8
         for (int k = 0; k < t.n_parts; ++k) sum += part[(int64_t)k * blocks * 16 + e];
         const int b = e >> 4, p = (e & 15) >> 2, q = e & 3;
         A[(b / side * 4 + p) * kLd + b % side * 4 + q] = sum;
@@ -1090,32 +1101,30 @@ small_steps_kernel(Step s, SmallNs ns) {
     if (tid == 0) {
         double sum = 0.0;
         for (int k = 0; k < t.m; ++k) sum += A[k * kLd + k];
-        norm = sqrt(sum) + ns.eps;
-        ((float*)(s.ws + t.r[0]))[0] = (float)(1.0 / norm);
+        *norm = sqrt(sum) + ns.eps;
+        ((float*)(s.ws + t.r[0]))[0] = (float)(1.0 / *norm);
     }
     __syncthreads();
-    double c[16];
-    auto product = [&](const double* x, const double* y) {     // the thread's 4 x 4 of x y
+    double c[R * R];
+    auto product = [&](const double* x, const double* y) {     // the thread's part of x y
 #pragma unroll
-        for (int e = 0; e < 16; ++e) c[e] = 0.0;
-        if (on)
-            for (int k = 0; k < side * 4; ++k) {
-                double u[4], v[4];
+        for (int e = 0; e < R * R; ++e) c[e] = 0.0;
+#pragma unroll(R == 1 ? 16 : 4)
+        for (int k = 0; k < kSide; ++k) {
+            double u[R], v[R];
 #pragma unroll
-                for (int p = 0; p < 4; ++p) u[p] = x[(bi + p) * kLd + k], v[p] = y[k * kLd + bj + p];
+            for (int p = 0; p < R; ++p) u[p] = x[(bi + p) * kLd + k], v[p] = y[k * kLd + bj + p];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) c[e] = fma(u[e >> 2], v[e & 3], c[e]);
-            }
-        __syncthreads();
-    };
-    auto each = [&](auto&& f) {                                 // f(element, its product)
-        if (on) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) f((bi + (e >> 2)) * kLd + bj + (e & 3), c[e], bi + (e >> 2) == bj + (e & 3));
+            for (int e = 0; e < R * R; ++e) c[e] = fma(u[e / R], v[e % R], c[e]);
         }
         __syncthreads();
     };
-    const double inv = 1.0 / (norm * norm);
+    auto each = [&](auto&& f) {                                 // f(element, its product)
+#pragma unroll
+        for (int e = 0; e < R * R; ++e) f((bi + e / R) * kLd + bj + e % R, c[e], bi + e / R == bj + e % R);
+        __syncthreads();
+    };
+    const double inv = 1.0 / (*norm * *norm);
     each([&](int at, double, bool) { A[at] *= inv; });
     for (int k = 0; k < ns.steps; ++k) {
         product(A, A);
@@ -1138,6 +1147,16 @@ small_steps_kernel(Step s, SmallNs ns) {
         const int i = e / kSmall, j = e % kSmall;
         out[e] = j < side * 4 ? (float)P[i * kLd + j] : 0.0f;
     }
+}
+__global__ void __launch_bounds__(kThreads)
+small_steps_kernel(Step s, SmallNs ns) {
+    if (skipped(s.res)) return;
+    __shared__ double A[kSmall * kStepsLd], Q[kSmall * kStepsLd], P[kSmall * kStepsLd], W[kSmall * kStepsLd];
+    __shared__ double norm;
+    const Mat t = s.mats[blockIdx.x];
+    if (t.m <= 16) small_steps<1>(s, ns, t, A, Q, P, W, &norm);
+    else if (t.m <= 32) small_steps<2>(s, ns, t, A, Q, P, W, &norm);
+    else small_steps<4>(s, ns, t, A, Q, P, W, &norm);
 }
 
 // Second pass: P (U / norm), a block's columns, and what becomes of it.  A thread has 4 rows
