@@ -986,7 +986,7 @@ matrix_join_kernel(Step s, Product c, MuonBufs mb, MuonConsts mc) {
 // and the result P U / (||U|| + eps): two passes over the matrix and three launches, all to
 // 32 bits.  A's rounding grows with the square of what the steps multiply small singular
 // values by, so A, Q and P are fp64.  (The way of the larger ones, three launches for
-// each step, took 250 us for 56 factors of 16 x 2048, this one 53.)
+// each step, took 250 us for 56 factors of 16 x 2048, this one 40.)
 constexpr int kSmall = 64;                 // shorter side, at most
 constexpr int kSmallCols = 128;            // columns of the wide form that are in LDS at once
 constexpr int kSmallParts = 256;           // blocks of a matrix, at most
@@ -1581,30 +1581,35 @@ struct NsConsts {
 };
 
 // Bounds of the singular values through the steps, from 1: the largest value that the
-// polynomial takes between 0 and the last bound; of B's eigenvalues; and of T's, what the
-// polynomial applied twice multiplies a value by, less a^2.  Sampled at 4096 points, the
-// first with its second-order error added.
+// polynomial takes between 0 and the last bound, at the end or where its derivative, a
+// quadratic of x^2, is 0; of B's eigenvalues likewise; and of T's, what the polynomial applied
+// twice multiplies a value by, less a^2, at 192 points (scale_for leaves a tenth to spare).
+// All of them at 4096 points took 60 us of each call, more than the kernels of small lists.
 bool ns_bounds(const zero_newton_schulz& ns, double* most_b, double* most_t) {
     const double a = ns.a, b = ns.b, c = ns.c;
+    const double disc = 9 * b * b - 20 * a * c;
+    const double half = disc >= 0 ? -0.5 * (3 * b + copysign(sqrt(disc), b)) : 0.0;
+    // x^2 where the value, the slope and B's eigenvalue may have their extremes; what is not
+    // inside (inf and NaN of a zero divisor among it) is passed over
+    const double of_value[2] = {half / (5 * c), a / half}, of_slope = -0.3 * b / c, of_b = -0.5 * b / c;
     double r = 1.0, top_b = 0.0, top_t = 0.0, grow = 1.0;
     for (int k = 0; k < ns.steps; ++k) {
-        const int n = 4096;
-        double top = 0.0;
-        for (int q = 0; q <= n; ++q) {
-            const double x = r * q / n, l = x * x;
-            const double e = b * l + c * l * l, y = (a + e) * x, ll = y * y;
-            top_b = std::max(top_b, fabs(e));
-            top_t = std::max(top_t, fabs((a + b * ll + c * ll * ll) * (a + e) - a * a));
-            top = std::max(top, fabs(y));
-        }
-        double slope = 0.0;
-        for (int q = 0; q <= n; ++q) {
-            const double l = (r * q / n) * (r * q / n);
-            slope = std::max(slope, fabs(a + 3 * b * l + 5 * c * l * l));
+        const double end = r * r;
+        auto value = [&](double l) { return fabs(sqrt(l) * (a + b * l + c * l * l)); };
+        auto slope_at = [&](double l) { return fabs(a + 3 * b * l + 5 * c * l * l); };
+        auto inside = [&](double l) { return l > 0 && l < end; };
+        double top = value(end), slope = std::max(fabs(a), slope_at(end));
+        for (const double l : of_value)
+            if (inside(l)) top = std::max(top, value(l));
+        if (inside(of_slope)) slope = std::max(slope, slope_at(of_slope));
+        top_b = std::max(top_b, fabs(b * end + c * end * end));
+        if (inside(of_b)) top_b = std::max(top_b, fabs(b * of_b + c * of_b * of_b));
+        const int n = 192;
+        for (int q = 1; q <= n; ++q) {
+            const double x = r * q / n, l = x * x, f = a + b * l + c * l * l, ll = f * x * f * x;
+            top_t = std::max(top_t, fabs((a + b * ll + c * ll * ll) * f - a * a));
         }
         grow *= slope;
-        const double h = r / n;
-        top += h * h / 8 * (6 * fabs(b) * r + 20 * fabs(c) * r * r * r);
         if (!(top <= kMostSigma)) return false;
         r = std::max(top, 1e-3);
     }
