@@ -721,6 +721,7 @@ int zero_muon_step(float* master, float* momentum, void* param16, const void* gr
  * what lies outside the slice.
  *   out    device, out: row t's dim elements from out + t * out_ld
  *   table  device, in: the slice, W's elements from `begin`
+ * out overlaps neither ids nor table.
  * Errors: ZERO_EINVAL for NULL or misaligned pointers, sizes below 1 (n_tokens: 0), an
  * unknown type, rows closer than dim, a slice outside the table, a scale that is not
  * finite; ZERO_ERANGE for sizes beyond the limits. */

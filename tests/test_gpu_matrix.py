@@ -432,3 +432,51 @@ def test_empty_lists():
     plan = Z.zero_muon_plan([(0, 0, 9)])
     p, h = torch.zeros(1, device="cuda"), torch.zeros(1, device="cuda", dtype=torch.half)
     Z.zero_muon_step(p, p, h, h, plan, Z.zero_muon_hparams(), result(), workspace(plan))
+
+
+def orth64(g):
+    """On the device, for large ones: the polynomial in 64 bits."""
+    x = g.double()
+    x = x / (torch.linalg.vector_norm(x) + EPS)
+    wide = x if x.shape[0] <= x.shape[1] else x.t().contiguous()
+    for _ in range(5):
+        s = wide.mm(wide.t().contiguous())
+        wide = A * wide + (B * s + C * s.mm(s)).mm(wide)
+    return wide if g.shape[0] <= g.shape[1] else wide.t().contiguous()
+
+
+@pytest.mark.parametrize("precise", [False, True])
+@pytest.mark.parametrize("shapes", [
+    [(2300, 2400)],                         # 256 wide tiles, none of a whole round: all cut
+    [(2300, 5000)],                         # in pairs (not in 32 bits)
+    [(3000, 2350), (2350, 3000)],
+    [(1500, 1700), (300, 260), (900, 2000), (64, 70)],   # one group for all, and a small one
+    [(5000, 4100)],                         # whole tiles and cut ones
+])
+def test_large_tiles(shapes, precise):
+    limit = TYPICAL if not precise else (2.0 ** -21 + math.sqrt(max(map(max, shapes))) * 2.0 ** -24) * \
+        (abs(B) + 2 * abs(C)) * math.sqrt(5) * 4
+    # the update is the gradient, in 32 bits and as the step takes it
+    g16 = [update(r, c, 5).cuda().half() for r, c in shapes]
+    want = [orth64(g) for g in g16]
+    outs = [torch.empty(g.shape, device="cuda") for g in g16]
+    plan = Z.zero_matrix_plan(g16, out=outs, precise=precise)
+    Z.zero_orthogonalize(plan, workspace(plan))
+    for o, w in zip(outs, want):
+        assert float((o.double() - w).norm()) <= limit * float(w.norm())
+    ends = [0]
+    for r, c in shapes:
+        ends.append(ends[-1] + r * c)
+    matrices = [(at, r, c) for at, (r, c) in zip(ends, shapes)]
+    grad = torch.cat([g.reshape(-1) for g in g16])
+    master, momentum = torch.ones(ends[-1], device="cuda"), torch.zeros(ends[-1], device="cuda")
+    p16 = torch.zeros(ends[-1], device="cuda", dtype=torch.half)
+    plan = Z.zero_muon_plan(matrices, precise=precise)
+    hp = Z.zero_muon_hparams(lr=2.0, weight_decay=0.0, nesterov=False, scaling=None)
+    Z.zero_muon_step(master, momentum, p16, grad, plan, hp, result(), workspace(plan))
+    for (at, r, c), w in zip(matrices, want):
+        o = (1.0 - master[at:at + r * c].double().view(r, c)) / 2
+        # the weights' own rounding: 2^-24 of at most 1 + 2 |w|, each
+        own = 2.0 ** -24 * (math.sqrt(r * c) + 2 * float(w.norm())) / 2
+        assert float((o - w).norm()) <= limit * float(w.norm()) + own
+    assert torch.equal(momentum, grad.float()) and torch.equal(p16, master.half())
