@@ -597,9 +597,14 @@ int zero_tensor_accumulate_norm(const zero_tensor_plan* plan, const void* table,
  *   A = X X^T,  X <- a X + (b A + c A A) X
  * on the wide form (G or its transpose, rows <= columns), transposed back.  A matrix of
  * zeros gives zeros; one that holds inf or NaN gives NaN.  The products are fp16 with
- * fp32 sums, the linear term a X has 22 bits; the result is off by up to 1.4e-3 of its
- * norm (3.4e-3 for a matrix of almost rank 1), and with `precise`, where every factor has
- * 22 bits, by 1e-6 to 1e-5 (3e-4).  With a shorter side of at most 64 all is in 32 bits or
+ * fp32 sums, the linear term a X has 22 bits.  With the usual coefficients the result is
+ * off, relative to its norm,
+ *   by 2e-4 to 1e-3 for a matrix of full rank, or with some percent of noise,
+ *   by up to 0.1 / sqrt(shorter side) for one of exactly or almost low rank or of few
+ *   distinct singular values (at 65 x 200 4e-3, at 1024 x 1024 1.5e-3; of one direction
+ *   9e-3 and 1e-3), and by up to 2e-2 for one whose entries are all alike,
+ * and with `precise`, where every factor has 22 bits, by 1e-6 to 1e-5, up to 5e-5 of low
+ * rank and 1e-3 of rank 1 to 4.  With a shorter side of at most 64 all is in 32 bits or
  * more.  The same call gives the same bits; in another list a matrix's sums may be cut
  * elsewhere, which changes the result within these errors. */
 

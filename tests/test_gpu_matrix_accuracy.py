@@ -1,0 +1,144 @@
+"""The errors that the header states for orthogonalisation, on the matrices where they are
+largest: of exactly and almost low rank, of two levels of singular values, of equal entries.
+
+Limits.  A step's planes are rounded entry by entry, half a step of fp16 at most; off the
+diagonals nothing makes up for it.  Independent roundings e of the entries of an m x m plane
+of 2-norm 1 and of X's rows are, over the directions that a matrix of rank r does have, an
+error of e sqrt(r / m) of the result, and over the m - r others one that later steps multiply by
+a each, of e / sqrt(m) or less: with e = 2^-11 / sqrt(3) (rms), |b| + 2 |c| = 8.8 and what two
+steps between make of it, 0.06 / sqrt(m) in all (one direction, whose roundings are fewest and
+weigh most: 0.08); two steps to a pass multiply planes once more, 0.1.  Entries that are all
+alike are all rounded alike: 2^-11 (|b| + 2 |c|) in a step and twice that with the next one's,
+2e-2 over five.  To 32 bits the same with 2^-21, and with X's own last bit, 2^-22 of the entries,
+which 485 times in the m directions that a matrix of low rank does not have is 485 2^-22 / sqrt(3)
+of what is there, and the fp32 sums' 2^-24 sqrt(n / 32) with it.
+"""
+import math
+
+import pytest
+import torch
+
+import zero_partitioned_mixed_shard_amd as Z
+
+pytestmark = pytest.mark.gpu
+
+
+def single(x):
+    return torch.tensor(x, dtype=torch.float32).double().item()
+
+
+A, B, C, EPS = single(3.4445), single(-4.7750), single(2.0315), single(1e-7)
+
+
+def orth64(g):
+    x = g.double()
+    x = x / (torch.linalg.vector_norm(x) + EPS)
+    wide = x if x.shape[0] <= x.shape[1] else x.t().contiguous()
+    for _ in range(5):
+        s = wide.mm(wide.t().contiguous())
+        wide = A * wide + (B * s + C * s.mm(s)).mm(wide)
+    return wide if g.shape[0] <= g.shape[1] else wide.t().contiguous()
+
+
+def of_rank(rows, cols, rank, gen, noise=0.0):
+    g = torch.randn(rows, rank, generator=gen, dtype=torch.float64) @ \
+        torch.randn(rank, cols, generator=gen, dtype=torch.float64)
+    return g / math.sqrt(rank) + noise * torch.randn(rows, cols, generator=gen, dtype=torch.float64)
+
+
+def of_levels(rows, cols, rank, level, gen):
+    """`rank` singular values of 1, the others of `level`."""
+    m, n = min(rows, cols), max(rows, cols)
+    u = torch.linalg.qr(torch.randn(m, m, generator=gen, dtype=torch.float64))[0]
+    v = torch.linalg.qr(torch.randn(n, m, generator=gen, dtype=torch.float64))[0]
+    s = torch.full((m,), level, dtype=torch.float64)
+    s[:rank] = 1.0
+    g = (u * s) @ v.t()
+    return g if rows <= cols else g.t().contiguous()
+
+
+def matrix(kind, rows, cols):
+    gen, m = torch.Generator().manual_seed(rows * 31 + cols), min(rows, cols)
+    if kind == "normal":
+        return torch.randn(rows, cols, generator=gen, dtype=torch.float64)
+    if kind == "noise":
+        return of_rank(rows, cols, max(1, m // 16), gen, 0.5)
+    if kind == "alike":
+        return torch.full((rows, cols), 0.37, dtype=torch.float64)
+    if kind == "one":
+        return of_rank(rows, cols, 1, gen)
+    if kind == "almost one":
+        return of_rank(rows, cols, 1, gen, 1e-3)
+    if kind == "two levels":
+        return of_levels(rows, cols, m // 2, 1e-3, gen)
+    return of_rank(rows, cols, max(2, m // int(kind)), gen)
+
+
+def error(g, precise, out=torch.float32, **kw):
+    y = torch.zeros(g.shape, dtype=out, device="cuda")
+    plan = Z.zero_matrix_plan([g], out=[y], precise=precise, **kw)
+    ws = torch.full((max(1, Z.zero_matrix_workspace_bytes(plan)),), 0xFF, dtype=torch.uint8, device="cuda")
+    Z.zero_orthogonalize(plan, ws)
+    want = orth64(g)
+    return float((y.double() - want).norm() / want.norm())
+
+
+def limits(kind, rows, cols):
+    """(in fp16 products, to 32 bits) of the header."""
+    m, n = min(rows, cols), max(rows, cols)
+    if kind in ("normal", "noise"):
+        return 2e-3, 1e-5
+    if kind == "alike":
+        return 2e-2, 1e-3
+    if kind in ("one", "almost one"):
+        return 0.08 / math.sqrt(m), 1e-3
+    return (0.1 if m >= 2048 and 2 * n >= 3 * m else 0.06) / math.sqrt(m), 5e-5
+
+
+KINDS = ["normal", "noise", "2", "4", "16", "one", "almost one", "two levels", "alike"]
+
+
+@pytest.mark.parametrize("rows,cols", [(65, 66), (65, 200), (512, 128), (256, 256), (300, 400), (512, 1376),
+                                       (768, 2100), (1024, 1024), (2800, 1040), (1500, 1700)])
+@pytest.mark.parametrize("kind", KINDS)
+def test_errors_are_as_stated(kind, rows, cols):
+    g = matrix(kind, rows, cols).float().cuda()
+    fast, precise = limits(kind, rows, cols)
+    assert error(g, False) <= fast
+    assert error(g, True) <= precise
+
+
+@pytest.mark.parametrize("kind", ["noise", "4", "16", "one", "alike"])
+def test_errors_of_two_steps_to_a_pass(kind):
+    rows, cols = 2048, 4096
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    if kind == "alike":
+        g = torch.full((rows, cols), 0.37, device="cuda")
+    else:
+        k = 1 if kind == "one" else 2048 // (16 if kind == "noise" else int(kind))
+        g = torch.randn(rows, k, device="cuda", generator=gen) @ torch.randn(k, cols, device="cuda", generator=gen)
+        if kind == "noise":
+            g = g / math.sqrt(k) + 0.5 * torch.randn(rows, cols, device="cuda", generator=gen)
+    fast, precise = limits(kind, rows, cols)
+    assert error(g, False) <= fast
+    assert error(g, True) <= precise
+
+
+def test_a_gradient_of_few_tokens():
+    """What a first step meets: the product of 48 tokens' activations and errors, in bf16, of
+    which the update is a multiple."""
+    rows, cols = 320, 768
+    gen = torch.Generator().manual_seed(5)
+    g = of_rank(rows, cols, 48, gen).bfloat16().cuda()
+    assert error(g, False) <= 0.06 / math.sqrt(320)
+    m = torch.zeros(rows * cols, device="cuda")
+    p = torch.zeros(rows * cols, device="cuda")
+    p16 = torch.zeros(rows * cols, device="cuda", dtype=torch.bfloat16)
+    plan = Z.zero_muon_plan([(0, rows, cols)])
+    ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    one = torch.zeros(4, dtype=torch.int32, device="cuda")
+    one.view(torch.float32)[3] = 1.0
+    hp = Z.zero_muon_hparams(lr=1.0, weight_decay=0.0, scaling=None)
+    Z.zero_muon_step(p, m, p16, g.reshape(-1), plan, hp, one, ws)
+    want = orth64(g)
+    assert float((-p.double().view(rows, cols) - want).norm()) <= 0.06 / math.sqrt(320) * float(want.norm())

@@ -27,11 +27,17 @@
 // multiplied by a in every step (485 times in 5 steps), and so would be the rounding of X:
 // the linear term a X takes both parts, the products hi alone, but for what is large on the
 // planes' diagonals: what these lose in rounding, and their product with lo, are added in
-// the tiles' ends to first order.  Relative error of the result (2-norm) against 64 bits:
-// 3e-4 to 1.4e-3 for normal matrices and for ones of low rank with 5 % of noise, up to
-// 3.4e-3 for ones of almost rank 1 (0.1 % of noise; without lo 0.12, in bf16 1).
+// the tiles' ends to first order.  Relative error of the result (2-norm) against 64 bits, for
+// the usual coefficients: 2e-4 to 1e-3 for matrices of full rank, or of low rank with some
+// percent of noise.  Where many directions have no part the planes are not near a multiple of
+// the identity, and the roundings off their diagonals count: up to 0.06 / sqrt(m) of exactly
+// or almost low rank or of two levels (3.6e-3 at 65 x 200, 1.4e-3 at 1024 x 1024), 0.08 of one
+// direction (8.5e-3 at 65 x 20000), 0.1 with two steps to a pass (1.6e-3 at 2048 x 4096).
+// Where all entries are alike so are their roundings: 7e-3, in pairs 1.6e-2.  Without lo a
+// matrix of almost rank 1 would be off by 0.12, in bf16 by 1.
 // With `precise` A, B and X have two parts and every product is hi hi + hi lo + lo hi, three
-// times the matrix work: 1e-6 to 1e-5, and up to 3e-4 for large ones of almost rank 1.
+// times the matrix work: 1e-6 to 1e-5, up to 5e-5 of low rank; of rank 1 to 4, whose result
+// is small beside what the other directions make of X's last bits, up to 7e-4 (8192 x 16384).
 
 #include <math.h>
 #include <string.h>
@@ -1217,8 +1223,8 @@ small_apply_kernel(Step s, Source src, MuonBufs mb, MuonConsts mc) {
 // ------------------------------------------------------------ host ---------
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
-// Matrices with a shorter side of at most kTogether take their steps in pairs, and are `many`
-// with so many tiles of 256 on and below their diagonals.
+// Matrices with a shorter side of at most kTogether are `many` with so many tiles of 256 on and
+// below their diagonals.
 constexpr int64_t kTogether = 1024, kMany = 480, kManyPrecise = 240;
 // The tile of a matrix's products, by its shorter side.
 // 256 wide ones do up to 1.7 times the work of 128 wide ones in the same time, which need
@@ -1230,16 +1236,21 @@ int tile_for(int64_t m, bool many) {
 }
 // Whether two steps go together: with Q = a + B, the second step's A is Q A Q and what
 // both do to X is Q' Q, 5 products of m x m (half computed) in the place of 2 and of one
-// of m x n by its transpose and one of m x m by m x n: fewer operations where n > m.  Of
-// the smaller matrices all go together, since their time is that of the launches.
-bool pairs_for(int64_t m, int64_t n) { return m <= kTogether || 2 * n >= 3 * m; }
+// of m x n by its transpose and one of m x m by m x n: fewer operations where n > m.  The
+// planes' roundings then go through four products and not two, and weigh 2 to 5 times as much
+// in a matrix of low rank, the more the smaller it is: 65 x 200 of rank 16 is off by 6.0e-3 in
+// pairs, 1040 x 2800 of rank 65 by 2.7e-3, 2048 x 4096 of rank 128 by 1.6e-3.
+constexpr int64_t kLeastPairs = 2048;
+bool pairs_for(int64_t m, int64_t n) { return m >= kLeastPairs && 2 * n >= 3 * m; }
 // A list of so few 128 wide tiles below the diagonals goes through the steps together, with
-// 128 wide tiles and in pairs: one matrix of 2048 x 2048 in 473 us and not 535, of 2048 x
-// 8192 in 781 and not 830, but two of 2048 x 2048 (272 tiles) in 819 and not 745.  In 32 bits
-// one of 1500 x 1500 (78 tiles) takes 568 us and not 591, one of 2048 x 5504 1840 and not
-// 1511.  Where the list would be several groups, one after the other, and is one round of
-// blocks together, too: 3 of 1500 x 1700 and 9 of 800 x 900 in 804 us and not 1121.
-constexpr int64_t kFew = 160, kFewPrecise = 80, kRound = 512;
+// 128 wide tiles (and in pairs where pairs_for says so of all): one matrix of 2048 x 2048 (136
+// tiles) in 390 us and not 525, of 2816 x 2816 (253) in 699 and not 837, two of 2048 x 2048
+// (272) in 685 and not 739, but one of 3000 x 3000 (300) in 1059 and not 942, two of 2304 x
+// 2304 (342) in 858 and not 822.  In 32 bits one of 1500 x 1500 (78) takes 558 us and not 579,
+// one of 1664 x 5504 (91) 1290 and not 1236, of 2048 x 5504 (136) 1846 and not 1506.  Where the
+// list would be several groups, one after the other, and is one round of blocks together, too: 3
+// of 1500 x 1700 and 9 of 800 x 900 in 717 us and not 1051, in 32 bits in 1688 and not 2010.
+constexpr int64_t kFew = 272, kFewPrecise = 80, kRound = 512;
 // Tiles below the diagonal of a group of matrices, and bytes of its planes, after
 // which the next matrix begins another group.
 constexpr int64_t kGroupTiles = 1024, kGroupBytes = int64_t(4) << 30;
@@ -1380,17 +1391,18 @@ struct Build {
         const bool many = tiles >= (precise ? kManyPrecise : kMany);
         // whether all of them go together
         int64_t tiles128 = 0;
-        bool kinds[4] = {false, false, false, false};
+        bool kinds[4] = {false, false, false, false}, pairs = !precise;
         for (const Mat& t : in) {
             if (t.m <= kSmall) continue;
             const int64_t q = up(t.m, 128) / 128;
             tiles128 += q * (q + 1) / 2;
             kinds[2 * (tile_for(t.m, many) == 256) + (!precise && pairs_for(t.m, t.n))] = true;
+            pairs = pairs && pairs_for(t.m, t.n);
         }
         const bool one = tiles128 <= (precise ? kFewPrecise : kFew) ||
                          (tiles128 <= kRound && kinds[0] + kinds[1] + kinds[2] + kinds[3] > 1);
         auto kind_of = [&](const Mat& t) {
-            return one ? (precise ? 0 : 1) : 2 * (tile_for(t.m, many) == 256) + (!precise && pairs_for(t.m, t.n));
+            return one ? (int)pairs : 2 * (tile_for(t.m, many) == 256) + (!precise && pairs_for(t.m, t.n));
         };
         std::vector<Mat> few;
         for (const Mat& t : in)
