@@ -604,7 +604,8 @@ int zero_tensor_accumulate_norm(const zero_tensor_plan* plan, const void* table,
  *   distinct singular values (at 65 x 200 4e-3, at 1024 x 1024 1.5e-3; of one direction
  *   9e-3 and 1e-3), and by up to 2e-2 for one whose entries are all alike,
  * and with `precise`, where every factor has 22 bits, by 1e-6 to 1e-5, up to 5e-5 of low
- * rank and 1e-3 of rank 1 to 4.  With a shorter side of at most 64 all is in 32 bits or
+ * rank and 1e-3 of rank 1 to 4.  (fp16 results can hold more than the first: ask for
+ * `precise` there, as the Python plan does.)  With a shorter side of at most 64 all is in 32 bits or
  * more.  The same call gives the same bits; in another list a matrix's sums may be cut
  * elsewhere, which changes the result within these errors. */
 

@@ -142,3 +142,24 @@ def test_a_gradient_of_few_tokens():
     Z.zero_muon_step(p, m, p16, g.reshape(-1), plan, hp, one, ws)
     want = orth64(g)
     assert float((-p.double().view(rows, cols) - want).norm()) <= 0.06 / math.sqrt(320) * float(want.norm())
+
+
+@pytest.mark.parametrize("kind", ["normal", "noise", "4", "two levels"])
+@pytest.mark.parametrize("rows,cols", [(65, 200), (300, 400), (1024, 700), (1500, 1700)])
+def test_float16_results_are_off_by_their_rounding(kind, rows, cols):
+    """A rounding is off by at most half of 2^-10 of its binade's first value, evenly spread: in the
+    2-norm by 2^-10 / sqrt(12) of the result, and the products' 5e-5 beside it."""
+    g = matrix(kind, rows, cols).half().cuda()
+    assert error(g, None, torch.float16) <= 2.0 ** -10 / math.sqrt(12) + 5e-5
+
+
+def test_who_takes_two_parts():
+    g = torch.ones(70, 80, device="cuda")
+    half, bf, f32 = (torch.empty(70, 80, device="cuda", dtype=t) for t in
+                     (torch.float16, torch.bfloat16, torch.float32))
+    for outs, precise, want in (([half], None, (False, 2)), ([bf], None, (False, 1)), ([f32], None, (True, 2)),
+                                ([half, bf], None, (False, 2)), ([half], False, (False, 1)),
+                                ([half], True, (True, 2)), ([f32], False, (False, 1))):
+        plan = Z.zero_matrix_plan([g] * len(outs), out=outs, precise=precise)
+        assert (plan.precise, plan.parts) == want and plan.c.precise == plan.parts - 1
+    assert Z.zero_muon_plan([(0, 70, 80)]).parts == 1 and Z.zero_muon_plan([(0, 70, 80)], precise=True).parts == 2

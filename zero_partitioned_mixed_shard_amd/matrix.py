@@ -60,6 +60,7 @@ class _Plan:
         self._host = np.zeros(self.c.table_bytes, dtype=np.uint8)
         _check(table(list_p, ctypes.byref(self.c), self._host.ctypes.data), table.__name__)
         self.device, self.precise = device, bool(precise)
+        self.parts = 2 if precise else 1        # fp16 parts of a product's factors
         self.n_matrices, self.numel, self.extent = n, self.c.numel, self.c.extent
         self.workspace_bytes = int(self.c.workspace_bytes)
         with torch.cuda.device(device):
@@ -109,7 +110,10 @@ class zero_matrix_plan(_Plan):
               types; None: the tensors themselves.  A matrix with consecutive rows needs
               a result with consecutive rows, a transposed one a transposed one.
     precise   results to 32 bits, at three times the matrix work; None: where some
-              result is float32
+              result is float32.  Of float16 results, whose own rounding (2e-4) is finer
+              than the faster products' (2e-4 to 1e-3, of low rank more), None takes the
+              same products (`parts` is 2 then, `precise` False); False leaves them to
+              the faster ones
     device    by default the tensors' (needed for an empty list)
 
     The plan keeps the tensors and holds their addresses.  Results that overlap each
@@ -159,11 +163,14 @@ class zero_matrix_plan(_Plan):
                 lds = (cols, cols)
             entries[k] = (t.data_ptr(), y.data_ptr(), rows, cols, *lds, types[t.dtype],
                           types[y.dtype])
+        two = precise
         if precise is None:
             precise = any(y.dtype == torch.float32 for y in outs)
+            two = precise or any(y.dtype == torch.float16 for y in outs)
         self.tensors, self.out = tensors, outs
-        self._build(entries.ctypes.data, len(tensors), precise, device, _lib.zero_matrix_plan_init,
+        self._build(entries.ctypes.data, len(tensors), two, device, _lib.zero_matrix_plan_init,
                     _lib.zero_matrix_plan_table)
+        self.precise = bool(precise)
 
 
 def _rows(t) -> set:
