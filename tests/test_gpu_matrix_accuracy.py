@@ -163,3 +163,31 @@ def test_who_takes_two_parts():
         plan = Z.zero_matrix_plan([g] * len(outs), out=outs, precise=precise)
         assert (plan.precise, plan.parts) == want and plan.c.precise == plan.parts - 1
     assert Z.zero_muon_plan([(0, 70, 80)]).parts == 1 and Z.zero_muon_plan([(0, 70, 80)], precise=True).parts == 2
+
+
+@pytest.mark.parametrize("rows,cols,kind", [(65, 200000, "normal"), (200000, 130, "normal"), (130, 100000, "alike"),
+                                            (1100, 70000, "normal"), (70, 4000000, "alike"), (4000000, 65, "normal")])
+def test_long_sums(rows, cols, kind):
+    """A's diagonal is a sum of as many positive terms as there are columns: in chains of at
+    most 1024 fp32 sums, or 3 times as many, and these added up, its error does not grow with them."""
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    g = torch.full((rows, cols), 0.37, device="cuda") if kind == "alike" else \
+        torch.randn(rows, cols, device="cuda", generator=gen)
+    fast, precise = limits(kind, rows, cols)
+    assert error(g, False) <= fast
+    assert error(g, True) <= precise
+
+
+def test_long_ones_among_others():
+    """A long matrix is a group of its own, whatever is beside it."""
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    shapes = [(200, 300), (66, 40000), (20, 50000), (33000, 70), (1030, 200), (90, 32768), (90, 32769)]
+    g = [torch.randn(s, device="cuda", generator=gen) for s in shapes]
+    for precise in (False, True):
+        out = [torch.zeros_like(x) for x in g]
+        plan = Z.zero_matrix_plan(g, out=out, precise=precise)
+        ws = torch.full((plan.workspace_bytes,), 0xFF, dtype=torch.uint8, device="cuda")
+        Z.zero_orthogonalize(plan, ws)
+        for x, y in zip(g, out):
+            want = orth64(x)
+            assert float((y.double() - want).norm()) <= limits("normal", *x.shape)[precise] * float(want.norm())

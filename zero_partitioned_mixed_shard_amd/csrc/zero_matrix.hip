@@ -1276,6 +1276,12 @@ Cut cut_for(int64_t n, int tile, int64_t stages) {
     return best;
 }
 
+// Columns whose products are added up in one chain of fp32 sums (1024 of them, each of 32
+// products, three times as many in 32 bits): of a longer matrix, which is a group of its own,
+// every tile of A is cut.  In one chain, or 16, all entries of 70 x 4000000 alike left the result
+// 1.8e-3 off in 32 bits.
+constexpr int64_t kMostDepth = 32768;
+
 struct Build {
     std::vector<Group> groups;
     std::vector<Mat> mats;
@@ -1339,6 +1345,10 @@ struct Build {
         }
         const int64_t thrice = precise ? 3 : 1;
         g.gram = cut_for(g.n_tri, tile, thrice * short_n / kBK);
+        if (short_n > kMostDepth) {
+            const int64_t parts = thrice * ((short_n + kMostDepth - 1) / kMostDepth);
+            g.gram = {0, (int32_t)std::max<int64_t>(parts, g.gram.whole == 0 ? g.gram.parts : 1), 0};
+        }
         g.square = cut_for(g.n_tri, tile, thrice * short_m / kBK);
         g.apply = cut_for(g.n_full, tile, thrice * short_m / kBK);
         int64_t sums = 0;
@@ -1346,7 +1356,9 @@ struct Build {
                               std::make_pair(g.apply, g.n_full)})
             if (c.first.parts > 1) sums = std::max(sums, (c.second - c.first.whole) * c.first.parts);
         ws = std::max(ws, up(at + sums * tile * tile * 4, 256));
-        if (g.n_units > kMaxLaunchBlocks || g.n_full > kMaxLaunchBlocks) return false;
+        if (g.n_units > kMaxLaunchBlocks || g.n_full > kMaxLaunchBlocks ||
+            (g.n_tri - g.gram.whole) * g.gram.parts > kMaxLaunchBlocks)
+            return false;
         mats.insert(mats.end(), v.begin(), v.end());
         groups.push_back(g);
         return true;
@@ -1417,6 +1429,10 @@ struct Build {
                 if (t.m <= kSmall || kind_of(t) != kind) continue;
                 t.mp = (int32_t)up(t.m, tile), t.np = (int32_t)up(t.n, tile);
                 const int64_t q = t.mp / tile;
+                if (t.np > kMostDepth) {
+                    if (!add(&t, 1, tile, pairs, precise)) return ZERO_ERANGE;
+                    continue;
+                }
                 v.push_back(t);
                 tiles += q * (q + 1) / 2;
                 bytes += 8 * (int64_t)t.mp * t.np + 8 * (int64_t)t.mp * t.mp;
