@@ -191,3 +191,16 @@ def test_long_ones_among_others():
         for x, y in zip(g, out):
             want = orth64(x)
             assert float((y.double() - want).norm()) <= limits("normal", *x.shape)[precise] * float(want.norm())
+
+
+@pytest.mark.parametrize("rows,cols", [(16, 300), (64, 40000), (3000, 30), (70, 300), (500, 400)])
+@pytest.mark.parametrize("largest", [3.3e38, 2.0 ** 100, 2.0 ** 60])
+def test_values_at_the_end_of_the_range(rows, cols, largest):
+    """The norm is beyond fp32's range, or its reciprocal subnormal; the result is what it is for
+    any other multiple of the matrix."""
+    g = matrix("normal", rows, cols)
+    g = (g * (largest / float(g.abs().max()))).float().cuda()
+    assert bool(g.isfinite().all())
+    assert error(g, True) <= limits("normal", rows, cols)[1]
+    if min(rows, cols) > 64:
+        assert error(g, False) <= limits("normal", rows, cols)[0]

@@ -319,6 +319,15 @@ matrix_norm_kernel(Step s, Source src) {
         ((double*)(s.ws + s.part_off))[idx] = (part[0] + part[1]) + (part[2] + part[3]);
 }
 
+// A factor of a matrix's elements as two, the first a power of two: of a norm near the end of
+// fp32's range or beyond it the factor itself would be subnormal, and lose bits.  (v * 2^-64 is
+// exact, or of an element that is 0 beside the norm.)
+__device__ __forceinline__ void store_factor(float* to, double by) {
+    const bool large = by < 0x1p-64;
+    to[0] = large ? 0x1p-64f : 1.0f;
+    to[1] = (float)(large ? by * 0x1p64 : by);
+}
+
 // One block per matrix: its factor kScaleX / (norm + eps), the partials in order.
 __global__ void __launch_bounds__(kThreads)
 matrix_factor_kernel(Step s, float eps) {
@@ -334,7 +343,7 @@ matrix_factor_kernel(Step s, float eps) {
     __syncthreads();
     if (threadIdx.x == 0) {
         const double norm = sqrt((part[0] + part[1]) + (part[2] + part[3]));
-        ((float*)(s.ws + s.inv_off))[blockIdx.x] = (float)((double)kScaleX / (norm + (double)eps));
+        store_factor((float*)(s.ws + s.inv_off) + 2 * blockIdx.x, (double)kScaleX / (norm + (double)eps));
     }
 }
 
@@ -355,7 +364,8 @@ matrix_init_kernel(Step s, int64_t mat0, Source src) {
     __shared__ float turn[kUnitN * (kUnitM + 1)];
     const Item it = s.items[item_of<8>(blockIdx.x, s.n_items)];
     const Mat t = s.mats[it.mat];
-    const float inv = ((const float*)(s.ws + s.inv_off))[it.mat - mat0];
+    const float* inv = (const float*)(s.ws + s.inv_off) + 2 * (it.mat - mat0);
+    const float inv0 = inv[0], inv1 = inv[1];
     f16* x = (f16*)(s.ws + t.x[0]);
     const int64_t lower = t.plane_x / 2;
     float v[kQuarters][8];
@@ -390,7 +400,7 @@ matrix_init_kernel(Step s, int64_t mat0, Source src) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             f16 h, l;
-            split(v[q][e] * inv, h, l);
+            split(v[q][e] * inv0 * inv1, h, l);
             hi[e] = h;
             lo[e] = l;
         }
@@ -1013,9 +1023,10 @@ __device__ __forceinline__ bool small_item(const Mat& t, int q, int64_t c0, int&
     return i < t.m;
 }
 // A chunk of the update into LDS: by column (to[k * LD + i]), or by row (to[i * LD + k]),
-// times `by`.
+// times `by0` times `by1`.
 template <bool FIRST, bool BY_COLUMN, typename Source>
-__device__ __forceinline__ void small_load(const Mat& t, const Source& src, int64_t c0, float by, float* to) {
+__device__ __forceinline__ void small_load(const Mat& t, const Source& src, int64_t c0, float by0, float by1,
+                                           float* to) {
     for (int q = threadIdx.x;; q += kThreads) {
         int i, k, n;
         if (!small_item(t, q, c0, i, k, n)) break;
@@ -1029,7 +1040,7 @@ __device__ __forceinline__ void small_load(const Mat& t, const Source& src, int6
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const int ii = t.tall ? i + e : i, kk = t.tall ? k : k + e;
-            if (ii < kSmall) to[BY_COLUMN ? kk * kSmallLd + ii : ii * kSmallRow + kk] = v[e] * by;
+            if (ii < kSmall) to[BY_COLUMN ? kk * kSmallLd + ii : ii * kSmallRow + kk] = v[e] * by0 * by1;
         }
     }
 }
@@ -1055,7 +1066,7 @@ small_gram_kernel(Step s, Source src) {
     for (int e = 0; e < 16; ++e) acc[e] = 0.0;
     const int64_t end = (int64_t)(it.i + 1) * t.np < t.n ? (int64_t)(it.i + 1) * t.np : t.n;
     for (int64_t c0 = (int64_t)it.i * t.np; c0 < end; c0 += kSmallCols) {
-        small_load<true, true>(t, src, c0, 1.0f, u);
+        small_load<true, true>(t, src, c0, 1.0f, 1.0f, u);
         __syncthreads();
         if (slice < slices) {
             for (int k = slice; k < kSmallCols; k += slices) {
@@ -1108,7 +1119,7 @@ __device__ __forceinline__ void small_steps(const Step& s, const SmallNs& ns, co
         double sum = 0.0;
         for (int k = 0; k < t.m; ++k) sum += A[k * kLd + k];
         *norm = sqrt(sum) + ns.eps;
-        ((float*)(s.ws + t.r[0]))[0] = (float)(1.0 / *norm);
+        store_factor((float*)(s.ws + t.r[0]), 1.0 / *norm);
     }
     __syncthreads();
     double c[R * R];
@@ -1177,14 +1188,14 @@ small_apply_kernel(Step s, Source src, MuonBufs mb, MuonConsts mc) {
     const Item it = s.items[blockIdx.x];
     const Mat t = s.mats[it.mat];
     const int side = (t.m + 3) / 4;
-    const float inv = ((const float*)(s.ws + t.r[0]))[0];
+    const float inv[2] = {((const float*)(s.ws + t.r[0]))[0], ((const float*)(s.ws + t.r[0]))[1]};
     for (int e = threadIdx.x; e < side * 4 * kSmall; e += kThreads) P[e] = ((const float*)(s.ws + t.p[1]))[e];
     for (int e = threadIdx.x; e < kSmall * kSmallRow; e += kThreads) u[e] = 0.0f;
     __syncthreads();
     const float step = MUON ? muon_step(t, mc) : 0.0f;
     const int64_t end = (int64_t)(it.i + 1) * t.np < t.n ? (int64_t)(it.i + 1) * t.np : t.n;
     for (int64_t c0 = (int64_t)it.i * t.np; c0 < end; c0 += kSmallCols) {
-        small_load<false, false>(t, src, c0, inv, u);
+        small_load<false, false>(t, src, c0, inv[0], inv[1], u);
         __syncthreads();
         for (int q = threadIdx.x; q < side * (kSmallCols / 4); q += kThreads) {
             const int i = q / (kSmallCols / 4) * 4, k = q % (kSmallCols / 4) * 4;
@@ -1312,7 +1323,7 @@ struct Build {
             t.part0 = parts, t.n_parts = (int32_t)u;
             parts += u;
         }
-        g.inv_off = at, at = up(at + 4 * count, 256);
+        g.inv_off = at, at = up(at + 8 * count, 256);
         g.part_off = at, at = up(at + 8 * parts, 256);
         g.sums_off = at;
         g.unit0 = (int64_t)items.size();
@@ -1378,7 +1389,7 @@ struct Build {
             t.n_parts = (int32_t)((chunks + per - 1) / per);
             t.p[0] = at, at = up(at + t.n_parts * side * side * 128, 256);
             t.p[1] = at, at = up(at + side * 4 * kSmall * 4, 256);
-            t.r[0] = at, at = up(at + 4, 256);
+            t.r[0] = at, at = up(at + 8, 256);
             for (int64_t k = 0; k < t.n_parts; ++k) item((int64_t)mats.size(), k, 0);
             mats.push_back(t);
         }
