@@ -1,0 +1,104 @@
+"""The Muon step, alone and in ShardStep, against its definition in 64 bits, in limits that a step
+without decay, of the other momentum or 5 % too long or short would miss.
+
+Limits.  An update to 32 bits is off by at most 5e-5 of its norm (the header's, for these
+matrices; of shorter sides up to 64 by the 24 bits of its factors, amplified by at most 3.45
+a step), of one fp16 part by 2e-3; a weight's step is two products and a difference in fp32,
+each off by 2^-24 of its operands.
+"""
+import math
+import struct
+
+import numpy as np
+import pytest
+import torch
+
+import zero_partitioned_mixed_shard_amd as Z
+from zero_partitioned_mixed_shard_amd.shard import ShardStep
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"fp16": torch.float16, "bf16": torch.bfloat16}
+
+
+def single(x):
+    return float(np.float32(x))
+
+
+A, B, C, EPS = single(3.4445), single(-4.7750), single(2.0315), single(1e-7)
+
+
+def orth64(g):
+    x = g.double()
+    x = x / (x.norm() + EPS)
+    wide = x if x.shape[0] <= x.shape[1] else x.t()
+    for _ in range(5):
+        s = wide @ wide.t()
+        wide = A * wide + (B * s + C * s @ s) @ wide
+    return wide if g.shape[0] <= g.shape[1] else wide.t()
+
+
+def gradient(rows, cols, gen):
+    """A part of low rank and noise."""
+    k = max(1, min(rows, cols) // 8)
+    return torch.randn(rows, k, generator=gen) @ torch.randn(k, cols, generator=gen) / math.sqrt(k) + \
+        0.5 * torch.randn(rows, cols, generator=gen)
+
+
+SHAPES = [(64, 200), (300, 130), (1, 50), (40, 1), (257, 257), (129, 1025), (1100, 300)]
+
+
+def flat(seed, dtype, gap=5):
+    """(matrices, master, momentum, gradient) with odd offsets and gaps."""
+    gen, matrices, at = torch.Generator().manual_seed(seed), [], 3
+    for r, c in SHAPES:
+        matrices.append((at, r, c))
+        at += r * c + gap
+    p, m, g = torch.randn(at, generator=gen) * 0.02, torch.zeros(at), torch.zeros(at)
+    for o, r, c in matrices:
+        m[o:o + r * c] = gradient(r, c, gen).reshape(-1) * 3e-3
+        g[o:o + r * c] = gradient(r, c, gen).reshape(-1) * 1e-3
+    return matrices, p, m, (g * 64).to(TYPES[dtype])
+
+
+def reference(p, m, g, matrices, hp, inv, coef, **change):
+    """(p, m) in 64 bits; change: nesterov, decay or a factor of the step, as a mistake would."""
+    p, m, g = p.double().clone(), m.double().clone(), g.double()
+    for o, r, c in matrices:
+        s = slice(o, o + r * c)
+        gg = g[s] * inv * coef
+        m[s] = hp.momentum * m[s] + gg
+        u = gg + hp.momentum * m[s] if change.get("nesterov", hp.nesterov) else m[s]
+        alpha = {0: 1.0, 1: math.sqrt(max(1.0, r / c)), 2: 0.2 * math.sqrt(max(r, c))}[hp.scaling]
+        o64 = orth64(u.view(r, c)).reshape(-1)
+        p[s] = p[s] * (1.0 - hp.lr * change.get("decay", hp.weight_decay)) - \
+            hp.lr * alpha * change.get("factor", 1.0) * o64
+    return p, m
+
+
+def step_limit(p, o, s, hp, precise):
+    """Of the 2-norm of a matrix's weights after the step."""
+    r, c = s
+    update = hp.lr * {0: 1.0, 1: math.sqrt(max(1.0, r / c)), 2: 0.2 * math.sqrt(max(r, c))}[hp.scaling] * o
+    own = 3.45 ** 5 * 2.0 ** -22 if min(r, c) <= 64 else 5e-5 if precise else 2e-3
+    return own * update + 2.0 ** -23 * (p + update)
+
+
+def result(sumsq, overflow=0, inv=1.0):
+    return torch.frombuffer(bytearray(struct.pack("<dIf", sumsq, overflow, inv)), dtype=torch.int32).cuda()
+
+
+def test_shard_step_takes_32_bits_on_request():
+    o, r, c = 0, 200, 260
+    start = (torch.randn(r * c, generator=torch.Generator().manual_seed(1)) * 0.02).half()
+    grad = (gradient(r, c, torch.Generator().manual_seed(2)) * 0.05).half().reshape(-1)
+    off = []
+    for precise in (False, True):
+        st = ShardStep(0, r * c, [(0, r * c)], Z.ZERO_FP16, lr=0.01, matrices=[(o, r, c)], muon_precise=precise)
+        assert st.muon_plan.precise == precise
+        st.load_param16(start.cuda())
+        assert st.step([grad.cuda()]).applied
+        want, _ = reference(start, torch.zeros(r * c), grad, [(o, r, c)], st.muon_hp, 1.0, 1.0)
+        update = float((want - start.double() * (1 - st.muon_hp.lr * st.muon_hp.weight_decay)).norm())
+        off.append(float((st.master.double().cpu() - want).norm()) / update)
+    assert off[0] <= 2e-3 and off[1] <= 1e-5

@@ -189,10 +189,12 @@ class ShardStep:
                  min_gap: int = 0, device_control: bool = False, placement: str = "interleaved",
                  arena_slack: int = 0, batched: bool = True, rank_layout: str = "flat",
                  matrices: Sequence[Tuple[int, int, int]] = (),
-                 muon: Optional[zero_muon_hparams] = None, device="cuda"):
+                 muon: Optional[zero_muon_hparams] = None, device="cuda",
+                 muon_precise: bool = False):
         """matrices: (flat offset, rows, cols) of the tensors that take Muon steps, each inside
         one owner's range; muon: their hyper-parameters (by default lr, weight_decay and
-        max_grad_norm as given here)."""
+        max_grad_norm as given here); muon_precise: updates to 32 bits, at three times the
+        matrix work (zero_muon_plan's precise)."""
         self.begin, self.end = begin, end
         self.count = end - begin
         self.owners = [(a - begin, b - begin) for a, b in owners]
@@ -239,7 +241,7 @@ class ShardStep:
         if batched and (len(self._reduce_list) > 1 or rank_layout == "bucket"):
             ws = max(ws, zero_range_workspace_bytes(self._reduce_list))
         self.workspace = torch.empty((ws + 7) // 8, dtype=torch.float64, device=device)
-        self._matrices(matrices, muon, lr, weight_decay, max_grad_norm, device)
+        self._matrices(matrices, muon, muon_precise, lr, weight_decay, max_grad_norm, device)
         self.placement = placement if arena else "separate"
         self.placement_ms = {}                  # first stage: one timed step per candidate
         self.placement_finalists_ms = {}        # second stage: median of three, six fastest
@@ -253,7 +255,7 @@ class ShardStep:
             self.ctl = control_to_device(zero_step_control_init(
                 scale0, min_scale, window, float(divisor), beta1, beta2), device=device)
 
-    def _matrices(self, matrices, muon, lr, weight_decay, max_grad_norm, device) -> None:
+    def _matrices(self, matrices, muon, precise, lr, weight_decay, max_grad_norm, device) -> None:
         """The plan of the Muon steps, and AdamW's ranges without them."""
         self.muon_plan = None
         self._adamw_list = self._owner_list
@@ -273,7 +275,7 @@ class ShardStep:
         if sum(r * c for _, r, c in at) + sum(n for _, n in rest) != sum(b - a for a, b in self.owners):
             raise ValueError("matrices overlap, or lie outside the owners' ranges")
         self._adamw_list = [(a, n) for a, n in rest if n > 0]
-        self.muon_plan = zero_muon_plan(at, device=device)
+        self.muon_plan = zero_muon_plan(at, precise=precise, device=device)
         self.muon_hp = zero_muon_hparams(lr=lr, weight_decay=weight_decay, max_grad_norm=max_grad_norm) \
             if muon is None else muon
         self.muon_workspace = torch.empty(max(1, zero_matrix_workspace_bytes(self.muon_plan)),
