@@ -102,3 +102,73 @@ def test_shard_step_takes_32_bits_on_request():
         update = float((want - start.double() * (1 - st.muon_hp.lr * st.muon_hp.weight_decay)).norm())
         off.append(float((st.master.double().cpu() - want).norm()) / update)
     assert off[0] <= 2e-3 and off[1] <= 1e-5
+
+
+def test_shard_step_clips_matrices_and_the_rest_alike():
+    """A clip given to the step, none to muon: the matrices take it too.  The momentum after the
+    first step is the clipped gradient, element by element."""
+    rows, cols, rest = 40, 70, 500
+    n = rows * cols + rest
+    gen = torch.Generator().manual_seed(3)
+    start = (torch.randn(n, generator=gen) * 0.02).half()
+    grad = (torch.randn(n, generator=gen) * 0.1).half()
+    clip = 0.25
+    coef = clip / (float(grad.double().norm()) + 1e-6)
+    assert coef < 0.1
+    muon = Z.zero_muon_hparams(lr=0.01, weight_decay=0.1)
+    st = ShardStep(0, n, [(0, n)], Z.ZERO_FP16, lr=0.01, weight_decay=0.1, max_grad_norm=clip,
+                   matrices=[(0, rows, cols)], muon=muon)
+    assert st.muon_hp is muon and muon.max_grad_norm == 0
+    st.load_param16(start.cuda())
+    assert st.step([grad.cuda()]).applied
+    g = grad.double() * coef
+    got = st.exp_avg.double().cpu()
+    inside, beta1 = slice(0, rows * cols), single(0.9)
+    # two products, the coefficient's own rounding, and AdamW's (1 - beta1)
+    assert bool(((got - g)[inside].abs() <= 4 * 2.0 ** -24 * g[inside].abs() + 1e-45).all())
+    assert bool(((got - (1 - beta1) * g)[rows * cols:].abs() <= 2.0 ** -20 * g[rows * cols:].abs()).all())
+    want, _ = reference(start, torch.zeros(n), grad, [(0, rows, cols)], muon, 1.0, coef)
+    o = float(orth64(g[inside].view(rows, cols)).norm())
+    off = float((st.master.double().cpu() - want)[inside].norm())
+    assert off <= step_limit(float(start.double()[inside].norm()), o, (rows, cols), muon, False)
+    # the clip follows the step's own, and the learning rate muon's
+    before, st.hp.max_grad_norm, muon.lr, muon.weight_decay = st.exp_avg.clone(), 0.0, 0.0, 0.0
+    master = st.master.clone()
+    assert st.step([grad.cuda()]).applied
+    want = single(0.95) * before.double().cpu()[inside] + grad.double()[inside]
+    assert bool(((st.exp_avg.double().cpu()[inside] - want).abs() <= 2.0 ** -22 * (want.abs() + grad.double()[inside].abs())).all())
+    assert torch.equal(st.master[inside], master[inside])
+
+
+def test_two_clips_are_refused():
+    kw = dict(matrices=[(0, 8, 9)])
+    for step_clip, muon_clip in ((1.0, 0.5), (0.0, 1.0)):
+        with pytest.raises(ValueError, match="clip"):
+            ShardStep(0, 72, [(0, 72)], Z.ZERO_FP16, max_grad_norm=step_clip,
+                      muon=Z.zero_muon_hparams(max_grad_norm=muon_clip), **kw)
+    for step_clip, muon_clip in ((1.0, 1.0), (0.1, 0.1), (1.0, 0.0), (0.0, 0.0), (0.0, -1.0)):
+        ShardStep(0, 72, [(0, 72)], Z.ZERO_FP16, max_grad_norm=step_clip,
+                  muon=Z.zero_muon_hparams(max_grad_norm=muon_clip), **kw)
+
+
+def test_captured_step_clips():
+    """Captured and replayed, the clip is the capture's; with an active one every replay is the
+    eager step's."""
+    matrices, p, m, g = flat(4, "bf16")
+    n = p.numel()
+    kw = dict(lr=0.01, max_grad_norm=0.01, matrices=matrices, device_control=True, own_ranks=True, world=1)
+    steps = [ShardStep(0, n, [(0, n)], Z.ZERO_BF16, muon=Z.zero_muon_hparams(lr=0.01), **kw) for _ in range(2)]
+    for st in steps:
+        st.load_param16(p.bfloat16().cuda())
+        st.rank_bufs[0].copy_(g)
+    graph = steps[0].capture()
+    for k in range(3):
+        for st in steps:
+            st.rank_bufs[0].copy_(g * (k + 1))
+        graph.replay()
+        torch.cuda.synchronize()
+        steps[1].step()
+        for x, y in zip((steps[0].master, steps[0].exp_avg, steps[0].param16),
+                        (steps[1].master, steps[1].exp_avg, steps[1].param16)):
+            assert torch.equal(x, y), k
+    assert float((steps[1].exp_avg[matrices[1][0]:matrices[2][0]]).norm()) < 0.05

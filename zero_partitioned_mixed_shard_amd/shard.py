@@ -22,7 +22,8 @@ call per window and per owner.
 With `matrices` (whole tensors of two dimensions, as round-robin ownership gives them) the
 step is Muon's there and AdamW's in the rest of every owner's range: one
 zero_adamw_step_ranges call, then one zero_muon_step call, both with the same
-result.  The momentum is exp_avg; exp_avg_sq is not used there.
+result and the same clip.  The momentum is exp_avg; exp_avg_sq, which has the flat buffer's
+offsets as all of them do, is not used there.
 
 With fused=False the reduce and the check are separate calls
 (zero_reduce_owned per window, then zero_unscale_check_norm per owner).
@@ -192,8 +193,10 @@ class ShardStep:
                  muon: Optional[zero_muon_hparams] = None, device="cuda",
                  muon_precise: bool = False):
         """matrices: (flat offset, rows, cols) of the tensors that take Muon steps, each inside
-        one owner's range; muon: their hyper-parameters (by default lr, weight_decay and
-        max_grad_norm as given here); muon_precise: updates to 32 bits, at three times the
+        one owner's range; muon: their hyper-parameters (by default lr and weight_decay as given
+        here; a schedule of the learning rate sets hp.lr and muon_hp.lr).  The clip is of the
+        whole gradient, so it is hp.max_grad_norm for all steps: muon's own may be left 0 or has
+        to be the same.  muon_precise: updates to 32 bits, at three times the
         matrix work (zero_muon_plan's precise)."""
         self.begin, self.end = begin, end
         self.count = end - begin
@@ -278,6 +281,8 @@ class ShardStep:
         self.muon_plan = zero_muon_plan(at, precise=precise, device=device)
         self.muon_hp = zero_muon_hparams(lr=lr, weight_decay=weight_decay, max_grad_norm=max_grad_norm) \
             if muon is None else muon
+        if self.muon_hp.max_grad_norm > 0 and self.muon_hp.max_grad_norm != self.hp.max_grad_norm:
+            raise ValueError("muon's max_grad_norm is not the step's: one gradient has one clip")
         self.muon_workspace = torch.empty(max(1, zero_matrix_workspace_bytes(self.muon_plan)),
                                           dtype=torch.uint8, device=device)
 
@@ -530,7 +535,9 @@ class ShardStep:
             if self._adamw_list:
                 zero_adamw_step_ranges(self.master, self.exp_avg, self.exp_avg_sq, self.param16, red,
                                        self._adamw_list, self.hp, self.res, ctl_dev=ctl)
-            zero_muon_step(self.master, self.exp_avg, self.param16, red, self.muon_plan, self.muon_hp,
+            muon = type(self.muon_hp).from_buffer_copy(self.muon_hp)
+            muon.max_grad_norm = self.hp.max_grad_norm
+            zero_muon_step(self.master, self.exp_avg, self.param16, red, self.muon_plan, muon,
                            self.res, self.muon_workspace)
         elif self.batched and len(self._owner_list) > 1:
             zero_adamw_step_ranges(self.master, self.exp_avg, self.exp_avg_sq, self.param16, red,
