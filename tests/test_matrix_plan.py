@@ -256,3 +256,35 @@ def test_accumulators_stay_in_place(tmp_path):
             bad.append((name, line.strip()))
     assert len(kernels) == 28 and products >= 28 * 64
     assert not bad, bad[:5]
+
+
+def test_a_plans_table_stays_for_torchs_streams(monkeypatch):
+    """A plan that is dropped while a call on another stream runs: the table's memory waits for
+    that stream.  torch's own streams are recorded, once each; a caller's, which may be gone by
+    then, are not."""
+    import contextlib
+    from types import SimpleNamespace as NS
+
+    import torch
+
+    dev = torch.device("cuda", 0)
+
+    def stream(handle, stream_id):
+        return NS(device=dev, cuda_stream=handle, stream_id=stream_id)
+
+    default, pool, other, external = stream(0, 0), stream(0x5000, 35), stream(0x5100, 67), stream(0x6000, 0x6000)
+    current, seen, ran = [default], [], []
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: current[0])
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda d=None: default)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    for kind in (Z.zero_matrix_plan, Z.zero_muon_plan):
+        plan = object.__new__(kind)
+        plan.device, plan._streams = dev, {0x4000}
+        plan.table = NS(record_stream=lambda s: seen.append(s.cuda_stream))
+        seen.clear(), ran.clear()
+        for s, now in ((None, default), (pool, default), (0x5000, default), (None, other), (external, default),
+                       (None, external), (0x7000, default), (0, pool), (default, pool)):
+            current[0] = now
+            plan._call(lambda raw: ran.append(raw) or 0, (), s)
+        assert ran == [0, 0x5000, 0x5000, 0x5100, 0x6000, 0x6000, 0x7000, 0, 0]
+        assert seen == [0, 0x5000, 0x5100]

@@ -13,7 +13,8 @@ Calls are asynchronous on the current stream of the plan's device (or ``stream``
 allocate nothing and can be captured in a graph (build the plan before the capture, and
 keep it and what the calls use for as long as the graph is replayed).  They do not tell
 torch's allocator what they use on which stream: where a call runs on another stream than
-a tensor's own, keep the plan, the tensors and the workspace until it is done.
+a tensor's own, keep the plan, the tensors and the workspace until it is done.  (The plan's
+own table stays for torch's streams; a plan drops the tensors that it keeps.)
 """
 from __future__ import annotations
 
@@ -24,6 +25,7 @@ import numpy as np
 
 from . import (RESULT_BYTES, ZERO_BF16, ZERO_FP16, ZERO_FP32, ZERO_MUON_ASPECT, ZERO_MUON_NONE,
                ZERO_MUON_RMS, ZERO_OK, _check, _lib, zero_newton_schulz)
+from .tensors import _Table
 
 _ENTRY = np.dtype([("src", np.uint64), ("dst", np.uint64), ("rows", np.int64), ("cols", np.int64),
                    ("src_ld", np.int64), ("dst_ld", np.int64), ("src_dtype", np.int32),
@@ -39,7 +41,7 @@ class zero_matrix_plan_t(ctypes.Structure):
                 ("precise", ctypes.c_int32)]
 
 
-class _Plan:
+class _Plan(_Table):
     """A list of matrices with its table on the host and on the device."""
 
     def _build(self, list_p, n: int, precise: bool, device, init, table) -> None:
@@ -68,6 +70,7 @@ class _Plan:
             self.table = torch.from_numpy(self._host).to(device)
             # complete before any stream's calls; the calls then need no events
             stream.synchronize()
+            self._streams = {stream.cuda_stream}
         self._args = (ctypes.byref(self.c), self._host.ctypes.data, self.table.data_ptr())
 
     def _buffer(self, t, dtypes, count: int, name: str) -> int:
@@ -94,6 +97,8 @@ class _Plan:
             if stream.device != self.device:
                 raise ValueError(f"a stream of {self.device} expected")
             raw = stream.cuda_stream
+        if raw not in self._streams:
+            self._keep_table(raw, stream)
         with torch.cuda.device(self.device):
             rc = fn(*args, raw)
         if rc != ZERO_OK:

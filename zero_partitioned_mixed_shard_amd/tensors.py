@@ -59,7 +59,27 @@ def _order(t):
     return tuple(st for st, _ in dims)
 
 
-class zero_tensor_plan:
+class _Table:
+    """What plans have in common: a table on the device that calls on any stream read."""
+
+    def _keep_table(self, raw: int, stream) -> None:
+        """On a call's first use of a stream: the table is the plan's own, so its memory
+        stays until that stream is done.  Only for torch's streams, which live for ever:
+        the record is used when the table is freed, and a stream of the caller's making
+        may have been destroyed by then (and its handle be another stream's)."""
+        import torch
+        if raw == 0:
+            stream = torch.cuda.default_stream(self.device)
+        elif stream is None or isinstance(stream, int):
+            stream = torch.cuda.current_stream(self.device)
+        # a handle that is not the current stream's, or a stream around a handle, whose
+        # id the handle is, is the caller's
+        if stream.cuda_stream == raw and (raw == 0 or stream.stream_id != raw):
+            self.table.record_stream(stream)
+            self._streams.add(raw)
+
+
+class zero_tensor_plan(_Table):
     """The plan and device table of a list of tensors.
 
     tensors   device tensors of one device, each torch.float32, float16 or
@@ -166,22 +186,6 @@ class zero_tensor_plan:
                 rc = fn(*self._args, *args, raw)
         if rc != ZERO_OK:
             _check(rc, fn.__name__)
-
-    def _keep_table(self, raw: int, stream) -> None:
-        """On a call's first use of a stream: the table is the plan's own, so its memory
-        stays until that stream is done.  Only for torch's streams, which live for ever:
-        the record is used when the table is freed, and a stream of the caller's making
-        may have been destroyed by then (and its handle be another stream's)."""
-        import torch
-        if raw == 0:
-            stream = torch.cuda.default_stream(self.device)
-        elif stream is None or isinstance(stream, int):
-            stream = torch.cuda.current_stream(self.device)
-        # a handle that is not the current stream's, or a stream around a handle, whose
-        # id the handle is, is the caller's
-        if stream.cuda_stream == raw and (raw == 0 or stream.stream_id != raw):
-            self.table.record_stream(stream)
-            self._streams.add(raw)
 
     def _buffer(self, t, nbytes: int, name: str) -> int:
         if t.device != self.device:
