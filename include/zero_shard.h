@@ -653,7 +653,7 @@ typedef struct zero_matrix_plan {
 
 /* Plan of a list (host array; n_matrices 0 is allowed).  No result may overlap another
  * result, nor a matrix other than its own in the same place; blocks of columns of one
- * buffer (the same distance of rows) do not overlap.
+ * buffer (the same distance of rows) do not overlap, nor single rows beside such a block.
  * Errors: ZERO_EINVAL for a NULL argument, a negative size, an unknown type, a NULL or
  * misaligned pointer, rows closer than their elements, results that overlap;
  * ZERO_ERANGE for sides beyond the limits, addresses that overflow, or a list that host

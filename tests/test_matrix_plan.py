@@ -288,3 +288,27 @@ def test_a_plans_table_stays_for_torchs_streams(monkeypatch):
             plan._call(lambda raw: ran.append(raw) or 0, (), s)
         assert ran == [0, 0x5000, 0x5000, 0x5100, 0x6000, 0x6000, 0x7000, 0, 0]
         assert seen == [0, 0x5000, 0x5100]
+
+
+def bytes_of(at, rows, cols, ld):
+    return {at + 4 * (r * ld + c) + b for r in range(rows) for c in range(cols) for b in range(4)}
+
+
+def test_single_rows_beside_blocks():
+    """A row's distance to the next is nothing that a list of one row has: it may lie between
+    the rows of a block of columns.  Against the bytes themselves."""
+    block = entry(src=MIB, dst=MIB, rows=4, cols=8, src_ld=24, dst_ld=24)
+    assert init([block, entry(src=MIB + 4 * 32, dst=MIB + 4 * 32, rows=1, cols=16)])[0] == OK
+    assert init([block, entry(src=MIB + 4 * 32, dst=MIB + 4 * 32, rows=1, cols=17)])[0] == EINVAL
+    own = bytes_of(MIB, 4, 8, 24)
+    for cols in (1, 3, 16, 17, 24, 40):
+        for at in range(-45, 90):
+            where = MIB + 4 * at
+            row = entry(src=where, dst=where, rows=1, cols=cols, src_ld=cols + at % 5, dst_ld=cols + at % 5)
+            free = own.isdisjoint(bytes_of(where, 1, cols, 0))
+            for order in ([block, row], [row, block]):
+                assert init(order)[0] == (OK if free else EINVAL), (cols, at)
+    # two single rows, of any distances
+    for at, free in ((7, False), (8, True), (-8, True), (-7, False), (0, False)):
+        other = entry(src=MIB + 4 * at, dst=MIB + 4 * at, rows=1, cols=8, src_ld=30, dst_ld=30)
+        assert (init([entry(src=MIB, dst=MIB, rows=1, cols=8), other])[0] == OK) == free, at

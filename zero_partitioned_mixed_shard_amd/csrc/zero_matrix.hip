@@ -1491,13 +1491,15 @@ struct Span {
     int64_t owner;
 };
 // Whether two spans share a byte.  Column blocks of one buffer (the same pitch)
-// interleave without sharing any.
+// interleave without sharing any; a span of one row has whatever pitch the other has.
 bool share(const Span& x, const Span& y) {
     if (x.end <= y.at || y.end <= x.at) return false;
-    if (x.pitch != y.pitch) return true;
+    const bool one_x = x.end - x.at == x.row, one_y = y.end - y.at == y.row;
+    if (x.pitch != y.pitch && !one_x && !one_y) return true;
+    const uintptr_t pitch = one_x ? y.pitch : x.pitch;
     const Span &lo = x.at <= y.at ? x : y, &hi = x.at <= y.at ? y : x;
-    const uintptr_t d = (hi.at - lo.at) % lo.pitch;
-    return d < lo.row || d + hi.row > lo.pitch;
+    const uintptr_t d = (hi.at - lo.at) % pitch;
+    return d < lo.row || d + hi.row > pitch;
 }
 
 int build_entries(const zero_matrix_entry* e, int64_t n, Build& b, bool precise, int64_t* numel) {
