@@ -204,3 +204,15 @@ def test_values_at_the_end_of_the_range(rows, cols, largest):
     assert error(g, True) <= limits("normal", rows, cols)[1]
     if min(rows, cols) > 64:
         assert error(g, False) <= limits("normal", rows, cols)[0]
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 7), (7, 1), (1, 1000), (3, 200), (16, 1025), (1025, 16), (17, 33),
+                                       (63, 65), (64, 64), (64, 40000), (40001, 5)])
+@pytest.mark.parametrize("kind", ["normal", "4", "one", "alike"])
+def test_small_sides_are_in_32_bits(rows, cols, kind):
+    """The polynomial of the Gram matrix is made in 64 bits, P (its 2-norm at most 3.4445^5) rounded to
+    fp32, and P U is a sum of up to 64 fp32 products: 2^-24 of |P| |U| each, of independent signs,
+    4 times that at most over all of a row."""
+    g = matrix(kind, rows, cols).float().cuda()
+    for precise in (False, True):
+        assert error(g, precise) <= 3.4445 ** 5 * 2.0 ** -22

@@ -172,3 +172,88 @@ def test_captured_step_clips():
                         (steps[1].master, steps[1].exp_avg, steps[1].param16)):
             assert torch.equal(x, y), k
     assert float((steps[1].exp_avg[matrices[1][0]:matrices[2][0]]).norm()) < 0.05
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("precise", [False, True])
+@pytest.mark.parametrize("nesterov,scaling,clip", [(True, "rms", 0.0), (False, "rms", 0.01), (True, "aspect", 0.01),
+                                                   (False, None, 0.0), (True, None, 1e9)])
+def test_step(dtype, precise, nesterov, scaling, clip):
+    matrices, p, m, g = flat(11, dtype)
+    inv = 2.0 ** -6
+    # the norm is of the whole gradient, of all owners: larger than these matrices'
+    sumsq = 9.0 * float((g.double() * inv).square().sum())
+    clip, inv = single(clip), single(inv)
+    coef = min(1.0, clip / (math.sqrt(sumsq) + 1e-6)) if clip > 0 else 1.0
+    assert (coef < 0.1) == (clip == single(0.01))
+    coef = single(coef)
+    hp = Z.zero_muon_hparams(lr=0.01, momentum=0.9, weight_decay=0.5, max_grad_norm=clip, nesterov=nesterov,
+                             scaling=scaling)
+    plan = Z.zero_muon_plan(matrices, precise=precise)
+    ws = torch.full((plan.workspace_bytes,), 0xFF, dtype=torch.uint8, device="cuda")
+    dp, dm, dg, p16 = p.cuda(), m.cuda(), g.cuda(), p.to(TYPES[dtype]).cuda()
+    Z.zero_muon_step(dp, dm, p16, dg, plan, hp, result(sumsq, 0, inv), ws)
+    wp, wm = reference(p, m, g, matrices, hp, inv, coef)
+    got, mom = dp.double().cpu(), dm.double().cpu()
+    assert bool(((mom - wm).abs() <= 4 * 2.0 ** -24 * (m.double().abs() + (g.double() * inv * coef).abs()) + 1e-45).all())
+    wrong = [reference(p, m, g, matrices, hp, inv, coef, **c)[0] for c in
+             (dict(decay=0.0), dict(nesterov=not nesterov), dict(factor=1.05), dict(factor=0.95))]
+    inside = torch.zeros(p.numel(), dtype=torch.bool)
+    for o, r, c in matrices:
+        s = slice(o, o + r * c)
+        inside[s] = True
+        size = float(p[s].double().norm())
+        alpha = {0: 1.0, 1: math.sqrt(max(1.0, r / c)), 2: 0.2 * math.sqrt(max(r, c))}[hp.scaling]
+        o64 = float((p[s].double() * (1 - hp.lr * hp.weight_decay) - wp[s]).norm()) / (hp.lr * alpha)
+        limit = step_limit(size, o64, (r, c), hp, precise)
+        assert float((got[s] - wp[s]).norm()) <= limit, (r, c)
+        # what a mistake would have given lies outside (a clipped gradient is little beside the
+        # momentum, and the two forms' updates nearer)
+        for w in wrong:
+            assert float((w[s] - wp[s]).norm()) > limit, (r, c)
+        assert torch.equal(p16.cpu()[s].view(torch.int16), dp.cpu()[s].to(TYPES[dtype]).view(torch.int16))
+    assert torch.equal(dp.cpu()[~inside], p[~inside]) and torch.equal(dm.cpu()[~inside], m[~inside])
+
+
+@pytest.mark.parametrize("precise", [False, True])
+def test_step_of_large_tiles(precise):
+    """256 wide tiles, one step at a time and two to a pass, with momentum, decay and the rms
+    factor; the products in 64 bits on the device."""
+    shapes = [(2100, 3300), (2300, 2200), (2048, 300)]
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    n = sum(r * c for r, c in shapes)
+    p = torch.randn(n, device="cuda", generator=gen) * 0.02
+    m, g = (torch.randn(n, device="cuda", generator=gen) * 1e-2 for _ in range(2))
+    g = g.bfloat16()
+    hp = Z.zero_muon_hparams(lr=0.01, momentum=0.9, weight_decay=0.5, max_grad_norm=0.5)
+    sumsq = float(g.double().square().sum())
+    coef = single(hp.max_grad_norm / (math.sqrt(sumsq) + 1e-6))
+    assert coef < 0.1
+    matrices, at = [], 0
+    for r, c in shapes:
+        matrices.append((at, r, c))
+        at += r * c
+    plan = Z.zero_muon_plan(matrices, precise=precise)
+    ws = torch.full((plan.workspace_bytes,), 0xFF, dtype=torch.uint8, device="cuda")
+    dp, dm, p16 = p.clone(), m.clone(), p.bfloat16()
+    Z.zero_muon_step(dp, dm, p16, g, plan, hp, result(sumsq), ws)
+    gg = g.double() * coef
+    wm = hp.momentum * m.double() + gg
+    u = gg + hp.momentum * wm
+    assert bool(((dm.double() - wm).abs() <= 4 * 2.0 ** -24 * (m.double().abs() + gg.abs()) + 1e-45).all())
+    for o, r, c in matrices:
+        s = slice(o, o + r * c)
+        x = u[s].view(r, c)
+        x = x / (torch.linalg.vector_norm(x) + EPS)
+        x = x if r <= c else x.t().contiguous()
+        for _ in range(5):
+            q = x.mm(x.t().contiguous())
+            x = A * x + (B * q + C * q.mm(q)).mm(x)
+        x = (x if r <= c else x.t()).reshape(-1)
+        step = hp.lr * 0.2 * math.sqrt(max(r, c))
+        want = p[s].double() * (1 - hp.lr * hp.weight_decay) - step * x
+        size, norm = float(p[s].double().norm()), float(x.norm())
+        limit = step_limit(size, norm, (r, c), hp, precise)
+        assert float((dp[s].double() - want).norm()) <= limit
+        assert hp.lr * hp.weight_decay * size > 2 * limit and 0.05 * step * norm > 2 * limit
+    assert torch.equal(p16, dp.bfloat16())
