@@ -312,3 +312,88 @@ def test_single_rows_beside_blocks():
     for at, free in ((7, False), (8, True), (-8, True), (-7, False), (0, False)):
         other = entry(src=MIB + 4 * at, dst=MIB + 4 * at, rows=1, cols=8, src_ld=30, dst_ld=30)
         assert (init([entry(src=MIB, dst=MIB, rows=1, cols=8), other])[0] == OK) == free, at
+
+
+def registers(operand):
+    """The vector registers that an operand names."""
+    m = re.fullmatch(r"v(\d+)|v\[(\d+):(\d+)\]", operand.strip())
+    if not m:
+        return set()
+    return {int(m[1])} if m[1] else set(range(int(m[2]), int(m[3]) + 1))
+
+
+def wait_states(text):
+    m = re.match(r"s_nop (\d+)", text)
+    return 1 + int(m[1]) if m else 1
+
+
+def written_too_late(lines):
+    """Products whose operands a vector instruction writes less than two wait states before, on
+    any way to them: [(vector instruction, product)]."""
+    code = [ln.split(";")[0].strip() for ln in lines]
+    code = [ln for ln in code if ln and (not ln.startswith(".") or ln.endswith(":"))]
+    labels = {ln[:-1]: k for k, ln in enumerate(code) if ln.endswith(":")}
+    jumps = {}
+    for k, ln in enumerate(code):
+        m = re.match(r"s_c?branch\w* (\S+)", ln)
+        if m and m[1] in labels:
+            jumps.setdefault(labels[m[1]], []).append(k)
+    bad = []
+
+    def back(k, states, reads, product):
+        """Looks at what is before code[k], `states` wait states before the product."""
+        while k > 0 and states < 2:
+            k -= 1
+            if code[k].endswith(":"):
+                for j in jumps.get(k, []):
+                    back(j, states + 1, reads, product)      # the jump itself is a wait state
+                continue
+            if re.match(r"s_(branch|endpgm|setpc)", code[k]):
+                return
+            if code[k].startswith("v_") and not code[k].startswith(("v_mfma", "v_cmp", "v_readfirstlane", "v_readlane")):
+                first = code[k].split(None, 1)[1].split(",")[0] if " " in code[k] else ""
+                if registers(first) & reads:
+                    bad.append((code[k], product))
+            states += wait_states(code[k])
+
+    for k, ln in enumerate(code):
+        m = re.match(r"v_mfma_\S+ (.*)", ln)
+        if m:
+            ops = re.findall(r"[av]\[\d+:\d+\]|[av]\d+", m[1])
+            back(k, 0, set().union(*(registers(o) for o in ops[1:3])), ln)
+    return bad
+
+
+def test_written_too_late_is_found():
+    mfma = "\tv_mfma_f32_16x16x32_f16 a[0:3], v[4:7], v[8:11], a[0:3]"
+    assert written_too_late(["\tv_mov_b32_e32 v5, v1", mfma])
+    assert written_too_late(["\tv_mov_b32_e32 v5, v1", "\ts_nop 0", mfma])
+    assert written_too_late(["\tv_lshlrev_b64 v[10:11], 1, v[2:3]", ".LBB0_1:", mfma])
+    assert not written_too_late(["\tv_mov_b32_e32 v5, v1", "\ts_nop 1", mfma])
+    assert not written_too_late(["\tv_mov_b32_e32 v5, v1", "\ts_add_u32 s0, s0, 1", "\ts_nop 0", mfma])
+    assert not written_too_late(["\tv_mov_b32_e32 v12, v5", mfma])
+    assert not written_too_late(["\tds_read_b128 v[4:7], v1", mfma])
+    loop = [".LBB0_1:", mfma, "\ts_nop 7", "\tv_mov_b32_e32 v9, v1", "\ts_cbranch_scc1 .LBB0_1"]
+    assert written_too_late(loop)
+    assert not written_too_late(loop[:4] + ["\ts_nop 1"] + loop[4:])
+
+
+def test_operands_are_written_in_time(tmp_path):
+    """What the compiler takes for some instruction reads its operands as a matrix instruction
+    does: two wait states have to lie between a vector instruction that writes one and the
+    product (what comes from LDS is waited for, since the instruction names it)."""
+    src = os.path.join(build.PKG, "csrc", "zero_matrix.hip")
+    out = str(tmp_path / "zero_matrix.s")
+    flags = [f for f in build.FLAGS if f != "-shared"]
+    subprocess.run([build.HIPCC, *flags, "-S", "--cuda-device-only", "-o", out, src], check=True, capture_output=True)
+    kernels, lines = 0, None
+    for line in open(out):
+        if re.match(r"_ZN\S+:", line):
+            lines = [] if "matrix_product_kernel" in line else None
+        elif lines is not None and line.startswith(".Lfunc_end"):
+            assert any("v_mfma_" in ln for ln in lines)
+            assert not written_too_late(lines)
+            kernels, lines = kernels + 1, None
+        elif lines is not None:
+            lines.append(line)
+    assert kernels == 28
