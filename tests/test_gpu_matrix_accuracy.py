@@ -222,3 +222,19 @@ def test_small_sides_are_in_32_bits(rows, cols, kind):
         limit = max(limit, (min(rows, cols) / 2 + 1) * 3.4445 ** 5 * 2.0 ** -24 / 0.68)
     for precise in (False, True):
         assert error(g, precise) <= limit
+
+
+@pytest.mark.parametrize("count,rows,cols", [(41, 1024, 1024), (43, 1024, 1024), (80, 600, 620), (17, 1000, 1024),
+                                             (19, 1000, 1024)])
+def test_lists_on_both_sides_of_the_tiles_rule(count, rows, cols):
+    gen = torch.Generator(device="cuda").manual_seed(count)
+    src = torch.randn(count, rows, cols, device="cuda", generator=gen).bfloat16()
+    for precise in (False, True):
+        out = torch.zeros(count, rows, cols, device="cuda")
+        plan = Z.zero_matrix_plan(list(src), out=list(out), precise=precise)
+        ws = torch.full((plan.workspace_bytes,), 0xFF, dtype=torch.uint8, device="cuda")
+        Z.zero_orthogonalize(plan, ws)
+        for k in (0, count // 2, count - 1):
+            want = orth64(src[k])
+            off = float((out[k].double() - want).norm())
+            assert off <= limits("normal", rows, cols)[precise] * float(want.norm()), (precise, k)

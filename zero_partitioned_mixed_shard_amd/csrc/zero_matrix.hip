@@ -1234,16 +1234,17 @@ small_apply_kernel(Step s, Source src, MuonBufs mb, MuonConsts mc) {
 // ------------------------------------------------------------ host ---------
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
-// Matrices with a shorter side of at most kTogether are `many` with so many tiles of 256 on and
-// below their diagonals.
-constexpr int64_t kTogether = 1024, kMany = 480, kManyPrecise = 240;
 // The tile of a matrix's products, by its shorter side.
 // 256 wide ones do up to 1.7 times the work of 128 wide ones in the same time, which need
-// more of LDS than of the matrix cores; these are more, and each shorter.  9 matrices of
-// 1024 x 1024 to 4096 (90 tiles of 256): 690 us with 128, 920 with 256; 24 of 1024 x 1024
-// (240) 1177 and 1226, 48 of them 2379 and 2261.  In 32 bits 1611, 1624; 2489, 2302; 5150, 4095.
+// more of LDS than of the matrix cores; these are more, and each shorter.  Shorter sides of up
+// to kTogether take 256 wide ones where the list has `many` of them, on and below the diagonals:
+// 36 of 1024 x 1024 (360) take 1645 us with 128 and 1754 with 256, 42 (420) 1866 and 1850, 48
+// (480) 2097 and 1934.  In 32 bits 12 (120) 1206 and 1344, 15 (150) 1491 and 1438, 18 (180) 1978
+// and 1759; 60 of 500 x 500 (180) 1037 and 1049, 120 (360) 2301 and 2101.  Where 256 pads more
+// than 128 does it never pays: 120 of 600 x 600 1766 and 2523, 100 of 800 x 800 3112 and 3759.
+constexpr int64_t kTogether = 1024, kMany = 420, kManyPrecise = 180;
 int tile_for(int64_t m, bool many) {
-    return 4 * up(m, 256) > 5 * up(m, 128) || (m <= kTogether && !many) ? 128 : 256;
+    return m > kTogether || (many && up(m, 256) == up(m, 128)) ? 256 : 128;
 }
 // Whether two steps go together: with Q = a + B, the second step's A is Q A Q and what
 // both do to X is Q' Q, 5 products of m x m (half computed) in the place of 2 and of one
