@@ -19,7 +19,6 @@
 namespace {
 
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
-typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 
 constexpr int kCols = 8;                   // columns of a lane
 constexpr int kSlab = 64 * kCols;          // columns of a wave

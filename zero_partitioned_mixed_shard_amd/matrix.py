@@ -194,7 +194,8 @@ def _rows(t) -> set:
 class zero_muon_plan(_Plan):
     """The plan of matrices of a flat shard: (offset, rows, cols) of each, as elements of
     the shard's buffers.  precise: zero_matrix_plan's, here by default False (an update
-    that is off by 1e-3 of itself moves a weight by 1e-3 of its step)."""
+    that is off by 1e-3 of itself, of low rank by a few times that, moves a weight by as
+    much of its step)."""
 
     def __init__(self, matrices: Sequence, precise: bool = False, device="cuda"):
         self.matrices = [(int(o), int(r), int(c)) for o, r, c in matrices]
