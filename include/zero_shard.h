@@ -602,13 +602,13 @@ int zero_tensor_accumulate_norm(const zero_tensor_plan* plan, const void* table,
  *   by 2e-4 to 1e-3 for a matrix of full rank, or with some percent of noise,
  *   by up to 0.1 / sqrt(shorter side) for one of exactly or almost low rank or of few
  *   distinct singular values (at 65 x 200 4e-3, at 1024 x 1024 1.5e-3; of one direction
- *   9e-3 and 1e-3), and by up to 2e-2 for one whose entries are all alike,
- * and with `precise`, where every factor has 22 bits, by 1e-6 to 1e-5, up to 5e-5 of low
- * rank and 1e-3 of rank 1 to 4.  (fp16 results can hold more than the first: ask for
- * `precise` there, as the Python plan does.)  With a shorter side of at most 64 all is in 32
- * bits or more: 1e-7 to 1e-6, up to 6e-5 of rank 1 and 2e-4 with all entries alike.  The
- * same call gives the same bits; in another list a matrix's sums may be cut elsewhere,
- * which changes the result within these errors. */
+ *   9e-3 and 1e-3), and by up to 3e-2 for one whose entries are all alike,
+ * and with `precise`, where every factor has 22 bits, by 1e-6 to 5e-6, up to 2e-5 of low
+ * rank, 2e-4 of rank 2 to 16, and 1e-3 of rank 1 or with all entries alike.  (fp16 results
+ * can hold more than the first: ask for `precise` there, as the Python plan does.)  With a
+ * shorter side of at most 64 all is in 32 bits or more: 1e-7 to 1e-6, up to 6e-5 of rank 1
+ * and 2e-4 with all entries alike.  The same call gives the same bits; in another list a
+ * matrix's sums may be cut elsewhere, which changes the result within these errors. */
 
 /* Coefficients.  They have to keep the singular values within 1.75: the largest value
  * of |a x + b x^3 + c x^5| for x in [0, 1], then in [0, that value], and so on for all

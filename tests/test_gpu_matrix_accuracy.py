@@ -8,8 +8,8 @@ error of e sqrt(r / m) of the result, and over the m - r others one that later s
 a each, of e / sqrt(m) or less: with e = 2^-11 / sqrt(3) (rms), |b| + 2 |c| = 8.8 and what two
 steps between make of it, 0.06 / sqrt(m) in all (one direction, whose roundings are fewest and
 weigh most: 0.08); two steps to a pass multiply planes once more, 0.1.  Entries that are all
-alike are all rounded alike: 2^-11 (|b| + 2 |c|) in a step and twice that with the next one's,
-2e-2 over five.  To 32 bits the same with 2^-21, and with X's own last bit, 2^-22 of the entries,
+alike are all rounded alike: 2^-11 (|b| + 2 |c|) in a step, 2.2e-2 over five, and in pairs of steps
+again once more of a's square, 3e-2.  To 32 bits the same with 2^-21, and with X's own last bit, 2^-22 of the entries,
 which 485 times in the m directions that a matrix of low rank does not have is 485 2^-22 / sqrt(3)
 of what is there, and the fp32 sums' 2^-24 sqrt(n / 32) with it.
 """
@@ -89,7 +89,7 @@ def limits(kind, rows, cols):
     if kind in ("normal", "noise"):
         return 2e-3, 1e-5
     if kind == "alike":
-        return 2e-2, 1e-3
+        return 3e-2 if m >= 2048 and 2 * n >= 3 * m else 2.2e-2, 1e-3
     if kind in ("one", "almost one"):
         return 0.08 / math.sqrt(m), 1e-3
     return (0.1 if m >= 2048 and 2 * n >= 3 * m else 0.06) / math.sqrt(m), 5e-5
@@ -238,3 +238,11 @@ def test_lists_on_both_sides_of_the_tiles_rule(count, rows, cols):
             want = orth64(src[k])
             off = float((out[k].double() - want).norm())
             assert off <= limits("normal", rows, cols)[precise] * float(want.norm()), (precise, k)
+
+
+@pytest.mark.parametrize("rows,cols,value", [(1926, 10327, 2.964), (3754, 6598, 7.826), (3282, 5389, 5.498)])
+def test_lower_parts_are_added_up_first(rows, cols, value):
+    """Equal entries: a tile's sums are rounded alike, and otherwise in a tile that is cut; what
+    differs is no multiple of the matrix, and later steps multiply it by a each.  With the large
+    products first there would be three times as many such roundings (5.8e-3)."""
+    assert error(torch.full((rows, cols), value, device="cuda"), True) <= 1e-3

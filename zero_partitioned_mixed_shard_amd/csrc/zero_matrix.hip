@@ -33,11 +33,13 @@
 // the identity, and the roundings off their diagonals count: up to 0.06 / sqrt(m) of exactly
 // or almost low rank or of two levels (3.6e-3 at 65 x 200, 1.4e-3 at 1024 x 1024), 0.08 of one
 // direction (8.5e-3 at 65 x 20000), 0.1 with two steps to a pass (1.6e-3 at 2048 x 4096).
-// Where all entries are alike so are their roundings: 7e-3, in pairs 1.6e-2.  Without lo a
+// Where all entries are alike so are their roundings: 8e-3, in pairs 2.1e-2.  Without lo a
 // matrix of almost rank 1 would be off by 0.12, in bf16 by 1.
-// With `precise` A, B and X have two parts and every product is hi hi + hi lo + lo hi, three
-// times the matrix work: 1e-6 to 1e-5, up to 5e-5 of low rank; of rank 1 to 4, whose result
-// is small beside what the other directions make of X's last bits, up to 7e-4 (8192 x 16384).
+// With `precise` A, B and X have two parts and every product is lo hi + hi lo + hi hi, three
+// times the matrix work: 1e-6 to 5e-6, up to 2e-5 of low rank; of rank 1 to 16, whose result
+// is small beside what the other directions make of X's last bits, more (16384 x 16384 of rank
+// 1 4e-4, of rank 4 1.4e-4, of rank 16 8e-5), and 4e-4 where all entries are alike (hi hi first
+// would be 6.7e-6 of full rank and not 2.7e-6, 9.5e-4 and not 4e-4, 5.8e-3 and not 4e-4).
 
 #include <math.h>
 #include <string.h>
@@ -854,15 +856,15 @@ matrix_product_kernel(Step s, Product c, MuonBufs mb, MuonConsts mc) {
         right_off[q] = kTri ? rows_lane_off((uint32_t)right_ld, lane)
                             : cols_lane_off<T, NW>((uint32_t)right_ld, lane, w, q);
     static_assert(NW * (512 / T) * 2 % 16 == 0, "the key's period");
-    // stages of the precise form: hi hi, hi lo, lo hi.  A part has a share of them, in
-    // fours.
+    // stages of the precise form: lo hi, hi lo, hi hi, the small ones first, so that they are
+    // not rounded to the bits of the large ones' sum.  A part has a share of them, in fours.
     const int per = depth / kBK, fours = (PRECISE ? 3 * per : per) / 4;
     const int first = (int)((int64_t)fours * part / parts) * 4;
     const int total = (int)((int64_t)fours * (part + 1) / parts) * 4 - first;
     const int64_t step_r = kTri ? kBK : (int64_t)kBK * right_ld;
     int seg = PRECISE ? first / per : 0;
     int left_in_seg = per - (first - seg * per);
-    const f16* next_l = left + (seg == 2 ? left_plane : 0) + (int64_t)(first - seg * per) * kBK;
+    const f16* next_l = left + (PRECISE && seg == 0 ? left_plane : 0) + (int64_t)(first - seg * per) * kBK;
     const f16* next_r = right + (seg == 1 ? right_plane : 0) + (int64_t)(first - seg * per) * step_r;
     constexpr int kSideLoads = kSide / 1024 / NW, kLoads = 2 * kSideLoads;   // of a wave
     auto load_piece = [&](char* lds, int q) {       // access q of the next stage
@@ -884,7 +886,7 @@ matrix_product_kernel(Step s, Product c, MuonBufs mb, MuonConsts mc) {
             const bool last = --left_in_seg == 0 && go;   // selected, not branched to
             left_in_seg = last ? per : left_in_seg;
             seg += last;
-            next_l = last ? left + (seg == 2 ? left_plane : 0) : next_l;
+            next_l = last ? left : next_l;
             next_r = last ? right + (seg == 1 ? right_plane : 0) : next_r;
         }
     };
