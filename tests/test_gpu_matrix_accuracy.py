@@ -169,7 +169,7 @@ def test_who_takes_two_parts():
                                             (1100, 70000, "normal"), (70, 4000000, "alike"), (4000000, 65, "normal")])
 def test_long_sums(rows, cols, kind):
     """A's diagonal is a sum of as many positive terms as there are columns: in chains of at
-    most 1024 fp32 sums, or 3 times as many, and these added up, its error does not grow with them."""
+    most 1024 fp32 sums, and these added up, its error does not grow with them."""
     gen = torch.Generator(device="cuda").manual_seed(7)
     g = torch.full((rows, cols), 0.37, device="cuda") if kind == "alike" else \
         torch.randn(rows, cols, device="cuda", generator=gen)

@@ -13,8 +13,8 @@ Calls are asynchronous on the current stream of the plan's device (or ``stream``
 allocate nothing and can be captured in a graph (build the plan before the capture, and
 keep it and what the calls use for as long as the graph is replayed).  They do not tell
 torch's allocator what they use on which stream: where a call runs on another stream than
-a tensor's own, keep the plan, the tensors and the workspace until it is done.  (The plan's
-own table stays for torch's streams; a plan drops the tensors that it keeps.)
+a tensor's own, keep the plan, the tensors and the workspace until it is done.  (Of
+a plan that goes before, its own table stays for torch's streams; its tensors need not.)
 """
 from __future__ import annotations
 

@@ -196,8 +196,8 @@ class ShardStep:
         one owner's range; muon: their hyper-parameters (by default lr and weight_decay as given
         here; a schedule of the learning rate sets hp.lr and muon_hp.lr).  The clip is of the
         whole gradient, so it is hp.max_grad_norm for all steps: muon's own may be left 0 or has
-        to be the same.  muon_precise: updates to 32 bits, at three times the
-        matrix work (zero_muon_plan's precise)."""
+        to be the same.  muon_precise: updates to 32 bits, at three times the matrix work
+        (zero_muon_plan's precise)."""
         self.begin, self.end = begin, end
         self.count = end - begin
         self.owners = [(a - begin, b - begin) for a, b in owners]
